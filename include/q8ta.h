@@ -72,6 +72,9 @@ typedef enum q8ta_status {
   Q8TA_ERR_HIP = 5          /* the HIP runtime reported an error */
 } q8ta_status;
 
+/* Element type of the floating-point tensors of the decode-step operators. */
+typedef enum q8ta_dtype { Q8TA_F32 = 0, Q8TA_F16 = 1, Q8TA_BF16 = 2 } q8ta_dtype;
+
 /* Message for the last non-OK status returned on the calling thread
  * (a static or thread-local string; never NULL). */
 const char* q8ta_last_error(void);
@@ -524,6 +527,52 @@ q8ta_status q8ta_conv2d_acc(const int8_t* x, int64_t N, int64_t IC,
                             int64_t dilation_h, int64_t dilation_w, int64_t groups,
                             int32_t* acc, int64_t H_out, int64_t W_out,
                             hipStream_t stream);
+
+/* ===========================================================================
+ * Decode-step operators: what a language model runs around its q8ta_linear
+ * projections.  Strides are in elements.  Index tensors live on the device and
+ * cannot be checked before the launch; what an index outside its range does is
+ * stated with each operator, and none reads or writes outside the tensors.
+ *
+ * The paged int8 cache that q8ta_rope_append fills and q8ta_tree_attention
+ * reads: codes int8 [pages, 2, kv_heads, page_size, dim] and scales fp32
+ * [pages, 2, kv_heads, page_size] (part 0 keys, part 1 values), element =
+ * code * scale.  Slot s of the cache is row s % page_size of page
+ * s / page_size.
+ */
+
+/* ---------------------------------------------------------------------------
+ * q8ta_rope_append: rotary positions, and the append of keys and values to
+ * the int8 cache.  For token t, with angle[p] = positions[t] * inv_freq[p] in
+ * 64 bits, the pair p of each query and key head's first rot elements,
+ *   (x[p], x[rot/2 + p])  or, interleaved,  (x[2p], x[2p + 1]) = (a, b),
+ * becomes factor * (a cos - b sin, b cos + a sin); elements past rot stay.
+ *   q_out = the turned queries, rounded once to the type;
+ *   cache row of slots[t]: keys turned, values as they are, each head's row
+ *   of dim elements with scale = amax / 127 (rounded to fp32) and codes
+ *   rint(x * 127 / amax) (all 0 for a row of zeros), formed in 64 bits.
+ * q: [tokens, heads, dim], k and v: [tokens, kv_heads, dim], of `dtype`, inner
+ * stride 1, any token and head strides (the slices of one fused projection);
+ * positions int32 [tokens]; slots int64 [tokens]; inv_freq fp64 [rot / 2];
+ * factor: on cos and sin (1, or the attention factor of a length-scaled
+ * layout), finite; interleaved: 0 or 1; q_out dense [tokens, heads, dim], may
+ * be q itself where that is dense.
+ * A slot outside [0, pages * page_size) stores nothing for its token (padding
+ * tokens: -1); slots that appear twice leave either token's row.  tokens == 0
+ * is a no-op.  Requirements: heads, kv_heads, dim, pages, page_size >= 1, dim
+ * <= 65536, heads + 2 * kv_heads <= 65535, rot even in [0, dim] (inv_freq may
+ * be NULL for 0), tokens < 2^31.  Any alignment; dim % 8 == 0 and rot % 8 == 0
+ * up to dim 512 with strides of whole groups of four elements and bases
+ * aligned to such groups take the vector kernel.
+ */
+q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                             const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                             q8ta_dtype dtype, int64_t tokens, int64_t heads, int64_t kv_heads,
+                             int64_t dim, const int32_t* positions, const int64_t* slots,
+                             const double* inv_freq, int64_t rot, double factor,
+                             int64_t interleaved, void* q_out, int8_t* cache, float* cache_scales,
+                             int64_t pages, int64_t page_size, hipStream_t stream);
 
 #ifdef __cplusplus
 }

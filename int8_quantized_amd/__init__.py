@@ -35,6 +35,7 @@ class Q8taError(RuntimeError):
         self.message = message
 
 
+_I = ctypes.c_int
 _I64 = ctypes.c_int64
 _DBL = ctypes.c_double
 _P = ctypes.c_void_p
@@ -97,6 +98,9 @@ SIGNATURES = {
     "q8ta_conv2d_acc": ([_P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64,
                          _I64, _I64, _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P],
                         ctypes.c_int),
+    "q8ta_rope_append": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I64, _I64,
+                          _I64, _P, _P, _P, _I64, _DBL, _I64, _P, _P, _P, _I64, _I64, _P],
+                         ctypes.c_int),
 }
 
 _lib = None
@@ -550,6 +554,67 @@ def q8ta_conv2d_acc(x, input_zero_point, weight, Kh, Kw, stride, padding, dilati
     return acc
 
 
+# ---------------------------------------------------------------------------
+# Decode-step operators
+
+_dtype_codes = None
+
+
+def _code(t, name, allowed=("fp32", "fp16", "bf16")):
+    """q8ta_dtype of a floating-point tensor."""
+    global _dtype_codes
+    if _dtype_codes is None:
+        torch = _torch()
+        _dtype_codes = {torch.float32: (0, "fp32"), torch.float16: (1, "fp16"),
+                        torch.bfloat16: (2, "bf16")}
+    c = _dtype_codes.get(t.dtype)
+    if c is None or c[1] not in allowed:
+        raise TypeError(f"{name} must be {' or '.join(allowed)} (got {t.dtype})")
+    return c[0]
+
+
+def _view(t, name, dim):
+    """Data pointer of a device tensor whose last of `dim` dimensions has stride 1."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have {dim} dimensions, the last of stride 1")
+    return t.data_ptr()
+
+
+def q8ta_rope_append(q, k, v, positions, slots, inv_freq, factor, interleaved, q_out, cache,
+                     cache_scales, stream=None):
+    """Rotary positions on q and k, and the append of k and v to the paged int8 cache.
+
+    q [T, heads, dim], k and v [T, kv_heads, dim] (fp32, fp16 or bf16, any token and head
+    strides), positions int32 [T], slots int64 [T] (negative: not stored), inv_freq fp64
+    [rot / 2]; q_out like q, dense; cache int8 [pages, 2, kv_heads, page, dim] and cache_scales
+    fp32 [pages, 2, kv_heads, page].  ``interleaved`` pairs neighbours, else the two halves of
+    the rotated part; ``factor`` multiplies cos and sin.  Returns q_out."""
+    torch = _torch()
+    if cache.dim() != 5 or cache.shape[1] != 2 or cache.shape[:4] != cache_scales.shape:
+        raise ValueError("cache [pages, 2, kv_heads, page, dim] and cache_scales [pages, 2, "
+                         "kv_heads, page] expected")
+    pages, _, hk, page, d = cache.shape
+    qp, kp, vp = _view(q, "q", 3), _view(k, "k", 3), _view(v, "v", 3)
+    T, hq = q.shape[0], q.shape[1]
+    if q.shape[2] != d or k.shape != (T, hk, d) or v.shape != (T, hk, d) or q_out.shape != q.shape:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, "
+                         f"v {tuple(v.shape)}, q_out {tuple(q_out.shape)}, cache {tuple(cache.shape)}")
+    if positions.shape != (T,) or slots.shape != (T,) or inv_freq.dim() != 1:
+        raise ValueError("positions [T], slots [T] and inv_freq [rot / 2] expected")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must have one dtype")
+    _check(lib().q8ta_rope_append(
+        qp, q.stride(0), q.stride(1), kp, k.stride(0), k.stride(1), vp, v.stride(0), v.stride(1),
+        _code(q, "q"), T, hq, hk, d, _dev(positions, torch.int32, "positions"),
+        _dev(slots, torch.int64, "slots"), _dev(inv_freq, torch.float64, "inv_freq"),
+        2 * inv_freq.shape[0], factor, int(interleaved), _dev(q_out, q.dtype, "q_out"),
+        _dev(cache, torch.int8, "cache"), _dev(cache_scales, torch.float32, "cache_scales"), pages,
+        page, _stream(stream)))
+    return q_out
+
+
 __all__ = [
     "Q8taError", "lib", "q8ta_last_error", "q8ta_quantize_per_tensor", "q8ta_dequantize_per_tensor",
     "q8ta_linear", "q8ta_linear_gemv", "q8ta_linear_dq", "q8ta_linear_acc", "q8ta_conv2d_transposed",
@@ -561,4 +626,5 @@ __all__ = [
     "q8ta_conv2d_acc", "q8ta_conv2d_transposed_weight_prepacked_bytes",
     "q8ta_conv2d_transposed_weight_prepack", "q8ta_conv2d_transposed_prepacked",
     "q8ta_quantize_conv2d_transposed_prepacked",
+    "q8ta_rope_append",
 ]

@@ -18,6 +18,8 @@
 
 #include "q8ta_internal.h"
 
+#include "decode.h"
+
 namespace q8ta {
 // Kernel-family choice forced through q8ta_select_kernel (0 = default).
 extern std::atomic<char> g_sel_linear, g_sel_deconv, g_sel_conv;
@@ -198,6 +200,14 @@ q8ta_status linear_impl(const char* op, bool gemv_only, const int8_t* x, int64_t
 }  // namespace
 
 namespace q8ta {
+
+q8ta_status report(q8ta_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return st;
+}
 
 namespace {
 

@@ -1,0 +1,83 @@
+// C entry points of the decode-step operators: argument checks, then the
+// launch.  Every check runs before any HIP call.
+#include <cmath>
+
+#include "decode.h"
+
+using namespace q8ta;
+
+namespace {
+
+constexpr int64_t kMaxElems = (int64_t)1 << 40;
+
+q8ta_status hip_status(hipError_t e, const char* what) {
+  if (e == hipSuccess) return Q8TA_OK;
+  return report(Q8TA_ERR_HIP, "%s: HIP error %d (%s)", what, (int)e, hipGetErrorString(e));
+}
+
+bool dtype_ok(int d) { return d == Q8TA_F32 || d == Q8TA_F16 || d == Q8TA_BF16; }
+
+// a * b * .. <= 2^40 for factors >= 1.
+bool fits(std::initializer_list<int64_t> f) {
+  int64_t left = kMaxElems;
+  for (int64_t x : f) {
+    if (x > left) return false;
+    left /= x;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                             const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                             q8ta_dtype dtype, int64_t tokens, int64_t heads, int64_t kv_heads,
+                             int64_t dim, const int32_t* positions, const int64_t* slots,
+                             const double* inv_freq, int64_t rot, double factor,
+                             int64_t interleaved, void* q_out, int8_t* cache, float* cache_scales,
+                             int64_t pages, int64_t page_size, hipStream_t stream) {
+  const char* op = "q8ta_rope_append";
+  if (!dtype_ok(dtype)) return report(Q8TA_ERR_UNSUPPORTED, "%s: unknown dtype %d", op, (int)dtype);
+  if (tokens < 0 || tokens >= ((int64_t)1 << 31))
+    return report(Q8TA_ERR_SHAPE, "%s: tokens out of range (%lld)", op, (long long)tokens);
+  if (heads < 1 || kv_heads < 1 || heads > 65535 || kv_heads > 65535 || heads + 2 * kv_heads > 65535)
+    return report(Q8TA_ERR_SHAPE, "%s: heads and kv_heads must be >= 1 and heads + 2 * kv_heads <= "
+                  "65535 (got %lld, %lld)", op, (long long)heads, (long long)kv_heads);
+  if (dim < 1 || dim > 65536)
+    return report(Q8TA_ERR_SHAPE, "%s: dim must be in [1, 65536] (got %lld)", op, (long long)dim);
+  if (rot < 0 || rot > dim || rot % 2 != 0)
+    return report(Q8TA_ERR_SHAPE, "%s: rot must be even and in [0, dim] (got %lld of %lld)", op,
+                  (long long)rot, (long long)dim);
+  if (pages < 1 || page_size < 1 || !fits({pages, page_size, kv_heads, dim, 2}))
+    return report(Q8TA_ERR_SHAPE, "%s: pages and page_size must be >= 1 and the cache at most 2^40 "
+                  "elements (got %lld, %lld)", op, (long long)pages, (long long)page_size);
+  if (tokens > 0 && !fits({tokens, heads, dim}))
+    return report(Q8TA_ERR_SHAPE, "%s: sizes too large", op);
+  for (int64_t st : {q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
+                     v_head_stride})
+    if (st < 0 || st > kMaxElems)
+      return report(Q8TA_ERR_SHAPE, "%s: strides must be in [0, 2^40] (got %lld)", op, (long long)st);
+  if (!std::isfinite(factor))
+    return report(Q8TA_ERR_QPARAM, "%s: factor must be finite (got %g)", op, factor);
+  if (interleaved != 0 && interleaved != 1)
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: interleaved must be 0 or 1 (got %lld)", op,
+                  (long long)interleaved);
+  if (tokens == 0) return Q8TA_OK;
+  if (!q || !k || !v || !positions || !slots || !q_out || !cache || !cache_scales ||
+      (rot > 0 && !inv_freq))
+    return report(Q8TA_ERR_NULL, "%s: a required pointer is NULL", op);
+  RopeArgs a{};
+  a.q = q; a.k = k; a.v = v;
+  a.q_ts = q_token_stride; a.q_hs = q_head_stride; a.k_ts = k_token_stride;
+  a.k_hs = k_head_stride; a.v_ts = v_token_stride; a.v_hs = v_head_stride;
+  a.dtype = dtype; a.tokens = tokens; a.heads = (int)heads; a.kv_heads = (int)kv_heads;
+  a.dim = (int)dim; a.rot = (int)rot; a.positions = positions; a.slots = slots;
+  a.inv_freq = inv_freq; a.factor = factor; a.interleaved = interleaved != 0; a.q_out = q_out;
+  a.cache = cache; a.scales = cache_scales; a.pages = pages; a.page = page_size;
+  return hip_status(launch_rope_append(a, stream), op);
+}
+
+}  // extern "C"

@@ -1,0 +1,83 @@
+// Arguments and launchers of the decode-step operators: rotary positions with
+// the int8 cache append, tree attention over that cache, the linear with
+// low-rank adapters, and token sampling.
+#pragma once
+
+#include "../../include/q8ta.h"
+
+#include "q8ta_internal.h"
+
+namespace q8ta {
+
+// Records the message of a failed call (q8ta_last_error) and returns st.
+q8ta_status report(q8ta_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+
+// Unsigned division of n < 2^31 by a fixed d in [1, 2^31): with
+// l = ceil(log2 d) and m = floor(2^(31+l) / d) + 1 (< 2^32), n * m / 2^(31+l)
+// exceeds n / d by n * (m * d - 2^(31+l)) / (d * 2^(31+l)), where
+// 0 < m * d - 2^(31+l) <= d <= 2^l: by at most n / (d * 2^31) < 1 / d, so the
+// floor is the quotient's.
+struct FastDiv {
+  uint32_t mul = 0, d = 1;
+  int shift = 31;
+};
+inline FastDiv make_fastdiv(uint32_t d) {
+  int l = 0;
+  while (((uint64_t)1 << l) < d) ++l;
+  FastDiv f;
+  f.d = d;
+  f.shift = 31 + l;
+  f.mul = (uint32_t)((((uint64_t)1 << (31 + l)) / d) + 1);
+  return f;
+}
+__host__ __device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
+  return (uint32_t)(((uint64_t)n * f.mul) >> f.shift);
+}
+
+// 16-bit floating-point values by their bits.
+struct Half {
+  uint16_t bits;
+};
+struct Bfloat {
+  uint16_t bits;
+};
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(Half x) { return (float)__builtin_bit_cast(_Float16, x.bits); }
+__device__ __forceinline__ float to_float(Bfloat x) {
+  return __builtin_bit_cast(float, (uint32_t)x.bits << 16);
+}
+// One rounding to nearest even; NaN stays NaN.
+template <class T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ Half from_float<Half>(float x) {
+  return Half{__builtin_bit_cast(uint16_t, (_Float16)x)};
+}
+template <>
+__device__ __forceinline__ Bfloat from_float<Bfloat>(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1)) >> 16;
+  return Bfloat{(uint16_t)(x != x ? (u >> 16) | 0x40 : r)};
+}
+
+struct RopeArgs {
+  const void *q, *k, *v;                         // [tokens, heads, dim] views, unit inner stride
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;   // token and head strides in elements
+  int dtype;
+  int64_t tokens;
+  int heads, kv_heads, dim, rot;
+  const int32_t* positions;
+  const int64_t* slots;
+  const double* inv_freq;
+  double factor;
+  bool interleaved;
+  void* q_out;
+  int8_t* cache;
+  float* scales;
+  int64_t pages, page;
+};
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t s);
+
+}  // namespace q8ta
