@@ -574,6 +574,44 @@ q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_he
                              int64_t interleaved, void* q_out, int8_t* cache, float* cache_scales,
                              int64_t pages, int64_t page_size, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * q8ta_tree_attention: attention of each request's newest tokens over the
+ * paged int8 cache: one token a request, or a tree of drafted tokens that is
+ * verified at once.  Request b's keys are the cache rows 0 .. lens[b] +
+ * counts[b] - 1 of its pages (row s in page table[b, s / page_size]): lens[b]
+ * rows of context, then its drafted tokens, already appended.  Token i < counts[b]
+ * sees the whole context and drafted token j < counts[b] if bit j of mask[b, i] is
+ * set (its ancestors and itself).  For head h, with the cache's head h / (heads
+ * / kv_heads):
+ *   s_j = softmax_scale * sum_d q[b, i, h, d] * key_j[d]        over the seen j
+ *   out[b, i, h] = sum_j softmax(s)_j * value_j,   lse[b, i, h] = log sum_j exp s_j
+ * A row that sees no key, and a token i >= counts[b], gets out 0 and lse -inf.
+ * q: [batch, tokens, heads, dim] of `dtype` (fp16 or bf16), inner stride 1, any
+ * other strides; table int32 [batch, table_pages]; lens int32 [batch]; counts
+ * int32 [batch] or NULL (tokens each); mask int64 [batch, tokens] or NULL (a
+ * chain: token i sees drafted tokens 0 .. i); out: dense, of `dtype`; lse: fp32
+ * [batch, tokens, heads] or NULL.
+ * Scores, the softmax's maximum and sum and the output's sums are held in 32
+ * bits; probabilities are rounded to fp16 for the product with the values.
+ * Cache rows outside a row's keys may hold anything.  lens and counts are taken
+ * into [0, table_pages * page_size] and [0, tokens], keys past the table's pages
+ * are not there, and a page number outside [0, pages) makes its keys unseen.
+ * Requirements: batch, tokens, heads, kv_heads, dim, pages, page_size and
+ * table_pages >= 1, tokens <= 64, heads a multiple of kv_heads, batch <= 65535,
+ * table_pages * page_size < 2^31 - 64, softmax_scale finite and > 0
+ * (Q8TA_ERR_QPARAM); dim a multiple of 16 up to 256, page_size a multiple of
+ * 16 and 16-byte aligned cache and cache_scales (else Q8TA_ERR_UNSUPPORTED).
+ * batch == 0 is a no-op.  Workspace where the keys are split over workgroups:
+ * 4 * (dim + 2) bytes for each split of each row.
+ */
+q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q_token_stride,
+                                int64_t q_head_stride, q8ta_dtype dtype, int64_t batch,
+                                int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                                const int8_t* cache, const float* cache_scales, int64_t pages,
+                                int64_t page_size, const int32_t* table, int64_t table_pages,
+                                const int32_t* lens, const int32_t* counts, const int64_t* mask,
+                                double softmax_scale, void* out, float* lse, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

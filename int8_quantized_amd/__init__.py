@@ -101,6 +101,8 @@ SIGNATURES = {
     "q8ta_rope_append": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I64, _I64,
                           _I64, _P, _P, _P, _I64, _DBL, _I64, _P, _P, _P, _I64, _I64, _P],
                          ctypes.c_int),
+    "q8ta_tree_attention": ([_P, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64,
+                             _I64, _P, _I64, _P, _P, _P, _DBL, _P, _P, _P], ctypes.c_int),
 }
 
 _lib = None
@@ -615,6 +617,39 @@ def q8ta_rope_append(q, k, v, positions, slots, inv_freq, factor, interleaved, q
     return q_out
 
 
+def q8ta_tree_attention(q, cache, cache_scales, table, lens, counts, mask, softmax_scale, out,
+                        lse=None, stream=None):
+    """Attention of each request's newest tokens (one, or a tree of drafted ones) over the paged
+    int8 cache.
+
+    q [B, T, heads, dim] (fp16 or bf16, any outer strides, T <= 64); cache and cache_scales as
+    q8ta_rope_append fills them; table int32 [B, pages of a request]; lens int32 [B]: context rows
+    before the T tokens' own; counts int32 [B] or None: tokens in use; mask int64 [B, T] or None:
+    bit j of mask[b, i] lets token i see token j (None: a chain); out like q, dense; lse fp32
+    [B, T, heads] or None.  Returns out."""
+    torch = _torch()
+    if cache.dim() != 5 or cache.shape[1] != 2 or cache.shape[:4] != cache_scales.shape:
+        raise ValueError("cache [pages, 2, kv_heads, page, dim] and cache_scales [pages, 2, "
+                         "kv_heads, page] expected")
+    pages, _, hk, page, d = cache.shape
+    qp = _view(q, "q", 4)
+    B, T, hq, _ = q.shape
+    if q.shape[3] != d or out.shape != q.shape or (lse is not None and lse.shape != (B, T, hq)):
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, cache {tuple(cache.shape)}, out "
+                         f"{tuple(out.shape)}, lse {None if lse is None else tuple(lse.shape)}")
+    if (table.dim() != 2 or table.shape[0] != B or lens.shape != (B,) or
+            (counts is not None and counts.shape != (B,)) or
+            (mask is not None and mask.shape != (B, T))):
+        raise ValueError("table [B, pages], lens [B], counts [B] and mask [B, T] expected")
+    _check(lib().q8ta_tree_attention(
+        qp, q.stride(0), q.stride(1), q.stride(2), _code(q, "q", ("fp16", "bf16")), B, T, hq, hk, d,
+        _dev(cache, torch.int8, "cache"), _dev(cache_scales, torch.float32, "cache_scales"), pages,
+        page, _dev(table, torch.int32, "table"), table.shape[1], _dev(lens, torch.int32, "lens"),
+        _opt(counts, torch.int32, "counts"), _opt(mask, torch.int64, "mask"), softmax_scale,
+        _dev(out, q.dtype, "out"), _opt(lse, torch.float32, "lse"), _stream(stream)))
+    return out
+
+
 __all__ = [
     "Q8taError", "lib", "q8ta_last_error", "q8ta_quantize_per_tensor", "q8ta_dequantize_per_tensor",
     "q8ta_linear", "q8ta_linear_gemv", "q8ta_linear_dq", "q8ta_linear_acc", "q8ta_conv2d_transposed",
@@ -626,5 +661,5 @@ __all__ = [
     "q8ta_conv2d_acc", "q8ta_conv2d_transposed_weight_prepacked_bytes",
     "q8ta_conv2d_transposed_weight_prepack", "q8ta_conv2d_transposed_prepacked",
     "q8ta_quantize_conv2d_transposed_prepacked",
-    "q8ta_rope_append",
+    "q8ta_rope_append", "q8ta_tree_attention",
 ]

@@ -80,4 +80,60 @@ q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_he
   return hip_status(launch_rope_append(a, stream), op);
 }
 
+q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q_token_stride,
+                                int64_t q_head_stride, q8ta_dtype dtype, int64_t batch,
+                                int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                                const int8_t* cache, const float* cache_scales, int64_t pages,
+                                int64_t page_size, const int32_t* table, int64_t table_pages,
+                                const int32_t* lens, const int32_t* counts, const int64_t* mask,
+                                double softmax_scale, void* out, float* lse, hipStream_t stream) {
+  const char* op = "q8ta_tree_attention";
+  if (dtype != Q8TA_F16 && dtype != Q8TA_BF16)
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: dtype must be fp16 or bf16 (got %d)", op, (int)dtype);
+  if (batch < 0 || batch > 65535)
+    return report(Q8TA_ERR_SHAPE, "%s: batch must be in [0, 65535] (got %lld)", op, (long long)batch);
+  if (tokens < 1 || tokens > 64)
+    return report(Q8TA_ERR_SHAPE, "%s: tokens must be in [1, 64] (got %lld)", op, (long long)tokens);
+  if (heads < 1 || kv_heads < 1 || heads > 65535 || heads % kv_heads != 0)
+    return report(Q8TA_ERR_SHAPE, "%s: heads must be a multiple of kv_heads and at most 65535 (got "
+                  "%lld, %lld)", op, (long long)heads, (long long)kv_heads);
+  // rows of a key head in tiles of 16, times the key heads: the grid's second size
+  if (kv_heads * ((tokens * (heads / kv_heads) + 15) / 16) > 65535)
+    return report(Q8TA_ERR_SHAPE, "%s: too many heads (%lld) for %lld tokens", op, (long long)heads,
+                  (long long)tokens);
+  if (dim < 1) return report(Q8TA_ERR_SHAPE, "%s: dim must be >= 1 (got %lld)", op, (long long)dim);
+  if (dim % 16 != 0 || dim > 256)
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: dim must be a multiple of 16 up to 256 (got %lld)", op,
+                  (long long)dim);
+  if (pages < 1 || page_size < 1 || table_pages < 1 || page_size >= ((int64_t)1 << 31) ||
+      !fits({pages, page_size, kv_heads, dim, 2}))
+    return report(Q8TA_ERR_SHAPE, "%s: pages, page_size and table_pages must be >= 1 and the cache at "
+                  "most 2^40 elements (got %lld, %lld, %lld)", op, (long long)pages,
+                  (long long)page_size, (long long)table_pages);
+  if (table_pages > (((int64_t)1 << 31) - 65) / page_size)
+    return report(Q8TA_ERR_SHAPE, "%s: table_pages * page_size must be below 2^31 - 64", op);
+  if (page_size % 16 != 0)
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: page_size must be a multiple of 16 (got %lld)", op,
+                  (long long)page_size);
+  for (int64_t st : {q_batch_stride, q_token_stride, q_head_stride})
+    if (st < 0 || st > kMaxElems)
+      return report(Q8TA_ERR_SHAPE, "%s: strides must be in [0, 2^40] (got %lld)", op, (long long)st);
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0) || !std::isfinite((float)softmax_scale) ||
+      (float)softmax_scale == 0.0f)
+    return report(Q8TA_ERR_QPARAM, "%s: softmax_scale must be finite and > 0 (got %g)", op, softmax_scale);
+  if (batch == 0) return Q8TA_OK;
+  if (!q || !cache || !cache_scales || !table || !lens || !out)
+    return report(Q8TA_ERR_NULL, "%s: a required pointer is NULL", op);
+  if (((uintptr_t)cache | (uintptr_t)cache_scales) & 15)
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: cache and cache_scales must be 16-byte aligned", op);
+  AttnArgs a{};
+  a.q = q; a.q_bs = q_batch_stride; a.q_ts = q_token_stride; a.q_hs = q_head_stride;
+  a.dtype = dtype; a.batch = (int)batch; a.tokens = (int)tokens; a.heads = (int)heads;
+  a.kv_heads = (int)kv_heads; a.dim = (int)dim; a.cache = cache; a.scales = cache_scales;
+  a.pages = pages; a.page = (int)page_size; a.table = table; a.table_pages = (int)table_pages;
+  a.lens = lens; a.counts = counts; a.mask = mask; a.scale = (float)softmax_scale; a.out = out;
+  a.lse = lse;
+  return hip_status(launch_tree_attention(a, stream), op);
+}
+
 }  // extern "C"

@@ -80,4 +80,32 @@ struct RopeArgs {
 };
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t s);
 
+struct AttnArgs {
+  const void* q;            // [batch, tokens, heads, dim] view, unit inner stride
+  int64_t q_bs, q_ts, q_hs;
+  int dtype;
+  int batch, tokens, heads, kv_heads, group, dim;   // group = heads / kv_heads
+  const int8_t* cache;      // [pages, 2, kv_heads, page, dim]
+  const float* scales;      // [pages, 2, kv_heads, page]
+  int64_t pages;
+  int page;
+  FastDiv page_div, group_div;
+  const int32_t* table;     // [batch, table_pages]
+  int table_pages;
+  const int32_t* lens;      // [batch]
+  const int32_t* counts;    // [batch] or NULL
+  const int64_t* mask;      // [batch, tokens] or NULL
+  float scale;              // softmax scale
+  void* out;                // [batch, tokens, heads, dim]
+  float* lse;               // [batch, tokens, heads] or NULL
+  // Split over the keys: workgroup `split` of a request takes keys
+  // [split * chunk, (split + 1) * chunk); with more than one split, partial
+  // sums go to part_o [splits, rows, dim] and part_ml [splits, rows] (running
+  // maximum in powers of two, sum), rows = batch * tokens * heads.
+  int chunk, splits;
+  float* part_o;
+  float2* part_ml;
+};
+hipError_t launch_tree_attention(AttnArgs a, hipStream_t s);
+
 }  // namespace q8ta
