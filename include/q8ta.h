@@ -612,6 +612,33 @@ q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
                                 const int32_t* lens, const int32_t* counts, const int64_t* mask,
                                 double softmax_scale, void* out, float* lse, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * q8ta_sample: one token a row from its logits and a given random number.
+ * With T, k, p, mp the row's temperature, top_k, top_p and min_p, and its
+ * tokens in the order of falling logits (equal ones by index):
+ *   w_j = exp((logit_j - logit_0) / T) for the first k tokens (all if k <= 0);
+ *   of these, in order, the ones with  sum of the w before them < p * sum of all w;
+ *   of these, the ones with w_j >= mp; the first token stays in any case.
+ *   token = the first index i, in the vocabulary's order, with
+ *           sum of the kept w up to and including i > u * sum of the kept w
+ *   logprob = log(w_token / sum of the kept w)
+ * T <= 0 (or NaN) is greedy: the first token, logprob 0.  top_p >= 1 and min_p
+ * <= 0 keep everything; NULL top_k, top_p or min_p is off for every row.
+ * Weights are formed in 64 bits and added as whole numbers of 2^-shift (shift
+ * = 62 - ceil(log2 vocab)), so that the sums, and the token, do not depend on an
+ * order.  -inf logits are never taken (NaN counts as -inf); +inf logits share the
+ * weight alone; a row with nothing but -inf gets token -1 and logprob -inf.
+ * u: in [0, 1); at 1 and beyond the last kept token is taken.
+ * logits: [rows, vocab] of `dtype`, rows row_stride elements apart;
+ * temperature, top_p, min_p, u fp32 [rows]; top_k int32 [rows]; tokens int32 [rows];
+ * logprobs fp32 [rows] or NULL.  Requirements: rows >= 0 (0 is a no-op), 1 <=
+ * vocab <= 2^24, row_stride >= vocab (any for one row).
+ */
+q8ta_status q8ta_sample(const void* logits, int64_t row_stride, q8ta_dtype dtype, int64_t rows,
+                        int64_t vocab, const float* temperature, const int32_t* top_k,
+                        const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+                        float* logprobs, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

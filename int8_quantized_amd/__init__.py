@@ -103,6 +103,7 @@ SIGNATURES = {
                          ctypes.c_int),
     "q8ta_tree_attention": ([_P, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64,
                              _I64, _P, _I64, _P, _P, _P, _DBL, _P, _P, _P], ctypes.c_int),
+    "q8ta_sample": ([_P, _I64, _I, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
 }
 
 _lib = None
@@ -650,6 +651,29 @@ def q8ta_tree_attention(q, cache, cache_scales, table, lens, counts, mask, softm
     return out
 
 
+def q8ta_sample(logits, temperature, top_k, top_p, min_p, u, tokens, logprobs=None, stream=None):
+    """One token a row by temperature, top-k, top-p and min-p from given random numbers.
+
+    logits [B, V] (fp32, fp16 or bf16, rows may be strided); temperature, top_p, min_p and u fp32
+    [B], top_k int32 [B] (top_k, top_p and min_p may be None); tokens int32 [B]; logprobs fp32 [B]
+    or None: the token's log-probability among those kept.  Temperature 0 is greedy.  Returns
+    tokens."""
+    torch = _torch()
+    lp = _view(logits, "logits", 2)
+    B, V = logits.shape
+    for name, t in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p),
+                    ("min_p", min_p), ("u", u), ("tokens", tokens), ("logprobs", logprobs)):
+        if t is not None and t.shape != (B,):
+            raise ValueError(f"{name} must be [{B}] (got {tuple(t.shape)})")
+    f32 = torch.float32
+    _check(lib().q8ta_sample(
+        lp, logits.stride(0), _code(logits, "logits"), B, V, _dev(temperature, f32, "temperature"),
+        _opt(top_k, torch.int32, "top_k"), _opt(top_p, f32, "top_p"), _opt(min_p, f32, "min_p"),
+        _dev(u, f32, "u"), _dev(tokens, torch.int32, "tokens"), _opt(logprobs, f32, "logprobs"),
+        _stream(stream)))
+    return tokens
+
+
 __all__ = [
     "Q8taError", "lib", "q8ta_last_error", "q8ta_quantize_per_tensor", "q8ta_dequantize_per_tensor",
     "q8ta_linear", "q8ta_linear_gemv", "q8ta_linear_dq", "q8ta_linear_acc", "q8ta_conv2d_transposed",
@@ -661,5 +685,5 @@ __all__ = [
     "q8ta_conv2d_acc", "q8ta_conv2d_transposed_weight_prepacked_bytes",
     "q8ta_conv2d_transposed_weight_prepack", "q8ta_conv2d_transposed_prepacked",
     "q8ta_quantize_conv2d_transposed_prepacked",
-    "q8ta_rope_append", "q8ta_tree_attention",
+    "q8ta_rope_append", "q8ta_tree_attention", "q8ta_sample",
 ]

@@ -136,4 +136,30 @@ q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
   return hip_status(launch_tree_attention(a, stream), op);
 }
 
+q8ta_status q8ta_sample(const void* logits, int64_t row_stride, q8ta_dtype dtype, int64_t rows,
+                        int64_t vocab, const float* temperature, const int32_t* top_k,
+                        const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+                        float* logprobs, hipStream_t stream) {
+  const char* op = "q8ta_sample";
+  if (!dtype_ok(dtype)) return report(Q8TA_ERR_UNSUPPORTED, "%s: unknown dtype %d", op, (int)dtype);
+  if (rows < 0 || rows >= ((int64_t)1 << 31))
+    return report(Q8TA_ERR_SHAPE, "%s: rows out of range (%lld)", op, (long long)rows);
+  if (vocab < 1 || vocab > ((int64_t)1 << 24))
+    return report(Q8TA_ERR_SHAPE, "%s: vocab must be in [1, 2^24] (got %lld)", op, (long long)vocab);
+  if (rows > 1 && (row_stride < vocab || row_stride > kMaxElems / rows))
+    return report(Q8TA_ERR_SHAPE, "%s: row_stride must be >= vocab and rows * row_stride <= 2^40 (got "
+                  "%lld)", op, (long long)row_stride);
+  if (rows == 0) return Q8TA_OK;
+  if (!logits || !temperature || !u || !tokens)
+    return report(Q8TA_ERR_NULL, "%s: logits, temperature, u and tokens must not be NULL", op);
+  SampleArgs a{};
+  a.logits = logits; a.row_stride = row_stride; a.dtype = dtype; a.rows = (int)rows;
+  a.vocab = (int)vocab; a.temperature = temperature; a.top_k = top_k; a.top_p = top_p;
+  a.min_p = min_p; a.u = u; a.tokens = tokens; a.logprobs = logprobs;
+  int bits = 0;
+  while (((int64_t)1 << bits) < vocab) ++bits;
+  a.shift = 62 - bits;
+  return hip_status(launch_sample(a, stream), op);
+}
+
 }  // extern "C"

@@ -108,4 +108,20 @@ struct AttnArgs {
 };
 hipError_t launch_tree_attention(AttnArgs a, hipStream_t s);
 
+struct SampleArgs {
+  const void* logits;       // [rows, vocab], row stride in elements
+  int64_t row_stride;
+  int dtype;
+  int rows, vocab;
+  int shift;                // a weight of 1 is 2^shift in whole numbers
+  const float* temperature;
+  const int32_t* top_k;     // NULL: off
+  const float* top_p;       // NULL: off
+  const float* min_p;       // NULL: off
+  const float* u;
+  int32_t* tokens;
+  float* logprobs;          // NULL: not wanted
+};
+hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
+
 }  // namespace q8ta
