@@ -542,6 +542,38 @@ q8ta_status q8ta_conv2d_acc(const int8_t* x, int64_t N, int64_t IC,
  */
 
 /* ---------------------------------------------------------------------------
+ * q8ta_linear_lora: the shared projection q8ta_linear computes, with the
+ * low-rank adapters of many requests at once, and a floating-point output:
+ *   acc[m, n] = sum_k (x[m, k] - input_zero_point) * weight[n, k]       (int32)
+ *   y = ((float)acc * (float)input_scale) * weight_scales[n] + bias[n]
+ *   with a = adapter_ids[m] in [0, adapters):
+ *     y += sum_r lora_b[a, n, r] * (adapter_scales[a] * (float)input_scale *
+ *                                   sum_k lora_a[a, r, k] * (x[m, k] - input_zero_point))
+ *   out[m, n] = y, or max(y, 0) for "relu", rounded once to out_dtype.
+ * A row whose id is outside [0, adapters) has no adapter (use -1).  The rows
+ * may come in any order; rows of one adapter next to each other share its
+ * reads.  The adapter's sums are held in 32 bits.
+ * x, weight, weight_scales, bias, activation as for q8ta_linear; lora_a
+ * [adapters, rank, K] and lora_b [adapters, N, rank], dense, of adapter_dtype
+ * (fp16 or bf16); adapter_scales: fp32 [adapters] or NULL (1 each); ranks: int32
+ * [adapters] or NULL: an adapter's own rank within `rank`, what lies past it is
+ * not read as numbers; adapter_ids: int32 [M]; out: dense [M, N] of
+ * out_dtype.  Requirements: as for q8ta_linear, M <= 2^21, N and K
+ * <= 2^30, 1 <= rank <= 512, 1 <= adapters <= 2^24.  Any K and alignment: where K is no multiple of 16 or x,
+ * weight or lora_a are not 16-byte aligned, they are first copied into rows
+ * that are (workspace: (M + N + 2 * adapters * rank) * K bytes, K rounded up to
+ * 64).  Workspace otherwise: 4 bytes for each row and rank (rounded up to
+ * 16).
+ */
+q8ta_status q8ta_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_scale,
+                             int64_t input_zero_point, const int8_t* weight, int64_t N,
+                             const float* weight_scales, const float* bias, const void* lora_a,
+                             const void* lora_b, q8ta_dtype adapter_dtype, int64_t adapters,
+                             int64_t rank, const float* adapter_scales, const int32_t* ranks,
+                             const int32_t* adapter_ids, const char* activation, void* out,
+                             q8ta_dtype out_dtype, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * q8ta_rope_append: rotary positions, and the append of keys and values to
  * the int8 cache.  For token t, with angle[p] = positions[t] * inv_freq[p] in
  * 64 bits, the pair p of each query and key head's first rot elements,

@@ -103,6 +103,8 @@ SIGNATURES = {
                          ctypes.c_int),
     "q8ta_tree_attention": ([_P, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64,
                              _I64, _P, _I64, _P, _P, _P, _DBL, _P, _P, _P], ctypes.c_int),
+    "q8ta_linear_lora": ([_P, _I64, _I64, _DBL, _I64, _P, _I64, _P, _P, _P, _P, _I, _I64, _I64, _P,
+                          _P, _P, _S, _P, _I, _P], ctypes.c_int),
     "q8ta_sample": ([_P, _I64, _I, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
 }
 
@@ -674,6 +676,42 @@ def q8ta_sample(logits, temperature, top_k, top_p, min_p, u, tokens, logprobs=No
     return tokens
 
 
+def q8ta_linear_lora(x, input_scale, input_zero_point, weight, weight_scales, bias, lora_a, lora_b,
+                     adapter_scales, ranks, adapter_ids, activation, out, stream=None):
+    """q8ta_linear's projection with the low-rank adapters of many requests, floating-point out.
+
+    x int8 [M, K], weight int8 [N, K]; lora_a [adapters, rank, K] and lora_b [adapters, N, rank]
+    (fp16 or bf16); adapter_scales fp32 [adapters] or None; ranks int32 [adapters] or None (each
+    adapter's own rank); adapter_ids int32 [M], negative for none; out [M, N] fp32, fp16 or bf16.
+    Returns out."""
+    torch = _torch()
+    if x.dim() != 2 or weight.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
+        raise ValueError("x [M, K], weight [N, K], lora_a [adapters, rank, K] and lora_b [adapters, N, "
+                         "rank] expected")
+    M, K = x.shape
+    N = weight.shape[0]
+    na, r = lora_a.shape[0], lora_a.shape[1]
+    if (weight.shape[1] != K or lora_a.shape[2] != K or lora_b.shape != (na, N, r) or
+            out.shape != (M, N) or adapter_ids.shape != (M,)):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, weight {tuple(weight.shape)}, lora_a "
+                         f"{tuple(lora_a.shape)}, lora_b {tuple(lora_b.shape)}, adapter_ids "
+                         f"{tuple(adapter_ids.shape)}, out {tuple(out.shape)}")
+    for name, t, n in (("weight_scales", weight_scales, N), ("bias", bias, N),
+                       ("adapter_scales", adapter_scales, na), ("ranks", ranks, na)):
+        if t is not None and t.numel() < n:
+            raise ValueError(f"{name} must have {n} entries (got {t.numel()})")
+    f32 = torch.float32
+    _check(lib().q8ta_linear_lora(
+        _dev(x, torch.int8, "x"), M, K, input_scale, input_zero_point,
+        _dev(weight, torch.int8, "weight"), N, _dev(weight_scales, f32, "weight_scales"),
+        _opt(bias, f32, "bias"), _dev(lora_a, lora_a.dtype, "lora_a"),
+        _dev(lora_b, lora_a.dtype, "lora_b"), _code(lora_a, "lora_a", ("fp16", "bf16")), na, r,
+        _opt(adapter_scales, f32, "adapter_scales"), _opt(ranks, torch.int32, "ranks"),
+        _dev(adapter_ids, torch.int32, "adapter_ids"), _act(activation),
+        _dev(out, out.dtype, "out"), _code(out, "out"), _stream(stream)))
+    return out
+
+
 __all__ = [
     "Q8taError", "lib", "q8ta_last_error", "q8ta_quantize_per_tensor", "q8ta_dequantize_per_tensor",
     "q8ta_linear", "q8ta_linear_gemv", "q8ta_linear_dq", "q8ta_linear_acc", "q8ta_conv2d_transposed",
@@ -685,5 +723,5 @@ __all__ = [
     "q8ta_conv2d_acc", "q8ta_conv2d_transposed_weight_prepacked_bytes",
     "q8ta_conv2d_transposed_weight_prepack", "q8ta_conv2d_transposed_prepacked",
     "q8ta_quantize_conv2d_transposed_prepacked",
-    "q8ta_rope_append", "q8ta_tree_attention", "q8ta_sample",
+    "q8ta_linear_lora", "q8ta_rope_append", "q8ta_tree_attention", "q8ta_sample",
 ]

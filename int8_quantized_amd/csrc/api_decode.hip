@@ -1,6 +1,7 @@
 // C entry points of the decode-step operators: argument checks, then the
 // launch.  Every check runs before any HIP call.
 #include <cmath>
+#include <cstring>
 
 #include "decode.h"
 
@@ -160,6 +161,50 @@ q8ta_status q8ta_sample(const void* logits, int64_t row_stride, q8ta_dtype dtype
   while (((int64_t)1 << bits) < vocab) ++bits;
   a.shift = 62 - bits;
   return hip_status(launch_sample(a, stream), op);
+}
+
+q8ta_status q8ta_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_scale,
+                             int64_t input_zero_point, const int8_t* weight, int64_t N,
+                             const float* weight_scales, const float* bias, const void* lora_a,
+                             const void* lora_b, q8ta_dtype adapter_dtype, int64_t adapters,
+                             int64_t rank, const float* adapter_scales, const int32_t* ranks,
+                             const int32_t* adapter_ids, const char* activation, void* out,
+                             q8ta_dtype out_dtype, hipStream_t stream) {
+  const char* op = "q8ta_linear_lora";
+  if (!x || !weight || !weight_scales || !lora_a || !lora_b || !adapter_ids || !out)
+    return report(Q8TA_ERR_NULL, "%s: a required pointer is NULL", op);
+  if (M < 1 || K < 1 || N < 1)
+    return report(Q8TA_ERR_SHAPE, "%s: M, K, N must be >= 1 (got %lld, %lld, %lld)", op, (long long)M,
+                  (long long)K, (long long)N);
+  if (rank < 1 || rank > 512 || adapters < 1 || adapters > ((int64_t)1 << 24))
+    return report(Q8TA_ERR_SHAPE, "%s: rank must be in [1, 512] and adapters in [1, 2^24] (got %lld, "
+                  "%lld)", op, (long long)rank, (long long)adapters);
+  const int64_t lim = (int64_t)1 << 30;
+  if (M > ((int64_t)1 << 21) || N > lim || K > lim || !fits({M, K}) || !fits({N, K}) || !fits({M, N}) ||
+      !fits({adapters, rank, K}) || !fits({adapters, rank, N}))
+    return report(Q8TA_ERR_SHAPE, "%s: sizes too large", op);
+  if (!std::isfinite(input_scale) || !(input_scale > 0.0))
+    return report(Q8TA_ERR_QPARAM, "%s: scale must be finite and > 0 (got %g)", op, input_scale);
+  if (input_zero_point < -128 || input_zero_point > 127)
+    return report(Q8TA_ERR_QPARAM, "%s: zero_point must be in [-128, 127] (got %lld)", op,
+                  (long long)input_zero_point);
+  if (adapter_dtype != Q8TA_F16 && adapter_dtype != Q8TA_BF16)
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: adapter dtype must be fp16 or bf16 (got %d)", op,
+                  (int)adapter_dtype);
+  if (!dtype_ok(out_dtype))
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: unknown output dtype %d", op, (int)out_dtype);
+  if (!activation || (strcmp(activation, "none") != 0 && strcmp(activation, "relu") != 0))
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: activation \"%.64s\" is not supported (\"none\" or "
+                  "\"relu\")", op, activation ? activation : "NULL");
+  LoraArgs a{};
+  a.lin.x = x; a.lin.w = weight; a.lin.wscale = weight_scales; a.lin.bias = bias;
+  a.lin.M = M; a.lin.K = K; a.lin.N = N; a.lin.izp = (int32_t)input_zero_point;
+  a.lin.rq.s_in = (float)input_scale;
+  a.a = lora_a; a.b = lora_b; a.ad_type = adapter_dtype; a.adapters = (int)adapters;
+  a.rank = (int)rank; a.rank_pad = (int)((rank + 15) / 16 * 16); a.ad_scales = adapter_scales;
+  a.ranks = ranks; a.ids = adapter_ids; a.relu = strcmp(activation, "relu") == 0; a.y = out;
+  a.y_type = out_dtype;
+  return hip_status(launch_linear_lora(a, stream), op);
 }
 
 }  // extern "C"

@@ -124,4 +124,35 @@ struct SampleArgs {
 };
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
 
+// The linear with low-rank adapters: lin holds x, w, the scales, bias, sizes
+// and the input zero point (lin.rq.s_in the input scale); row m adds
+// adapter_scale * B (A (x - zp) s_in) of adapter ids[m].
+struct LoraArgs {
+  LinearArgs lin;
+  const void *a, *b;        // [adapters, rank, K], [adapters, N, rank]
+  int ad_type;
+  int adapters, rank;
+  int rank_pad;             // rank rounded up to 16
+  const float* ad_scales;   // NULL: 1
+  const int32_t* ranks;     // NULL: rank each
+  const int32_t* ids;
+  bool relu;
+  void* y;
+  int y_type;
+  // t[m, r] = adapter_scale * s_in * sum_k A[r, k] (x[m, k] - zp) of the row's
+  // adapter (0 past its rank), [M, rank_pad]; rows without one are not written
+  float* t = nullptr;
+};
+// The adapter of row m, -1 for none (any id outside [0, adapters)).
+__device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t m) {
+  const int id = a.ids[m];
+  return id >= 0 && id < a.adapters ? id : -1;
+}
+__device__ __forceinline__ int rank_of(const LoraArgs& a, int id) {
+  if (!a.ranks) return a.rank;
+  const int r = a.ranks[id];
+  return r < 0 ? 0 : (r < a.rank ? r : a.rank);
+}
+hipError_t launch_linear_lora(LoraArgs a, hipStream_t s);
+
 }  // namespace q8ta
