@@ -143,9 +143,15 @@ def q8ta_select_kernel(op: str, kernel: str) -> None:
     _check(lib().q8ta_select_kernel(op.encode(), kernel.encode()))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev(t, dtype, name):
@@ -167,7 +173,9 @@ def _opt(t, dtype, name):
 
 def _stream(stream):
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building its Python object (2.8 us)
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -579,12 +587,25 @@ def _code(t, name, allowed=("fp32", "fp16", "bf16")):
 
 
 def _view(t, name, dim):
-    """Data pointer of a device tensor whose last of `dim` dimensions has stride 1."""
-    if t.device.type != "cuda":
+    """Data pointer, shape and strides of a device tensor whose last of `dim` dimensions has
+    stride 1."""
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
-    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != dim or (strides[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must have {dim} dimensions, the last of stride 1")
-    return t.data_ptr()
+    return t.data_ptr(), shape, strides
+
+
+def _ptr(t, dtype, name):
+    """_dev for the operators whose calls are short: the same checks, by their cheapest tests."""
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, dtype, name)
+
+
+def _opt_ptr(t, dtype, name):
+    return None if t is None else _ptr(t, dtype, name)
 
 
 def q8ta_rope_append(q, k, v, positions, slots, inv_freq, factor, interleaved, q_out, cache,
@@ -597,26 +618,30 @@ def q8ta_rope_append(q, k, v, positions, slots, inv_freq, factor, interleaved, q
     fp32 [pages, 2, kv_heads, page].  ``interleaved`` pairs neighbours, else the two halves of
     the rotated part; ``factor`` multiplies cos and sin.  Returns q_out."""
     torch = _torch()
-    if cache.dim() != 5 or cache.shape[1] != 2 or cache.shape[:4] != cache_scales.shape:
+    cs = cache.shape
+    if len(cs) != 5 or cs[1] != 2 or cs[:4] != cache_scales.shape:
         raise ValueError("cache [pages, 2, kv_heads, page, dim] and cache_scales [pages, 2, "
                          "kv_heads, page] expected")
-    pages, _, hk, page, d = cache.shape
-    qp, kp, vp = _view(q, "q", 3), _view(k, "k", 3), _view(v, "v", 3)
-    T, hq = q.shape[0], q.shape[1]
-    if q.shape[2] != d or k.shape != (T, hk, d) or v.shape != (T, hk, d) or q_out.shape != q.shape:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, "
-                         f"v {tuple(v.shape)}, q_out {tuple(q_out.shape)}, cache {tuple(cache.shape)}")
-    if positions.shape != (T,) or slots.shape != (T,) or inv_freq.dim() != 1:
+    pages, _, hk, page, d = cs
+    qp, qs, qt = _view(q, "q", 3)
+    kp, ks, kt = _view(k, "k", 3)
+    vp, vs, vt = _view(v, "v", 3)
+    T, hq, qd = qs
+    if qd != d or ks != (T, hk, d) or vs != ks or q_out.shape != qs:
+        raise ValueError(f"shape mismatch: q {tuple(qs)}, k {tuple(ks)}, v {tuple(vs)}, q_out "
+                         f"{tuple(q_out.shape)}, cache {tuple(cs)}")
+    pairs = inv_freq.shape
+    if positions.shape != (T,) or slots.shape != (T,) or len(pairs) != 1:
         raise ValueError("positions [T], slots [T] and inv_freq [rot / 2] expected")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    dtype = q.dtype
+    if k.dtype is not dtype or v.dtype is not dtype:
         raise TypeError("q, k and v must have one dtype")
     _check(lib().q8ta_rope_append(
-        qp, q.stride(0), q.stride(1), kp, k.stride(0), k.stride(1), vp, v.stride(0), v.stride(1),
-        _code(q, "q"), T, hq, hk, d, _dev(positions, torch.int32, "positions"),
-        _dev(slots, torch.int64, "slots"), _dev(inv_freq, torch.float64, "inv_freq"),
-        2 * inv_freq.shape[0], factor, int(interleaved), _dev(q_out, q.dtype, "q_out"),
-        _dev(cache, torch.int8, "cache"), _dev(cache_scales, torch.float32, "cache_scales"), pages,
-        page, _stream(stream)))
+        qp, qt[0], qt[1], kp, kt[0], kt[1], vp, vt[0], vt[1], _code(q, "q"), T, hq, hk, d,
+        _ptr(positions, torch.int32, "positions"), _ptr(slots, torch.int64, "slots"),
+        _ptr(inv_freq, torch.float64, "inv_freq"), 2 * pairs[0], factor, int(interleaved),
+        _ptr(q_out, dtype, "q_out"), _ptr(cache, torch.int8, "cache"),
+        _ptr(cache_scales, torch.float32, "cache_scales"), pages, page, _stream(stream)))
     return q_out
 
 
@@ -631,25 +656,28 @@ def q8ta_tree_attention(q, cache, cache_scales, table, lens, counts, mask, softm
     bit j of mask[b, i] lets token i see token j (None: a chain); out like q, dense; lse fp32
     [B, T, heads] or None.  Returns out."""
     torch = _torch()
-    if cache.dim() != 5 or cache.shape[1] != 2 or cache.shape[:4] != cache_scales.shape:
+    cs = cache.shape
+    if len(cs) != 5 or cs[1] != 2 or cs[:4] != cache_scales.shape:
         raise ValueError("cache [pages, 2, kv_heads, page, dim] and cache_scales [pages, 2, "
                          "kv_heads, page] expected")
-    pages, _, hk, page, d = cache.shape
-    qp = _view(q, "q", 4)
-    B, T, hq, _ = q.shape
-    if q.shape[3] != d or out.shape != q.shape or (lse is not None and lse.shape != (B, T, hq)):
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, cache {tuple(cache.shape)}, out "
+    pages, _, hk, page, d = cs
+    qp, qs, qt = _view(q, "q", 4)
+    B, T, hq, qd = qs
+    if qd != d or out.shape != qs or (lse is not None and lse.shape != (B, T, hq)):
+        raise ValueError(f"shape mismatch: q {tuple(qs)}, cache {tuple(cs)}, out "
                          f"{tuple(out.shape)}, lse {None if lse is None else tuple(lse.shape)}")
-    if (table.dim() != 2 or table.shape[0] != B or lens.shape != (B,) or
+    ts = table.shape
+    if (len(ts) != 2 or ts[0] != B or lens.shape != (B,) or
             (counts is not None and counts.shape != (B,)) or
             (mask is not None and mask.shape != (B, T))):
         raise ValueError("table [B, pages], lens [B], counts [B] and mask [B, T] expected")
+    i32 = torch.int32
     _check(lib().q8ta_tree_attention(
-        qp, q.stride(0), q.stride(1), q.stride(2), _code(q, "q", ("fp16", "bf16")), B, T, hq, hk, d,
-        _dev(cache, torch.int8, "cache"), _dev(cache_scales, torch.float32, "cache_scales"), pages,
-        page, _dev(table, torch.int32, "table"), table.shape[1], _dev(lens, torch.int32, "lens"),
-        _opt(counts, torch.int32, "counts"), _opt(mask, torch.int64, "mask"), softmax_scale,
-        _dev(out, q.dtype, "out"), _opt(lse, torch.float32, "lse"), _stream(stream)))
+        qp, qt[0], qt[1], qt[2], _code(q, "q", ("fp16", "bf16")), B, T, hq, hk, d,
+        _ptr(cache, torch.int8, "cache"), _ptr(cache_scales, torch.float32, "cache_scales"), pages,
+        page, _ptr(table, i32, "table"), ts[1], _ptr(lens, i32, "lens"),
+        _opt_ptr(counts, i32, "counts"), _opt_ptr(mask, torch.int64, "mask"), softmax_scale,
+        _ptr(out, q.dtype, "out"), _opt_ptr(lse, torch.float32, "lse"), _stream(stream)))
     return out
 
 
@@ -661,17 +689,18 @@ def q8ta_sample(logits, temperature, top_k, top_p, min_p, u, tokens, logprobs=No
     or None: the token's log-probability among those kept.  Temperature 0 is greedy.  Returns
     tokens."""
     torch = _torch()
-    lp = _view(logits, "logits", 2)
-    B, V = logits.shape
-    for name, t in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p),
-                    ("min_p", min_p), ("u", u), ("tokens", tokens), ("logprobs", logprobs)):
-        if t is not None and t.shape != (B,):
-            raise ValueError(f"{name} must be [{B}] (got {tuple(t.shape)})")
-    f32 = torch.float32
+    lp, ls, lt = _view(logits, "logits", 2)
+    B, V = ls
+    rows = (B,)
+    for t in (temperature, top_k, top_p, min_p, u, tokens, logprobs):
+        if t is not None and t.shape != rows:
+            raise ValueError(f"temperature, top_k, top_p, min_p, u, tokens and logprobs must be [{B}] "
+                             f"(got {tuple(t.shape)})")
+    f32, i32 = torch.float32, torch.int32
     _check(lib().q8ta_sample(
-        lp, logits.stride(0), _code(logits, "logits"), B, V, _dev(temperature, f32, "temperature"),
-        _opt(top_k, torch.int32, "top_k"), _opt(top_p, f32, "top_p"), _opt(min_p, f32, "min_p"),
-        _dev(u, f32, "u"), _dev(tokens, torch.int32, "tokens"), _opt(logprobs, f32, "logprobs"),
+        lp, lt[0], _code(logits, "logits"), B, V, _ptr(temperature, f32, "temperature"),
+        _opt_ptr(top_k, i32, "top_k"), _opt_ptr(top_p, f32, "top_p"), _opt_ptr(min_p, f32, "min_p"),
+        _ptr(u, f32, "u"), _ptr(tokens, i32, "tokens"), _opt_ptr(logprobs, f32, "logprobs"),
         _stream(stream)))
     return tokens
 
@@ -685,30 +714,31 @@ def q8ta_linear_lora(x, input_scale, input_zero_point, weight, weight_scales, bi
     adapter's own rank); adapter_ids int32 [M], negative for none; out [M, N] fp32, fp16 or bf16.
     Returns out."""
     torch = _torch()
-    if x.dim() != 2 or weight.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
+    xs, wsh, ash = x.shape, weight.shape, lora_a.shape
+    if len(xs) != 2 or len(wsh) != 2 or len(ash) != 3:
         raise ValueError("x [M, K], weight [N, K], lora_a [adapters, rank, K] and lora_b [adapters, N, "
                          "rank] expected")
-    M, K = x.shape
-    N = weight.shape[0]
-    na, r = lora_a.shape[0], lora_a.shape[1]
-    if (weight.shape[1] != K or lora_a.shape[2] != K or lora_b.shape != (na, N, r) or
-            out.shape != (M, N) or adapter_ids.shape != (M,)):
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, weight {tuple(weight.shape)}, lora_a "
-                         f"{tuple(lora_a.shape)}, lora_b {tuple(lora_b.shape)}, adapter_ids "
-                         f"{tuple(adapter_ids.shape)}, out {tuple(out.shape)}")
+    M, K = xs
+    N = wsh[0]
+    na, r, ak = ash
+    if (wsh[1] != K or ak != K or lora_b.shape != (na, N, r) or out.shape != (M, N) or
+            adapter_ids.shape != (M,)):
+        raise ValueError(f"shape mismatch: x {tuple(xs)}, weight {tuple(wsh)}, lora_a {tuple(ash)}, "
+                         f"lora_b {tuple(lora_b.shape)}, adapter_ids {tuple(adapter_ids.shape)}, out "
+                         f"{tuple(out.shape)}")
     for name, t, n in (("weight_scales", weight_scales, N), ("bias", bias, N),
                        ("adapter_scales", adapter_scales, na), ("ranks", ranks, na)):
         if t is not None and t.numel() < n:
             raise ValueError(f"{name} must have {n} entries (got {t.numel()})")
-    f32 = torch.float32
+    f32, i8, i32, ad = torch.float32, torch.int8, torch.int32, lora_a.dtype
     _check(lib().q8ta_linear_lora(
-        _dev(x, torch.int8, "x"), M, K, input_scale, input_zero_point,
-        _dev(weight, torch.int8, "weight"), N, _dev(weight_scales, f32, "weight_scales"),
-        _opt(bias, f32, "bias"), _dev(lora_a, lora_a.dtype, "lora_a"),
-        _dev(lora_b, lora_a.dtype, "lora_b"), _code(lora_a, "lora_a", ("fp16", "bf16")), na, r,
-        _opt(adapter_scales, f32, "adapter_scales"), _opt(ranks, torch.int32, "ranks"),
-        _dev(adapter_ids, torch.int32, "adapter_ids"), _act(activation),
-        _dev(out, out.dtype, "out"), _code(out, "out"), _stream(stream)))
+        _ptr(x, i8, "x"), M, K, input_scale, input_zero_point, _ptr(weight, i8, "weight"), N,
+        _ptr(weight_scales, f32, "weight_scales"), _opt_ptr(bias, f32, "bias"),
+        _ptr(lora_a, ad, "lora_a"), _ptr(lora_b, ad, "lora_b"),
+        _code(lora_a, "lora_a", ("fp16", "bf16")), na, r,
+        _opt_ptr(adapter_scales, f32, "adapter_scales"), _opt_ptr(ranks, i32, "ranks"),
+        _ptr(adapter_ids, i32, "adapter_ids"), _act(activation), _ptr(out, out.dtype, "out"),
+        _code(out, "out"), _stream(stream)))
     return out
 
 
