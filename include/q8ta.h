@@ -633,8 +633,8 @@ q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_he
  * table_pages * page_size < 2^31 - 64, softmax_scale finite and > 0
  * (Q8TA_ERR_QPARAM); dim a multiple of 16 up to 256, page_size a multiple of
  * 16 and 16-byte aligned cache and cache_scales (else Q8TA_ERR_UNSUPPORTED).
- * batch == 0 is a no-op.  Workspace where the keys are split over workgroups:
- * 4 * (dim + 2) bytes for each split of each row.
+ * batch == 0 is a no-op.  Workspace, but for caches of few keys: 4 * (dim +
+ * 2) bytes for each of up to 32768 partial rows.
  */
 q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q_token_stride,
                                 int64_t q_head_stride, q8ta_dtype dtype, int64_t batch,

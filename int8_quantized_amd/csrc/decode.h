@@ -57,9 +57,7 @@ __device__ __forceinline__ Half from_float<Half>(float x) {
 }
 template <>
 __device__ __forceinline__ Bfloat from_float<Bfloat>(float x) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, x);
-  const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1)) >> 16;
-  return Bfloat{(uint16_t)(x != x ? (u >> 16) | 0x40 : r)};
+  return Bfloat{__builtin_bit_cast(uint16_t, (__bf16)x)};
 }
 
 struct RopeArgs {
@@ -83,6 +81,7 @@ hipError_t launch_rope_append(const RopeArgs& a, hipStream_t s);
 struct AttnArgs {
   const void* q;            // [batch, tokens, heads, dim] view, unit inner stride
   int64_t q_bs, q_ts, q_hs;
+  bool q_aligned;           // every row starts on 16 bytes
   int dtype;
   int batch, tokens, heads, kv_heads, group, dim;   // group = heads / kv_heads
   const int8_t* cache;      // [pages, 2, kv_heads, page, dim]
@@ -98,11 +97,12 @@ struct AttnArgs {
   float scale;              // softmax scale
   void* out;                // [batch, tokens, heads, dim]
   float* lse;               // [batch, tokens, heads] or NULL
-  // Split over the keys: workgroup `split` of a request takes keys
-  // [split * chunk, (split + 1) * chunk); with more than one split, partial
-  // sums go to part_o [splits, rows, dim] and part_ml [splits, rows] (running
-  // maximum in powers of two, sum), rows = batch * tokens * heads.
-  int chunk, splits;
+  // Row blocks of a key head; keys of a grain; workgroups; and where a cut
+  // unit's sums go: part_o [slots, rows of a block, dim] and part_ml [slots,
+  // rows of a block] (running maximum in powers of two, sum), two slots a
+  // workgroup (see grains_of in attention.hip).
+  int row_blocks, grain, groups;
+  FastDiv grain_div, groups_div, heads_blocks_div;
   float* part_o;
   float2* part_ml;
 };
@@ -140,8 +140,12 @@ struct LoraArgs {
   void* y;
   int y_type;
   // t[m, r] = adapter_scale * s_in * sum_k A[r, k] (x[m, k] - zp) of the row's
-  // adapter (0 past its rank), [M, rank_pad]; rows without one are not written
+  // adapter (0 past its rank), [M, rank_pad]; rows without one are not written.
+  // With parts > 0, as that many bf16 values whose sum it is, [parts, M,
+  // rank_pad], instead.
   float* t = nullptr;
+  uint16_t* tp = nullptr;
+  int parts = 0;
 };
 // The adapter of row m, -1 for none (any id outside [0, adapters)).
 __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t m) {
@@ -154,5 +158,9 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int id) {
   return r < 0 ? 0 : (r < a.rank ? r : a.rank);
 }
 hipError_t launch_linear_lora(LoraArgs a, hipStream_t s);
+// The large GEMMs with the adapters' epilogue (t formed before): K and
+// alignment as for launch_gemm_w8 / launch_gemm_mx.
+hipError_t launch_gemm_w8_lora(const LoraArgs& a, hipStream_t s);
+hipError_t launch_gemm_mx_lora(const LoraArgs& a, hipStream_t s);
 
 }  // namespace q8ta

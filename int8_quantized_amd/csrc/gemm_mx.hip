@@ -51,6 +51,7 @@
 #include <cstdlib>
 #include <type_traits>
 
+#include "lora_epilogue.h"
 #include "q8ta_internal.h"
 
 namespace q8ta {
@@ -140,9 +141,10 @@ __device__ __forceinline__ int cslot(int r) { return (r & 3) * (BN / 4) + (r >> 
 // half-wave store 32 consecutive floats (one whole 128-byte line) of one
 // output row per register; in the other form each store instruction writes
 // 16-byte pieces of 32 rows, which the L2 has to merge.
-template <class C, bool PRE, bool KFULL, bool TR>
+// EP: NoLora, or the adapters' epilogue of q8ta_linear_lora (TR operand order).
+template <class C, bool PRE, bool KFULL, bool TR, class EP = NoLora>
 __global__ __launch_bounds__(C::NT, C::BLOCKS_PER_CU) void k_gemm_mx(LinearArgs a, int tiles_m,
-                                                                      int tiles_n) {
+                                                                      int tiles_n, EP ep) {
   __shared__ __attribute__((aligned(16))) int8_t smem[2 * C::STAGE];
   __shared__ __attribute__((aligned(16))) float epi_sc[C::BN];
   __shared__ __attribute__((aligned(16))) float epi_bi[C::BN];
@@ -373,6 +375,20 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS_PER_CU) void k_gemm_mx(LinearArgs 
   }
   __syncthreads();
 
+  if constexpr (EP::kOn) {
+    int32_t zc[C::FN];
+    float sc[C::FN], bi[C::FN];
+    Static<0, C::FN>::each([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      const int sl = cslot<C::BN>(wn * C::WN + i * 32 + lrow);
+      zc[i] = a.izp * epi_ws[sl];
+      sc[i] = epi_sc[sl];
+      bi[i] = epi_bi[sl];
+    });
+    lora_finish<typename EP::AT, typename EP::YT, C::FN>(ep.l, acc, zc, sc, bi, bm0 + wm * C::WM, bn0 + wn * C::WN, lane);
+    return;
+  }
+
   // Interior tiles of an output with fewer than 2^31 elements take the store
   // path without bounds checks: each lane's element offset is one 32-bit
   // value per channel, and the row offsets c * N are wave-uniform (scalar).
@@ -487,22 +503,38 @@ hipError_t launch_mx2(const LinearArgs& a, int tiles_m, int tiles_n, hipStream_t
   if (a.K % Cfg::BK == 0) {
     if (tr)
       hipLaunchKernelGGL((k_gemm_mx<Cfg, PRE, true, true>), grid, dim3(Cfg::NT), 0, s, a, tiles_m,
-                         tiles_n);
+                         tiles_n, NoLora{});
     else
       hipLaunchKernelGGL((k_gemm_mx<Cfg, PRE, true, false>), grid, dim3(Cfg::NT), 0, s, a, tiles_m,
-                         tiles_n);
+                         tiles_n, NoLora{});
   } else {
     if (tr)
       hipLaunchKernelGGL((k_gemm_mx<Cfg, PRE, false, true>), grid, dim3(Cfg::NT), 0, s, a, tiles_m,
-                         tiles_n);
+                         tiles_n, NoLora{});
     else
       hipLaunchKernelGGL((k_gemm_mx<Cfg, PRE, false, false>), grid, dim3(Cfg::NT), 0, s, a,
-                         tiles_m, tiles_n);
+                         tiles_m, tiles_n, NoLora{});
   }
   return hipGetLastError();
 }
 
 }  // namespace
+
+hipError_t launch_gemm_mx_lora(const LoraArgs& a, hipStream_t s) {
+  const int tiles_m = (int)((a.lin.M + Cfg::BM - 1) / Cfg::BM);
+  const int tiles_n = (int)((a.lin.N + Cfg::BN - 1) / Cfg::BN);
+  const dim3 grid((unsigned)(tiles_m * tiles_n));
+  return lora_types(a, [&](const auto& ep) {
+    typedef std::decay_t<decltype(ep)> EP;
+    if (a.lin.K % Cfg::BK == 0)
+      hipLaunchKernelGGL((k_gemm_mx<Cfg, false, true, true, EP>), grid, dim3(Cfg::NT), 0, s, a.lin,
+                         tiles_m, tiles_n, ep);
+    else
+      hipLaunchKernelGGL((k_gemm_mx<Cfg, false, false, true, EP>), grid, dim3(Cfg::NT), 0, s, a.lin,
+                         tiles_m, tiles_n, ep);
+    return hipGetLastError();
+  });
+}
 
 hipError_t launch_gemm_mx(const LinearArgs& a, hipStream_t s) {
   const int tiles_m = (int)((a.M + Cfg::BM - 1) / Cfg::BM);

@@ -69,6 +69,7 @@
 //    that are not stored); K must be a multiple of 64 (no partial steps).
 #include <type_traits>
 
+#include "lora_epilogue.h"
 #include "q8ta_internal.h"
 
 namespace q8ta {
@@ -141,8 +142,10 @@ struct Smem {
 // K loop and epilogue of one wave with FN weight fragments (32 rows each)
 // starting at tile row wr0 and activation rows xr0 .. xr0 + 63.  SUMK: the W
 // slice this wave sums for sum w (-1: none; PRE: never).
-template <class T, int SUMK, int SPAR, bool PRE, bool TR, bool PK>
-__device__ __forceinline__ void run(const LinearArgs& a, const Smem& sm,
+// EP: what becomes of the sums beyond the requantized or dequantized output
+// (NoLora), or the adapters' epilogue of q8ta_linear_lora (TR operand order).
+template <class T, int SUMK, int SPAR, bool PRE, bool TR, bool PK, class EP>
+__device__ __forceinline__ void run(const LinearArgs& a, const EP& ep, const Smem& sm,
                                     const int8_t* const (&gb)[T::NQ], const uint32_t (&voff)[T::NQ],
                                     const int (&ldo)[T::NQ], const int (&kst)[T::NQ],
                                     int wr0, int xr0, int lane, int tid, int KT, int64_t bm0,
@@ -283,6 +286,20 @@ __device__ __forceinline__ void run(const LinearArgs& a, const Smem& sm,
     }
   });
   __syncthreads();
+
+  if constexpr (EP::kOn) {
+    int32_t zc[FN];
+    float sc[FN], bi[FN];
+    Static<0, FN>::each([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      const int sl = cslot<T::TN>(wr0 + i * 32 + lrow);
+      zc[i] = a.izp * sm.ws[sl];
+      sc[i] = sm.sc[sl];
+      bi[i] = sm.bi[sl];
+    });
+    lora_finish<typename EP::AT, typename EP::YT, FN>(ep.l, acc, zc, sc, bi, bm0 + xr0, bn0 + wr0, lane);
+    return;
+  }
 
   // Interior tiles of an output with fewer than 2^31 elements store without
   // bounds checks: one 32-bit element offset per lane, wave-uniform row bases.
@@ -445,9 +462,9 @@ __device__ __forceinline__ void run(const LinearArgs& a, const Smem& sm,
 
 // One tile of shape T: tile t of a grid of tiles_m x tiles_n tiles (M
 // fastest) covering output columns n0 .. (tile column tn at n0 + tn * TN).
-template <class T, bool PRE, bool TR, bool PK>
-__device__ __forceinline__ void gemm_tile(const LinearArgs& a, const Smem& sm, int t, int tiles_m,
-                                          int64_t n0) {
+template <class T, bool PRE, bool TR, bool PK, class EP>
+__device__ __forceinline__ void gemm_tile(const LinearArgs& a, const EP& ep, const Smem& sm, int t,
+                                          int tiles_m, int64_t n0) {
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -526,18 +543,18 @@ __device__ __forceinline__ void gemm_tile(const LinearArgs& a, const Smem& sm, i
   // there are two such waves), so the v_dot4 work is the same on every SIMD.
   static_assert(T::WAVES_M == 2 || T::WAVES_M == 4, "sum w split");
   if (PRE) {
-    run<T, -1, -1, PRE, TR, PK>(a, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi);
+    run<T, -1, -1, PRE, TR, PK>(a, ep, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi);
   } else if constexpr (T::WAVES_M == 2) {
     if (wm == 0)
-      run<T, 0, -1, PRE, TR, PK>(a, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi);
+      run<T, 0, -1, PRE, TR, PK>(a, ep, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi);
     else
-      run<T, 1, -1, PRE, TR, PK>(a, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi);
+      run<T, 1, -1, PRE, TR, PK>(a, ep, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi);
   } else {
     switch (wm) {
-      case 0: run<T, 0, 0, PRE, TR, PK>(a, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi); break;
-      case 1: run<T, 1, 0, PRE, TR, PK>(a, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi); break;
-      case 2: run<T, 0, 1, PRE, TR, PK>(a, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi); break;
-      default: run<T, 1, 1, PRE, TR, PK>(a, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi); break;
+      case 0: run<T, 0, 0, PRE, TR, PK>(a, ep, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi); break;
+      case 1: run<T, 1, 0, PRE, TR, PK>(a, ep, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi); break;
+      case 2: run<T, 0, 1, PRE, TR, PK>(a, ep, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi); break;
+      default: run<T, 1, 1, PRE, TR, PK>(a, ep, sm, gb, voff, ldo, kst, wr0, xr0, lane, tid, KT, bm0, bn0, e_sc, e_bi); break;
     }
   }
 }
@@ -549,9 +566,10 @@ __device__ __forceinline__ void gemm_tile(const LinearArgs& a, const Smem& sm, i
 // the workgroups are dispatched round-robin over the 8 XCDs; they are
 // renumbered so that XCD x walks a contiguous run of tiles (M fastest),
 // which share slabs in its L2.
-template <class TA, class TB, bool PRE, bool TR, bool PK>
+template <class TA, class TB, bool PRE, bool TR, bool PK, class EP = NoLora>
 __global__ __launch_bounds__(TA::NT, 1) void k_gemm_w8(LinearArgs a, int tiles_ma, int tiles_na,
-                                                        int tiles_mb, int tiles_nb, int64_t n0b) {
+                                                        int tiles_mb, int tiles_nb, int64_t n0b,
+                                                        EP ep) {
   static_assert(TA::NT == TB::NT, "one block size");
   constexpr int STAGE = TA::STAGE > TB::STAGE ? TA::STAGE : TB::STAGE;
   constexpr int TN = TA::TN > TB::TN ? TA::TN : TB::TN;
@@ -569,16 +587,16 @@ __global__ __launch_bounds__(TA::NT, 1) void k_gemm_w8(LinearArgs a, int tiles_m
   const int nta = tiles_ma * tiles_na;
   const int b = blockIdx.x;
   if (b < nta)
-    gemm_tile<TA, PRE, TR, PK>(a, sm, remap(b, nta), tiles_ma, 0);
+    gemm_tile<TA, PRE, TR, PK>(a, ep, sm, remap(b, nta), tiles_ma, 0);
   else
-    gemm_tile<TB, PRE, TR, PK>(a, sm, remap(b - nta, tiles_mb * tiles_nb), tiles_mb, n0b);
+    gemm_tile<TB, PRE, TR, PK>(a, ep, sm, remap(b - nta, tiles_mb * tiles_nb), tiles_mb, n0b);
 }
 
 using T256 = Tile<2, 4, 4, 2>;   // 256 x 256, waves of 128 x 64
 using T128 = Tile<4, 2, 2, 2>;   // 256 W rows x 128 X rows, waves of 64 x 64
 
-template <bool PRE, bool PK>
-hipError_t launch_plan(const LinearArgs& a, hipStream_t s) {
+template <bool PRE, bool PK, class EP = NoLora>
+hipError_t launch_plan(const LinearArgs& a, hipStream_t s, const EP& ep = EP{}) {
   const int64_t tiles_m = (a.M + T256::BM - 1) / T256::BM;
   const int64_t tiles_n = (a.N + T256::TN - 1) / T256::TN;
   const int64_t tiles = tiles_m * tiles_n;
@@ -602,12 +620,17 @@ hipError_t launch_plan(const LinearArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(tiles_m * cols + tiles_mb * rest));
   const int64_t n0b = cols * T256::TN;
   // fp32 output (fused dequantize): the transposed form, whole-line stores
-  if (a.outf != nullptr && a.acc == nullptr)
-    hipLaunchKernelGGL((k_gemm_w8<T256, T128, PRE, true, PK>), grid, dim3(T256::NT), 0, s, a,
-                       (int)tiles_m, (int)cols, (int)tiles_mb, (int)rest, n0b);
-  else
-    hipLaunchKernelGGL((k_gemm_w8<T256, T128, PRE, false, PK>), grid, dim3(T256::NT), 0, s, a,
-                       (int)tiles_m, (int)cols, (int)tiles_mb, (int)rest, n0b);
+  if constexpr (EP::kOn) {
+    hipLaunchKernelGGL((k_gemm_w8<T256, T128, PRE, true, PK, EP>), grid, dim3(T256::NT), 0, s, a,
+                       (int)tiles_m, (int)cols, (int)tiles_mb, (int)rest, n0b, ep);
+  } else {
+    if (a.outf != nullptr && a.acc == nullptr)
+      hipLaunchKernelGGL((k_gemm_w8<T256, T128, PRE, true, PK>), grid, dim3(T256::NT), 0, s, a,
+                         (int)tiles_m, (int)cols, (int)tiles_mb, (int)rest, n0b, ep);
+    else
+      hipLaunchKernelGGL((k_gemm_w8<T256, T128, PRE, false, PK>), grid, dim3(T256::NT), 0, s, a,
+                         (int)tiles_m, (int)cols, (int)tiles_mb, (int)rest, n0b, ep);
+  }
   return hipGetLastError();
 }
 
@@ -629,6 +652,11 @@ bool gemm_w8_preferred(const LinearArgs& a) {
   const int64_t tiles = ((a.M + T256::BM - 1) / T256::BM) * tiles_n;
   const int64_t half = ((a.M + T128::BM - 1) / T128::BM) * tiles_n;
   return tiles >= 256 || (tiles <= 128 && half >= 128 && half <= 256);
+}
+
+hipError_t launch_gemm_w8_lora(const LoraArgs& a, hipStream_t s) {
+  if (!gemm_w8_supported(a.lin)) return hipErrorInvalidValue;
+  return lora_types(a, [&](const auto& ep) { return launch_plan<false, false>(a.lin, s, ep); });
 }
 
 hipError_t launch_gemm_w8(const LinearArgs& a, hipStream_t s) {

@@ -76,62 +76,94 @@ __device__ __forceinline__ v4f mfma16(v4u a, v4u b, v4f c) {
                                                    __builtin_bit_cast(v8b, b), c, 0, 0, 0);
 }
 
-constexpr int kDownWaves = 8;
+constexpr int kDownWaves = 16;
 
-template <class AT>
+// RB: blocks of 16 ranks a workgroup takes, D: 64-byte steps of K whose loads
+// are in flight at once.
+template <class AT, int RB, int D>
 __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
-  __shared__ float part[kDownWaves][16][17];
+  __shared__ float part[kDownWaves][16][16 * RB + 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int64_t m0 = (int64_t)blockIdx.x * 16, M = a.lin.M, K = a.lin.K;
-  const int slot = blockIdx.y, r0 = 16 * blockIdx.z;
+  const int r0 = 16 * RB * blockIdx.z;
   const int64_t m = m0 + n < M ? m0 + n : M - 1;
   const int id = m0 + n < M ? adapter_of(a, m) : -1;
-  // the slot-th distinct adapter of the 16 rows
-  uint64_t left = __ballot(id >= 0) & 0xffff;
-  uint64_t mine = 0;
-  int ad = -1;
-  for (int s = 0; left != 0; ++s) {
-    ad = __builtin_amdgcn_readlane(id, (uint32_t)__builtin_ctzll(left));
-    mine = __ballot(id == ad) & 0xffff;
-    if (s == slot) break;
-    left &= ~mine;
-  }
-  if (left == 0) return;
-  const int rank = rank_of(a, ad);
-  const bool rok = r0 + n < rank;
-
   const int8_t* xr = a.lin.x + m * K;
-  const AT* ar = (const AT*)a.a + ((int64_t)ad * a.rank + (rok ? r0 + n : 0)) * K;
-  v4f acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  if (r0 < rank) {
-    for (int64_t k = 64 * wave; k < K; k += 64 * kDownWaves) {
-      const int64_t kk = k + 16 * g;
-      const bool ok = kk < K;
-      v4u x = v4u{0, 0, 0, 0}, p = x, q = x;
-      if (ok) x = *reinterpret_cast<const v4u*>(xr + kk);
-      if (ok && rok) {
-        p = *reinterpret_cast<const v4u*>(ar + kk);
-        q = *reinterpret_cast<const v4u*>(ar + kk + 8);
+  // the distinct adapters of the 16 rows, this workgroup's every gridDim.y-th
+  uint64_t left = __ballot(id >= 0) & 0xffff;
+  for (int slot = 0; left != 0; ++slot) {
+    const int ad = __builtin_amdgcn_readlane(id, (uint32_t)__builtin_ctzll(left));
+    const uint64_t mine = __ballot(id == ad) & 0xffff;
+    left &= ~mine;
+    if (slot % gridDim.y != blockIdx.y) continue;
+    const int rank = rank_of(a, ad);
+    const AT* ar[RB];
+    bool rok[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int r = r0 + 16 * i + n;
+      rok[i] = r < rank;
+      ar[i] = (const AT*)a.a + ((int64_t)ad * a.rank + (rok[i] ? r : 0)) * K;
+    }
+    v4f acc[RB] = {};
+    if (r0 < rank) {
+      for (int64_t k0 = 64 * wave; k0 < K; k0 += 64 * kDownWaves * D) {
+        v4u x[D], p[D][RB][2];
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          const int64_t kk = k0 + 64 * kDownWaves * d + 16 * g;
+          const bool ok = kk < K;
+          x[d] = v4u{0, 0, 0, 0};
+          if (ok) x[d] = *reinterpret_cast<const v4u*>(xr + kk);
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              p[d][i][h] = v4u{0, 0, 0, 0};
+              if (ok && rok[i]) p[d][i][h] = *reinterpret_cast<const v4u*>(ar[i] + kk + 8 * h);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          const v4u x0 = less_zp<AT>(x[d][0], x[d][1], a.lin.izp);
+          const v4u x1 = less_zp<AT>(x[d][2], x[d][3], a.lin.izp);
+#pragma unroll
+          for (int i = 0; i < RB; ++i) {
+            acc[i] = mfma16<AT>(p[d][i][0], x0, acc[i]);
+            acc[i] = mfma16<AT>(p[d][i][1], x1, acc[i]);
+          }
+        }
       }
-      acc = mfma16<AT>(p, less_zp<AT>(x[0], x[1], a.lin.izp), acc);
-      acc = mfma16<AT>(q, less_zp<AT>(x[2], x[3], a.lin.izp), acc);
     }
-  }
-  // register r of lane (n, g): rank 4g + r, row n
+    // register r of lane (n, g): rank 4g + r of the block, row n
 #pragma unroll
-  for (int r = 0; r < 4; ++r) part[wave][n][4 * g + r] = acc[r];
-  __syncthreads();
-  if (tid < 256) {
-    const int row = tid / 16, r = tid % 16;
-    if ((mine >> row) & 1) {
-      float s = 0.0f;
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int w = 0; w < kDownWaves; ++w) s += part[w][row][r];
-      const float f = a.lin.rq.s_in * (a.ad_scales ? a.ad_scales[ad] : 1.0f);
-      a.t[(m0 + row) * a.rank_pad + r0 + r] = r0 + r < rank ? s * f : 0.0f;
+      for (int r = 0; r < 4; ++r) part[wave][n][16 * i + 4 * g + r] = acc[i][r];
+    __syncthreads();
+    for (int e = tid; e < 256 * RB; e += 64 * kDownWaves) {
+      const int row = e / (16 * RB), r = e % (16 * RB);
+      if (((mine >> row) & 1) && r0 + r < a.rank_pad) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kDownWaves; ++w) s += part[w][row][r];
+        const float f = a.lin.rq.s_in * (a.ad_scales ? a.ad_scales[ad] : 1.0f);
+        const int64_t at = (m0 + row) * a.rank_pad + r0 + r;
+        float t = r0 + r < rank ? s * f : 0.0f;
+        if (a.parts == 0) {
+          a.t[at] = t;
+        } else {
+          for (int q = 0; q < a.parts; ++q) {   // each the rounding of what is left
+            const Bfloat h = from_float<Bfloat>(t);
+            a.tp[q * M * a.rank_pad + at] = h.bits;
+            t = t - to_float(h);
+          }
+        }
+      }
     }
+    __syncthreads();
   }
 }
 
@@ -167,11 +199,12 @@ __device__ __forceinline__ float up_dot(const LoraArgs& a, int ad, int64_t n, co
   return s;
 }
 
-template <class AT, class YT, int MT, int FN>
-__global__ __launch_bounds__(256) void k_lora_rows(LoraArgs a) {
-  constexpr int BM = 16 * MT, BN = 16 * FN, kWaves = 4;
-  __shared__ int32_t part[kWaves][BM][BN + 1];
-  __shared__ int32_t wsum[kWaves][BN];
+// D: steps of K whose loads are in flight ahead of the products.
+template <class AT, class YT, int MT, int FN, int WAVES, int D>
+__global__ __launch_bounds__(64 * WAVES) void k_lora_rows(LoraArgs a) {
+  constexpr int BM = 16 * MT, BN = 16 * FN;
+  __shared__ int32_t part[WAVES][BM][BN + 1];
+  __shared__ int32_t wsum[WAVES][BN];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
@@ -191,36 +224,34 @@ __global__ __launch_bounds__(256) void k_lora_rows(LoraArgs a) {
   }
   v4i acc[FN][MT] = {};
   int32_t ws[FN] = {};
-  v4i wf[FN], xf[MT];
-  auto load = [&](int64_t k) {
-    const int64_t kk = k + 16 * g;
-    const bool ok = kk < K;   // past K: the row's first bytes, cleared below
+  v4i wf[D][FN], xf[D][MT];
+  // every load unconditional: chunks past K read the row's first bytes, and
+  // the weights' are replaced by zeros when they are used
+  auto load = [&](int64_t k, v4i (&w)[FN], v4i (&x)[MT]) {
+    const int64_t kk = k + 16 * g < K ? k + 16 * g : 0;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) wf[i] = *reinterpret_cast<const v4i*>(wp[i] + (ok ? kk : 0));
+    for (int i = 0; i < FN; ++i)
+      w[i] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wp[i] + kk));
 #pragma unroll
-    for (int j = 0; j < MT; ++j) xf[j] = *reinterpret_cast<const v4i*>(xp[j] + (ok ? kk : 0));
-    if (!ok) {
-#pragma unroll
-      for (int i = 0; i < FN; ++i) wf[i] = v4i{0, 0, 0, 0};
-    }
+    for (int j = 0; j < MT; ++j) x[j] = *reinterpret_cast<const v4i*>(xp[j] + kk);
   };
-  int64_t k = 64 * wave;
-  if (k < K) load(k);
-  for (; k < K; k += 64 * kWaves) {
-    v4i wc[FN], xc[MT];
+  constexpr int kStride = 64 * WAVES;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) wc[i] = wf[i];
+  for (int d = 0; d < D; ++d) load(64 * wave + kStride * d, wf[d], xf[d]);
+  for (int64_t k0 = 64 * wave; k0 < K; k0 += kStride * D) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j) xc[j] = xf[j];
-    if (k + 64 * kWaves < K) load(k + 64 * kWaves);
+    for (int d = 0; d < D; ++d) {
+      const bool ok = k0 + kStride * d + 16 * g < K;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
+      for (int i = 0; i < FN; ++i) {
+        const v4i w = ok ? wf[d][i] : v4i{0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < MT; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wc[i], xc[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < MT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, xf[d][j], acc[i][j], 0, 0, 0);
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
-        ws[i] = __builtin_amdgcn_sdot4(wc[i][d], 0x01010101, ws[i], false);
+        for (int e = 0; e < 4; ++e) ws[i] = __builtin_amdgcn_sdot4(w[e], 0x01010101, ws[i], false);
+      }
+      if (k0 + kStride * D < K) load(k0 + kStride * (D + d), wf[d], xf[d]);
     }
   }
   // register r of lane (n, g): channel 4g + r, row n
@@ -235,13 +266,13 @@ __global__ __launch_bounds__(256) void k_lora_rows(LoraArgs a) {
     if (g == 0) wsum[wave][16 * i + n] = ws[i];
   }
   __syncthreads();
-  for (int e = tid; e < BM * BN; e += 256) {
+  for (int e = tid; e < BM * BN; e += 64 * WAVES) {
     const int row = e / BN, c = e % BN;
     const int64_t m = m0 + row, ch = n0 + c;
     if (m >= M || ch >= N) continue;
     int32_t s = 0, w = 0;
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
+    for (int v = 0; v < WAVES; ++v) {
       s += part[v][row][c];
       w += wsum[v][c];
     }
@@ -251,7 +282,7 @@ __global__ __launch_bounds__(256) void k_lora_rows(LoraArgs a) {
     y = y + (a.lin.bias ? a.lin.bias[ch] : 0.0f);
     const int ad = adapter_of(a, m);
     if (ad >= 0) y = y + up_dot<AT>(a, ad, ch, a.t + m * a.rank_pad);
-    if (a.relu) y = __builtin_fmaxf(y, 0.0f);
+    if (a.relu) y = y < 0.0f ? 0.0f : y;
     ((YT*)a.y)[m * N + ch] = from_float<YT>(y);
   }
 }
@@ -285,26 +316,39 @@ hipError_t pad_rows(const void* src, int64_t rows, int64_t bytes, int64_t padded
   return hipGetLastError();
 }
 
+template <class AT, class YT, int MT, int FN, int WAVES, int D>
+hipError_t launch_shape(const LoraArgs& a, hipStream_t s) {
+  const dim3 g((unsigned)((a.lin.N + 16 * FN - 1) / (16 * FN)),
+               (unsigned)((a.lin.M + 16 * MT - 1) / (16 * MT)));
+  hipLaunchKernelGGL((k_lora_rows<AT, YT, MT, FN, WAVES, D>), g, dim3(64 * WAVES), 0, s, a);
+  return hipGetLastError();
+}
+
 template <class AT, class YT>
 hipError_t launch_rows(const LoraArgs& a, hipStream_t s) {
-  const int64_t M = a.lin.M, N = a.lin.N;
-  if (M <= 16) {
-    const dim3 g((unsigned)((N + 15) / 16), 1);
-    hipLaunchKernelGGL((k_lora_rows<AT, YT, 1, 1>), g, dim3(256), 0, s, a);
-  } else {
-    const dim3 g((unsigned)((N + 31) / 32), (unsigned)((M + 63) / 64));
-    hipLaunchKernelGGL((k_lora_rows<AT, YT, 4, 2>), g, dim3(256), 0, s, a);
-  }
+  if (a.lin.M <= 16) return launch_shape<AT, YT, 1, 1, 16, 4>(a, s);
+  if (a.lin.M <= 32) return launch_shape<AT, YT, 2, 2, 8, 4>(a, s);
+  return launch_shape<AT, YT, 4, 2, 8, 3>(a, s);
+}
+
+template <class AT>
+hipError_t launch_down(const LoraArgs& a, hipStream_t s) {
+  const unsigned tiles = (unsigned)((a.lin.M + 15) / 16);
+  const int rb = a.rank_pad > 16 ? 2 : 1;
+  const unsigned z = (unsigned)((a.rank_pad + 16 * rb - 1) / (16 * rb));
+  // workgroups a tile's adapters are dealt over: up to 16, fewer where the
+  // tiles alone fill the card
+  unsigned slots = (unsigned)(a.adapters < 16 ? a.adapters : 16);
+  const unsigned want = 1024 / (tiles * z) + 1;
+  slots = slots < want ? slots : want;
+  const dim3 g(tiles, slots, z), t(64 * kDownWaves);
+  if (rb == 2) hipLaunchKernelGGL((k_lora_down<AT, 2, 2>), g, t, 0, s, a);
+  else hipLaunchKernelGGL((k_lora_down<AT, 1, 4>), g, t, 0, s, a);
   return hipGetLastError();
 }
 
 template <class AT>
-hipError_t launch_adapter(const LoraArgs& a, hipStream_t s) {
-  const int slots = a.adapters < 16 ? a.adapters : 16;
-  const dim3 g((unsigned)((a.lin.M + 15) / 16), (unsigned)slots, (unsigned)(a.rank_pad / 16));
-  hipLaunchKernelGGL((k_lora_down<AT>), g, dim3(64 * kDownWaves), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+hipError_t launch_few(const LoraArgs& a, hipStream_t s) {
   switch (a.y_type) {
     case Q8TA_F32: return launch_rows<AT, float>(a, s);
     case Q8TA_F16: return launch_rows<AT, Half>(a, s);
@@ -312,20 +356,32 @@ hipError_t launch_adapter(const LoraArgs& a, hipStream_t s) {
   }
 }
 
+// Which product: the eight-wave GEMM, the two-workgroup GEMM, or k_lora_rows.
+char product_of(const LinearArgs& a) {
+  if (a.M > 64 && gemm_w8_preferred(a)) return 'w';
+  return a.M > 64 ? 'x' : 'r';
+}
+
 }  // namespace
 
 hipError_t launch_linear_lora(LoraArgs a, hipStream_t s) {
   const int64_t M = a.lin.M, N = a.lin.N, K = a.lin.K;
   const int64_t at = (int64_t)a.adapters * a.rank;
-  const size_t t_bytes = ((size_t)M * a.rank_pad * 4 + 255) / 256 * 256;
+  const int64_t kp = (K + 63) / 64 * 64;
+  LinearArgs whole = a.lin;
+  whole.K = kp;
   const bool pad = K % 16 != 0 ||
                    (((uintptr_t)a.lin.x | (uintptr_t)a.lin.w | (uintptr_t)a.a) & 15) != 0;
-  const int64_t kp = (K + 63) / 64 * 64;
+  const char product = product_of(pad ? whole : a.lin);
+  a.parts = product == 'r' ? 0 : (a.y_type == Q8TA_F32 ? 3 : 2);
+  const size_t t_bytes =
+      ((size_t)M * a.rank_pad * (a.parts ? 2 * a.parts : 4) + 255) / 256 * 256;
   const size_t bytes = t_bytes + (pad ? (size_t)(M + N + 2 * at) * kp : 0);
   void* ws = nullptr;
   hipError_t e = workspace_acquire(&ws, bytes, s);
   if (e != hipSuccess) return e;
   a.t = (float*)ws;
+  a.tp = (uint16_t*)ws;
   if (pad) {
     int8_t* x = (int8_t*)ws + t_bytes;
     int8_t* w = x + M * kp;
@@ -338,8 +394,13 @@ hipError_t launch_linear_lora(LoraArgs a, hipStream_t s) {
     a.a = ap;
     a.lin.K = kp;
   }
-  if (e == hipSuccess)
-    e = a.ad_type == Q8TA_F16 ? launch_adapter<Half>(a, s) : launch_adapter<Bfloat>(a, s);
+  const bool half = a.ad_type == Q8TA_F16;
+  if (e == hipSuccess) e = half ? launch_down<Half>(a, s) : launch_down<Bfloat>(a, s);
+  if (e == hipSuccess) {
+    if (product == 'w') e = launch_gemm_w8_lora(a, s);
+    else if (product == 'x') e = launch_gemm_mx_lora(a, s);
+    else e = half ? launch_few<Half>(a, s) : launch_few<Bfloat>(a, s);
+  }
   const hipError_t f = workspace_release(ws, s);
   return e != hipSuccess ? e : f;
 }
