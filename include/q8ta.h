@@ -657,7 +657,7 @@ q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
  * T <= 0 (or NaN) is greedy: the first token, logprob 0.  top_p >= 1 and min_p
  * <= 0 keep everything; NULL top_k, top_p or min_p is off for every row.
  * Weights are formed in 64 bits and added as whole numbers of 2^-shift (shift
- * = 62 - ceil(log2 vocab)), so that the sums, and the token, do not depend on an
+ * = 62 - ceil(log2 vocab), at most 50), so that the sums, and the token, do not depend on an
  * order.  -inf logits are never taken (NaN counts as -inf); +inf logits share the
  * weight alone; a row with nothing but -inf gets token -1 and logprob -inf.
  * u: in [0, 1); at 1 and beyond the last kept token is taken.

@@ -159,7 +159,7 @@ q8ta_status q8ta_sample(const void* logits, int64_t row_stride, q8ta_dtype dtype
   a.min_p = min_p; a.u = u; a.tokens = tokens; a.logprobs = logprobs;
   int bits = 0;
   while (((int64_t)1 << bits) < vocab) ++bits;
-  a.shift = 62 - bits;
+  a.shift = 62 - bits < 50 ? 62 - bits : 50;
   return hip_status(launch_sample(a, stream), op);
 }
 
