@@ -557,7 +557,8 @@ q8ta_status q8ta_conv2d_acc(const int8_t* x, int64_t N, int64_t IC,
  * [adapters, rank, K] and lora_b [adapters, N, rank], dense, of adapter_dtype
  * (fp16 or bf16); adapter_scales: fp32 [adapters] or NULL (1 each); ranks: int32
  * [adapters] or NULL: an adapter's own rank within `rank`, what lies past it is
- * not read as numbers; adapter_ids: int32 [M]; out: dense [M, N] of
+ * not read as numbers (an adapter value that is not finite makes outputs of its
+ * own rows not finite, and no others); adapter_ids: int32 [M]; out: dense [M, N] of
  * out_dtype.  Requirements: as for q8ta_linear, M <= 2^21, N and K
  * <= 2^30, 1 <= rank <= 512, 1 <= adapters <= 2^24.  Any K and alignment: where K is no multiple of 16 or x,
  * weight or lora_a are not 16-byte aligned, they are first copied into rows
@@ -625,12 +626,15 @@ q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_he
  * [batch, tokens, heads] or NULL.
  * Scores, the softmax's maximum and sum and the output's sums are held in 32
  * bits; probabilities are rounded to fp16 for the product with the values.
- * Cache rows outside a row's keys may hold anything.  lens and counts are taken
+ * Cache rows that no token of the request sees may hold anything, and a drafted
+ * token's scale that is not finite spoils the tokens that see it alone; value
+ * scales below 2^-24 of the largest that the request's tokens see lose bits.  lens and counts are taken
  * into [0, table_pages * page_size] and [0, tokens], keys past the table's pages
  * are not there, and a page number outside [0, pages) makes its keys unseen.
  * Requirements: batch, tokens, heads, kv_heads, dim, pages, page_size and
  * table_pages >= 1, tokens <= 64, heads a multiple of kv_heads, batch <= 65535,
- * table_pages * page_size < 2^31 - 64, softmax_scale finite and > 0
+ * batch * kv_heads * ceil(tokens * heads / kv_heads / 16) <= 2^29,
+ * table_pages * page_size <= 2^31 - 1024, softmax_scale finite and > 0
  * (Q8TA_ERR_QPARAM); dim a multiple of 16 up to 256, page_size a multiple of
  * 16 and 16-byte aligned cache and cache_scales (else Q8TA_ERR_UNSUPPORTED).
  * batch == 0 is a no-op.  Workspace, but for caches of few keys: 4 * (dim +

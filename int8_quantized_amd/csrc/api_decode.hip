@@ -98,10 +98,14 @@ q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
   if (heads < 1 || kv_heads < 1 || heads > 65535 || heads % kv_heads != 0)
     return report(Q8TA_ERR_SHAPE, "%s: heads must be a multiple of kv_heads and at most 65535 (got "
                   "%lld, %lld)", op, (long long)heads, (long long)kv_heads);
-  // rows of a key head in tiles of 16, times the key heads: the grid's second size
-  if (kv_heads * ((tokens * (heads / kv_heads) + 15) / 16) > 65535)
+  // rows of a key head in tiles of 16, times the key heads
+  const int64_t blocks = kv_heads * ((tokens * (heads / kv_heads) + 15) / 16);
+  if (blocks > 65535)
     return report(Q8TA_ERR_SHAPE, "%s: too many heads (%lld) for %lld tokens", op, (long long)heads,
                   (long long)tokens);
+  if (batch * blocks > (int64_t)1 << 29)
+    return report(Q8TA_ERR_SHAPE, "%s: batch (%lld) times row tiles of 16 (%lld) must be at most 2^29",
+                  op, (long long)batch, (long long)blocks);
   if (dim < 1) return report(Q8TA_ERR_SHAPE, "%s: dim must be >= 1 (got %lld)", op, (long long)dim);
   if (dim % 16 != 0 || dim > 256)
     return report(Q8TA_ERR_UNSUPPORTED, "%s: dim must be a multiple of 16 up to 256 (got %lld)", op,
@@ -111,8 +115,8 @@ q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     return report(Q8TA_ERR_SHAPE, "%s: pages, page_size and table_pages must be >= 1 and the cache at "
                   "most 2^40 elements (got %lld, %lld, %lld)", op, (long long)pages,
                   (long long)page_size, (long long)table_pages);
-  if (table_pages > (((int64_t)1 << 31) - 65) / page_size)
-    return report(Q8TA_ERR_SHAPE, "%s: table_pages * page_size must be below 2^31 - 64", op);
+  if (table_pages > (((int64_t)1 << 31) - 1024) / page_size)
+    return report(Q8TA_ERR_SHAPE, "%s: table_pages * page_size must be at most 2^31 - 1024", op);
   if (page_size % 16 != 0)
     return report(Q8TA_ERR_UNSUPPORTED, "%s: page_size must be a multiple of 16 (got %lld)", op,
                   (long long)page_size);

@@ -24,8 +24,8 @@
 //    128 against outputs that are means over the context and come out near
 //    zero: off by 1 % of such an output at 700 keys.)
 //  * Queries: fp16 as they are; bf16 scaled by a power of two that puts the
-//    largest of the wave's elements in [2^14, 2^15), where fp16 holds every
-//    element exactly but those more than 2^28 below it.  So a score is a sum
+//    row's largest element in [2^14, 2^15), where fp16 holds every element
+//    exactly but those more than 2^28 below it.  So a score is a sum
 //    of exact products in 32 bits.
 //  * The keys are the A operand: lane l gets the scores of query l % 16 for
 //    keys 16t + 4(l / 16) + r, which is also where the B operand of the second
@@ -189,8 +189,8 @@ __device__ __forceinline__ int64_t row_at(const AttnArgs& a, int b, int kvh, int
 // part of the last, whose sums go to slots 2i and 2i + 1 of workgroup i, for
 // k_attn_join.
 __device__ __forceinline__ int grains_of(const AttnArgs& a, int b) {
-  const int g = (int)fast_div((uint32_t)(span_of(a, b).total + a.grain - 1), a.grain_div);
-  return g < 1 ? 1 : g;
+  const int total = span_of(a, b).total;
+  return total < 1 ? 1 : (int)fast_div((uint32_t)(total - 1), a.grain_div) + 1;
 }
 // Running sums over the lanes of a wave (every lane active): within rows of 16
 // lanes, then each row's last sum onto the rows after it.
@@ -356,11 +356,12 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
   int step = k_begin + kStep * wave;
   v8h q[QT][DP / 32];
   uint64_t bits[QT];
-  float fac = a.scale * kLog2e;
+  float fac = a.scale * kLog2e;   // the first row tile's
+  int less[QT] = {};              // log2 of tile i - 1's factor over tile i's
   uint32_t ok_now;
   {
     v4u raw[QT][DP / 32];
-    float top = 0.0f;
+    int last = 0;
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
       const int row = row0 + 16 * i + n;
@@ -382,26 +383,28 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
       load_v();
     }
     ok_now = ok;
-    float up = 1.0f;
-    if constexpr (kBf) {
 #pragma unroll
-      for (int i = 0; i < QT; ++i)
+    for (int i = 0; i < QT; ++i) {
+      float up = 1.0f;
+      if constexpr (kBf) {
+        float top = 0.0f;
 #pragma unroll
         for (int k = 0; k < DP / 32; ++k)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t w = raw[i][k][e];
-            top = __builtin_fmaxf(top, __builtin_fabsf(__builtin_bit_cast(float, w << 16)));
-            top = __builtin_fmaxf(top, __builtin_fabsf(__builtin_bit_cast(float, w & 0xffff0000u)));
+            top = __builtin_fmaxf(top, finite_size(__builtin_bit_cast(float, w << 16)));
+            top = __builtin_fmaxf(top, finite_size(__builtin_bit_cast(float, w & 0xffff0000u)));
           }
-#pragma unroll
-      for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
-      const int sh = 14 - unit_exponent(top);
-      up = pow2f(sh);
-      fac = fac * pow2f(-sh);
-    }
-#pragma unroll
-    for (int i = 0; i < QT; ++i) {
+        top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+        // (rows below 2^-40, whose scores are none, by as much as that)
+        const int e = unit_exponent(top), sh = 14 - (e < -40 ? -40 : e);
+        up = pow2f(sh);
+        less[i] = sh - last;
+        last = sh;
+        if (i == 0) fac = fac * pow2f(-sh);
+      }
 #pragma unroll
       for (int k = 0; k < DP / 32; ++k) {
         Frag f;
@@ -459,14 +462,20 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
     // past the context, and where a page is none: keys a row may not see
     // (their scales may hold anything, so they are replaced, not multiplied away)
     const bool masked = step + kStep > sp.ctx || step + kStep > k_end || ok_now != (1u << TL) - 1;
-    uint32_t real = ~0u;   // bit 4t + r: this lane's key 16t + 4g + r is one
+    uint32_t real = ~0u;   // bit 4t + r: this lane's key 16t + 4g + r is one that some row sees
     if (masked) {
       real = 0;
+      uint64_t any_bits = bits[0];
+#pragma unroll
+      for (int i = 1; i < QT; ++i) any_bits |= bits[i];
+#pragma unroll
+      for (int x = 1; x < 16; x *= 2) any_bits |= __shfl_xor(any_bits, x);
 #pragma unroll
       for (int t = 0; t < TL; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const bool in = ((ok_now >> t) & 1) && step + 16 * t + 4 * g + r < k_end;
+          const int at = step + 16 * t + 4 * g + r - sp.ctx;
+          const bool in = ((ok_now >> t) & 1) && at < k_end - sp.ctx && (at < 0 || ((any_bits >> (at & 63)) & 1));
           real |= (uint32_t)in << (4 * t + r);
           vs[t][r] = in ? vs[t][r] : 0.0f;
         }
@@ -505,6 +514,12 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
       // e = 2^(s - m)
       float e[TL][4], top = 0.0f;
       const float base = m[i] == none ? 0.0f : m[i];
+      if (kBf && i > 0) {   // from one row's factor to the next
+#pragma unroll
+        for (int t = 0; t < TL; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) kf[t][r] = __builtin_ldexpf(kf[t][r], -less[i]);
+      }
 #pragma unroll
       for (int t = 0; t < TL; ++t)
 #pragma unroll
@@ -629,7 +644,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
       f[w] = M == none ? 0.0f : __builtin_amdgcn_exp2f(st[w].x - M);
-      L += st[w].y * f[w];
+      if (used) L += st[w].y * f[w];   // (an unused row's sum may not be finite)
     }
 #pragma unroll
     for (int j = 0; j < (kQuads + kPer - 1) / kPer; ++j) {
@@ -670,8 +685,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int E = DP / 64;
   const int lane = threadIdx.x & 63;
   const int64_t rows = (int64_t)a.batch * a.tokens * a.heads;
-  const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (at >= rows) return;
+  for (int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+       at < rows; at += (int64_t)gridDim.x * 4) {
   const int b = (int)(at / ((int64_t)a.tokens * a.heads));
   const int within = (int)(at - (int64_t)b * a.tokens * a.heads);
   const int tok = within / a.heads, head = within % a.heads;
@@ -682,7 +697,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   grains.of(a, lane, b, before, of_b);
   const int x0 = before * a.kv_heads * a.row_blocks + (kvh * a.row_blocks + r / R) * of_b;
   const int first = run_of(runs, x0), last = run_of(runs, x0 + of_b - 1);
-  if (first == last) return;   // finished where it was computed
+  if (first == last) continue;   // finished where it was computed
   const int n = last - first + 1, mr = r % R;
   // part i: the first run's last slot, then the others' first
   auto slot_of = [&](int i) { return (int64_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * R + mr; };
@@ -725,6 +740,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   for (int j = 0; j < E; ++j)
     if (lane + 64 * j < a.dim) ((T*)a.out)[at * a.dim + lane + 64 * j] = from_float<T>(x[j] * inv);
   if (lane == 0 && a.lse) a.lse[at] = L != 0.0f ? (M + __builtin_log2f(L)) * kLn2 : -INFINITY;
+  }
 }
 
 // `resident`: workgroups of this shape that run at once; 0: no unit is cut
@@ -736,10 +752,12 @@ hipError_t launch_shape(AttnArgs a, int resident, hipStream_t s) {
   a.row_blocks = (a.tokens * a.group + R - 1) / R;
   const int64_t units = (int64_t)a.batch * a.kv_heads * a.row_blocks;
   int64_t grain = resident ? 16 * TL * WAVES : keys;
-  while (units * ((keys + grain - 1) / grain) >= (int64_t)1 << 30) grain *= 2;
+  while (units * ((keys + grain - 1) / grain) >= (int64_t)1 << 30) grain = 2 * grain < keys ? 2 * grain : keys;
   const int64_t most = units * ((keys + grain - 1) / grain);
   a.grain = (int)grain;
-  a.groups = (int)(resident && most > resident ? resident : most);
+  // (the one-launch form: a workgroup a unit, within a launch's 2^32 threads)
+  const int64_t cap = resident ? resident : 65536;
+  a.groups = (int)(most < cap ? most : cap);
   a.grain_div = make_fastdiv((uint32_t)a.grain);
   a.groups_div = make_fastdiv((uint32_t)a.groups);
   a.heads_blocks_div = make_fastdiv((uint32_t)(a.kv_heads * a.row_blocks));
@@ -757,7 +775,7 @@ hipError_t launch_shape(AttnArgs a, int resident, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (cut) {
     if (e == hipSuccess) {
-      hipLaunchKernelGGL((k_attn_join<T, DP, R>), dim3((unsigned)((all + 3) / 4)), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((k_attn_join<T, DP, R>), dim3((unsigned)(all < (int64_t)1 << 20 ? (all + 3) / 4 : 1 << 18)), dim3(256), 0, s, a);
       e = hipGetLastError();
     }
     const hipError_t f = workspace_release(ws, s);

@@ -162,6 +162,57 @@ def test_tree_attention_unseen_rows_hold_anything(T, fill):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("fill", [math.nan, math.inf, -6e4])
+@pytest.mark.parametrize("T", [2, 7, 40])
+def test_tree_attention_queries_not_in_use_hold_anything(T, fill, dtype):
+    c = make(3, T, 8, 2, 64, 16, [300, 5, 0], seed=12, counts=[T - 1, 1, 0], dtype=dtype)
+    for b, n in enumerate((T - 1, 1, 0)):
+        c["q"][b, n:] = fill * (1e30 if dtype == "bf16" else 1.0)
+    clean = dict(c, q=torch.where(c["q"].float().abs() < 100, c["q"], torch.zeros_like(c["q"])))
+    want, want_lse, tol, tol_lse = definition(clean)
+    out, lse = run(c)
+    got, g = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(got - want) <= tol * 1.01 + np.abs(want) * torch.finfo(out.dtype).eps * 0.505 + 1e-7).all()
+    none = np.isneginf(want_lse)
+    assert (np.isneginf(g) == none).all()
+    assert (np.abs(g - np.where(none, 0, want_lse))[~none] <= tol_lse[~none]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fill", [math.nan, math.inf, 3e38])
+@pytest.mark.parametrize("T,n", [(3, 70), (24, 500), (40, 9)])
+def test_tree_attention_drafted_rows_that_others_see_hold_anything(T, n, fill):
+    """A drafted token's cache row whose scales are no numbers spoils the tokens that see it and no
+    other; one that no token sees may hold any number too."""
+    c = make(1, T, 8, 2, 64, 16, [n], seed=13)
+    bad = 1
+    if math.isfinite(fill):
+        c["mask"][0, 2:] &= ~(1 << bad)
+        c["mask"][0, bad] = 1
+    saw = ((c["mask"][0].view(np.uint64) >> np.uint64(bad)) & np.uint64(1)) == 1
+    assert saw.any() != math.isfinite(fill) and not saw.all()
+    want, want_lse, tol, tol_lse = definition(c)
+    s = n + bad
+    c["scales"][c["table"][0, s // 16], :, :, s % 16] = fill
+    out, lse = run(c)
+    err = np.abs(out.double().cpu().numpy() - want)
+    ok = err <= tol * 1.01 + np.abs(want) * torch.finfo(out.dtype).eps * 0.505 + 1e-7
+    assert ok[0, ~saw].all()
+    assert (np.abs(lse.double().cpu().numpy() - want_lse) <= tol_lse)[0, ~saw].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 20])
+def test_tree_attention_heads_of_different_size(T):
+    """Queries of one head 2^60 times another's: each keeps its own precision."""
+    c = make(1, T, 8, 1, 64, 16, [100], seed=14)
+    c["q"][:, :, 1::2] *= 2.0 ** -60
+    c["q"][:, :, 0] *= 2.0 ** 20
+    check(c)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 20])
 def test_tree_attention_wide_scores_and_scales(T):
     """Scores of hundreds (one key takes all), value scales over many orders."""
@@ -247,6 +298,7 @@ def test_tree_attention_refusals():
     for bad in (dict(batch=-1), dict(batch=65536), dict(tokens=0), dict(tokens=65), dict(heads=0),
                 dict(kv_heads=0), dict(heads=7), dict(heads=65536, kv_heads=1), dict(dim=0),
                 dict(heads=65535, kv_heads=65535, tokens=64), dict(pages=0), dict(page=0),
+                dict(batch=65535, heads=65535, kv_heads=65535, tokens=1),
                 dict(table_pages=0), dict(table_pages=1 << 27), dict(page=1 << 31),
                 dict(pages=1 << 40), dict(qb=-1), dict(qt=1 << 41)):
         refuse(q8.Q8TA_ERR_SHAPE, **bad)
