@@ -56,6 +56,18 @@ __device__ __forceinline__ lora_v4u lora_b8(const AT* b, int r, int rank, bool v
   return w;
 }
 
+// Non-zero where a value of the eight is infinite or NaN: an exponent of ones
+// carries into the sign's place.
+template <class AT>
+__device__ __forceinline__ uint32_t not_finite(const lora_v4u& w) {
+  constexpr uint32_t e = std::is_same<AT, Half>::value ? 0x7c007c00u : 0x7f807f80u;
+  constexpr uint32_t one = std::is_same<AT, Half>::value ? 0x04000400u : 0x00800080u;
+  uint32_t carry = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) carry |= (w[i] & e) + one;
+  return carry & 0x80008000u;
+}
+
 // y += t B^T for the 64 rows and 32 * FN channels of a wave's fragments.  The
 // rows' adapters are taken one after the other; rows of another adapter have a
 // t of zero.  t comes as P bf16 parts (its rounding to 2^-17 for two, 2^-25 for
@@ -83,6 +95,7 @@ __device__ __forceinline__ void lora_add(const LoraArgs& l, lora_v16f (&y)[FN][2
     const AT* bb = (const AT*)l.b + (int64_t)ad * N * l.rank;
     const uint16_t* t = l.tp + (row0 + lrow) * l.rank_pad + 8 * kg;
     const bool in0 = (mine >> lrow) & 1, in1 = (mine >> (32 + lrow)) & 1;
+    uint32_t odd = 0;   // bit i: this lane's channel of fragment i has such a value
     for (int r0 = 0; r0 < rank; r0 += 16 * H) {
       lora_v4u tf[H][2][P], w[H][FN];
 #pragma unroll
@@ -100,6 +113,19 @@ __device__ __forceinline__ void lora_add(const LoraArgs& l, lora_v16f (&y)[FN][2
         for (int i = 0; i < FN; ++i) {
           const int64_t n = ch0 + 32 * i + lrow < N ? ch0 + 32 * i + lrow : N - 1;
           w[h][i] = lora_b8<AT>(bb + n * l.rank, r0 + 16 * h + 8 * kg, rank, vec);
+        }
+      }
+      // a value that is not finite would spoil the tile's rows of other
+      // adapters (0 * inf): left out here, and its own rows become NaN below
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+          const uint32_t bad = not_finite<AT>(w[h][i]);
+          if (__any(bad != 0)) {
+            if (bad) w[h][i] = zero;
+            odd |= bad ? 1u << i : 0u;
+          }
         }
       }
 #pragma unroll
@@ -135,6 +161,22 @@ __device__ __forceinline__ void lora_add(const LoraArgs& l, lora_v16f (&y)[FN][2
               }
         }
       }
+    }
+    if (__any(odd != 0)) {
+      odd |= __shfl_xor(odd, 32);
+      const uint32_t own[2] = {(uint32_t)mine >> (4 * kg), (uint32_t)(mine >> 32) >> (4 * kg)};
+      // a NaN's bits where the bit is set
+      auto nan_if = [](uint32_t bits, int at) { return (bits >> at & 1) * 0x7fc00000u; };
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float v = y[i][j][r];   // (a bit cast of a vector's element reads element 0)
+            const uint32_t nan = nan_if(odd, i) & nan_if(own[j], 8 * (r / 4) + r % 4);
+            y[i][j][r] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) | nan);
+          }
     }
   }
 }

@@ -144,6 +144,23 @@ def test_linear_lora_ranks_ids_and_optional_tensors(M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ad", ["fp16", "bf16"])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,N", [(40, 100), (200, 300), (2050, 4200)])
+def test_linear_lora_adapter_that_is_no_number_spoils_its_own_rows_only(M, N, out, ad):
+    c = make(M, 1024, N, 24, 4, scattered(M, 4, 9), ad, out, seed=8)
+    want = run(c)
+    own = c["ids"] == 2
+    c["b"][2, ::3, 5] = float("inf")
+    c["b"][2, 1, 20] = float("nan")
+    got = run(c)
+    assert torch.equal(got[~own], want[~own])
+    assert not torch.isfinite(got[own][:, ::3]).any() and torch.isfinite(got[own][:, 2::3]).all()
+    c["a"][2, 0, 7] = float("nan")
+    assert torch.equal(run(c)[~own], want[~own])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 40, 520])
 @pytest.mark.parametrize("zp", [-128, 127])
 def test_linear_lora_zero_points_and_far_adapters(M, zp):
