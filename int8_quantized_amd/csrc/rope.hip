@@ -236,11 +236,26 @@ hipError_t launch_type(const RopeArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t s) {
-  switch (a.dtype) {
-    case Q8TA_F32: return launch_type<float>(a, s);
-    case Q8TA_F16: return launch_type<Half>(a, s);
-    default: return launch_type<Bfloat>(a, s);
+  // a launch has fewer than 2^32 threads: one for each 2^22 tokens
+  const int64_t es = a.dtype == Q8TA_F32 ? 4 : 2;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += (int64_t)1 << 22) {
+    RopeArgs p = a;
+    p.tokens = a.tokens - t0 < (int64_t)1 << 22 ? a.tokens - t0 : (int64_t)1 << 22;
+    p.q = (const char*)a.q + t0 * a.q_ts * es;
+    p.k = (const char*)a.k + t0 * a.k_ts * es;
+    p.v = (const char*)a.v + t0 * a.v_ts * es;
+    p.q_out = (char*)a.q_out + t0 * a.heads * a.dim * es;
+    p.positions = a.positions + t0;
+    p.slots = a.slots + t0;
+    hipError_t e;
+    switch (a.dtype) {
+      case Q8TA_F32: e = launch_type<float>(p, s); break;
+      case Q8TA_F16: e = launch_type<Half>(p, s); break;
+      default: e = launch_type<Bfloat>(p, s);
+    }
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 }  // namespace q8ta

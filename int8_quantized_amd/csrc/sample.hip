@@ -127,7 +127,8 @@ __device__ void sample_any(const SampleArgs& a, Shared& sh, float mx) {
   const T* row = (const T*)a.logits + (int64_t)blockIdx.x * a.row_stride;
   const float temp = a.temperature[blockIdx.x];
   const int k = a.top_k ? a.top_k[blockIdx.x] : 0;
-  const float p = a.top_p ? a.top_p[blockIdx.x] : 1.0f;
+  const float given_p = a.top_p ? a.top_p[blockIdx.x] : 1.0f;
+  const float p = given_p > 0.0f ? given_p : 0.0f;   // (a NaN keeps the first token alone, as 0 does)
   const float mp = a.min_p ? a.min_p[blockIdx.x] : 0.0f;
   const bool greedy = !(temp > 0.0f);
   const uint32_t top_key = key_of(mx);

@@ -130,6 +130,17 @@ def test_sample_top_p_border_on_equal_weights():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V", [64, 20000, (1 << 19) + 5])
+def test_sample_settings_that_are_no_numbers(V):
+    """A NaN keeps the first token alone: no sum is below it, no weight reaches it."""
+    x, g = rows(4, V, V)
+    nan = np.nan
+    _, tokens, lp = run(x, [1.0, 1.0, nan, 1.0], [0, 5000, 0, 20], [nan, nan, 0.9, 0.9], [0.0, 0.0, 0.0, nan],
+                        g.random(4))
+    assert (tokens == x.astype(np.float32).argmax(1)).all() and (lp == 0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("V", [64, 20000])
 def test_sample_masked_logits(V):
     B = len(SETTINGS)
