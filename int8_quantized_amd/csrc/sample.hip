@@ -3,18 +3,20 @@
 //
 // The kept tokens are a prefix of the row in the order of falling logits
 // (equal ones by index), so they are given by a border, and no sort of the row is
-// needed to find it.  One workgroup of 16 waves a row:
-//  * The largest logit, and each thread's own (first reading of the row).
-//  * Where the prefix is short -- top-k up to 1024, or min-p -- the few tokens that
-//    can be in it are collected (second reading): with top-k those at or above
-//    a bound that k of the threads' own largest logits reach, with min-p those
-//    of about its weight.  They are sorted in LDS, cut exactly in that order,
-//    sorted by index and drawn from.
-//  * Top-p over the whole vocabulary sums weights into bins of 1/64 of a
-//    power of two, finds the bin in which the border lies, and collects, sorts
-//    and cuts the tokens of that bin alone.
-//  * There the token is found in the vocabulary's order by sums over stretches
-//    of 64 lanes' elements (third reading), then inside one stretch.
+// needed to find it.  Four short launches, the first three with as many
+// workgroups a row as fill the card:
+//  1. k_sample_max: the largest logit of each group of up to 64 neighbouring
+//     loads.  Later readings skip the groups whose largest cannot matter.
+//  2. k_sample_gather: where the prefix is short -- top-k up to 1024, or min-p --
+//     the few tokens that can be in it: with top-k those at or above a bound that
+//     k of the groups reach, with min-p those of about its weight.  With top-p
+//     over the whole vocabulary, sums of weights in bins of 1/32 of a power of
+//     two; with no filter, sums over stretches of 64 loads.
+//  3. k_sample_border (top-p over the whole vocabulary): the bin in which the
+//     border lies, its tokens, and the sums over stretches of those above it.
+//  4. k_sample_pick, a workgroup a row: the collected tokens are sorted in LDS,
+//     cut exactly in that order and drawn from in the order of their indices; with
+//     sums over stretches the stretch is found, then the token inside it.
 //  * What these do not take (more than 4096 tokens tied or collected, top-k
 //    beyond 1024, a border below 2^-32 of the largest weight) goes the slow way:
 //    selection digit by digit of the key (the logit's bits in an
@@ -366,21 +368,23 @@ __device__ void sample_any(const SampleArgs& a, Shared& sh, float mx) {
   }
 }
 
-// Largest logit of a block's values, in every thread.
-__device__ __forceinline__ float block_max(float v, Shared& sh) {
+// Largest of a block's values, in every thread.
+template <int NW>
+__device__ __forceinline__ float block_max(float v, float (&tops)[kWaves]) {
 #pragma unroll
   for (int m = 32; m > 0; m /= 2) v = __builtin_fmaxf(v, __shfl_xor(v, m));
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh.tops[threadIdx.x >> 6] = v;
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = sh.tops[0];
+  v = tops[0];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) v = __builtin_fmaxf(v, sh.tops[w]);
+  for (int w = 1; w < NW; ++w) v = __builtin_fmaxf(v, tops[w]);
   return v;
 }
 
 // Sum of v over the threads before this one, and over all.
-__device__ __forceinline__ u64 block_scan(u64 v, Shared& sh, u64& all) {
+template <int NW>
+__device__ __forceinline__ u64 block_scan(u64 v, u64 (&sums)[kWaves], u64& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   u64 sum = v;
 #pragma unroll
@@ -389,377 +393,649 @@ __device__ __forceinline__ u64 block_scan(u64 v, Shared& sh, u64& all) {
     if (lane >= m) sum += o;
   }
   __syncthreads();
-  if (lane == 63) sh.sums[wave] = sum;
+  if (lane == 63) sums[wave] = sum;
   __syncthreads();
   u64 before = 0;
   all = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? sh.sums[w] : 0;
-    all += sh.sums[w];
+  for (int w = 0; w < NW; ++w) {
+    before += w < wave ? sums[w] : 0;
+    all += sums[w];
   }
   return before + sum - v;
 }
 
-// Falling order of n keys (a power of two of them, zeros behind the real ones).
-__device__ __forceinline__ void sort_down(u64* key, int n) {
-  for (int size = 2; size <= n; size *= 2)
-    for (int step = size / 2; step > 0; step /= 2) {
+constexpr int kCand = 4096;     // tokens that can be collected
+constexpr int kBins = 1024;     // weight bins, 32 to a power of two
+constexpr int kGroups = 4096;   // groups of loads, at most
+constexpr int kSteps = 1024;    // steps between the groups' largest logits
+constexpr int kBT = 256;        // threads of a part of a row
+constexpr int kParts = 32;      // parts of a row, at most
+
+// One 16-byte load of neighbouring elements, the load `at` of the row.  The
+// row's last one ends with it: what it shares with the one before, and every
+// element of a load that is not wanted, is -inf.
+template <class T>
+struct Vec {
+  static constexpr int N = 16 / sizeof(T);
+  typedef uint32_t raw_t __attribute__((ext_vector_type(4)));
+  raw_t raw;
+  int first;   // token of x[0]
+  float x[N];
+  // unconditional, so that several are in flight
+  __device__ __forceinline__ void fetch(const T* row, int at, bool wanted, int V) {
+    first = wanted ? at * N : 0;
+    first = first < V - N ? first : V - N;
+    if (first < 0) {   // V < N, every lane alike
+      first = 0;
+      raw = raw_t{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (e >= V) break;
+        if constexpr (sizeof(T) == 4) raw[e] = __builtin_bit_cast(uint32_t, to_float(row[e]));
+        else raw[e / 2] |= (uint32_t)row[e].bits << (16 * (e % 2));
+      }
+    } else {
+      __builtin_memcpy(&raw, row + first, 16);   // rows start anywhere
+    }
+  }
+  __device__ __forceinline__ void finish(int at, bool wanted, int V) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const uint32_t w = raw[e * sizeof(T) / 4];
+      float y;
+      if constexpr (sizeof(T) == 4) y = __builtin_bit_cast(float, w);
+      else y = to_float(T{(uint16_t)(w >> (16 * (e % 2)))});
+      x[e] = wanted && first + e >= at * N && first + e < V && y == y ? y : -INFINITY;
+    }
+  }
+};
+
+// How a row is divided, and its share of the workspace.
+struct Plan {
+  int loads;       // 16-byte loads of a row
+  int group_log;   // log2 of the loads of a group
+  int groups;
+  int per, parts;  // loads of a thread of a part; parts of a row
+  int stretches;   // of 64 loads
+  // bytes from a row's share to ...
+  int at_max, at_sums, at_bins, at_cand, row_bytes;
+  char* ws;
+};
+struct State {
+  int first;       // the first token of the largest logit
+  int n_cand;      // tokens collected
+  int cut_bin;
+  float mx;
+  u64 base;        // weight above the cut bin
+  double goal;     // top-p's share of all weights
+  u64 totals[kParts];
+};
+template <class P>
+__device__ __forceinline__ P* share(const Plan& p, int row, int at) {
+  return (P*)(p.ws + (int64_t)row * p.row_bytes + at);
+}
+
+enum Mode { kFirst, kFewK, kMinP, kTopP, kAll, kSlow };
+struct Settings {
+  float temp, p, mp;
+  int k;
+  Mode mode;
+  bool cut_p, cut_m;
+};
+__device__ __forceinline__ Settings settings_of(const SampleArgs& a, int row) {
+  Settings s;
+  s.temp = a.temperature[row];
+  s.k = a.top_k ? a.top_k[row] : 0;
+  s.p = a.top_p ? a.top_p[row] : 1.0f;
+  s.mp = a.min_p ? a.min_p[row] : 0.0f;
+  s.cut_p = s.p < 1.0f;
+  s.cut_m = s.mp > 0.0f;
+  if (!(s.temp > 0.0f) || !(1.0f >= s.mp) || s.k == 1 || !(s.p > 0.0f)) s.mode = kFirst;
+  else if (s.k > 0 && s.k < a.vocab) s.mode = s.k <= kSteps ? kFewK : kSlow;
+  else s.mode = s.cut_m ? kMinP : (s.cut_p ? kTopP : kAll);
+  return s;
+}
+
+__device__ __forceinline__ u64 place_of(float x, int token) {   // falls as the definition's order goes on
+  return (u64)key_of(x) << 32 | (uint32_t)~(uint32_t)token;
+}
+__device__ __forceinline__ float value_of(u64 place) {
+  const uint32_t key = (uint32_t)(place >> 32);
+  return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+__device__ __forceinline__ int token_of(u64 place) { return (int)~(uint32_t)place; }   // its low word
+
+struct BinOf {
+  float mx, per_bin;
+  __device__ __forceinline__ int operator()(float x) const {
+    const float at = (mx - x) * per_bin;   // inf * 0 and inf - inf: NaN, the last bin
+    return x == mx ? 0 : (at < (float)(kBins - 1) ? (int)at : kBins - 1);
+  }
+};
+__device__ __forceinline__ BinOf bins_of(const Row& r, float mx) {
+  return BinOf{mx, (float)(r.scale * (kBins / 32))};
+}
+
+// f(load of the row, its values) for n loads, load_at(i) the i-th of this thread
+// (-1: none, values of -inf), four in flight; every lane takes part in every one.
+template <class T, class L, class F>
+__device__ __forceinline__ void each_of(const SampleArgs& a, const T* row, int n, L&& load_at, F&& f) {
+  for (int i = 0; i < n; i += 4) {
+    Vec<T> v[4];
+    int at[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      at[u] = i + u < n ? load_at(i + u) : -1;
+      v[u].fetch(row, at[u], at[u] >= 0, a.vocab);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[u].finish(at[u], at[u] >= 0, a.vocab);
+      if (i + u < n) f(at[u], v[u]);
+    }
+  }
+}
+// All loads of a part, in the row's order; the first of a wave's is a multiple of 64.
+template <class T, class F>
+__device__ __forceinline__ void each_load(const SampleArgs& a, const Plan& p, const T* row, F&& f) {
+  const int first = blockIdx.x * p.per * kBT + threadIdx.x;
+  each_of(a, row, p.per, [&](int i) { return first + i * kBT < p.loads ? first + i * kBT : -1; }, f);
+}
+// The loads of the listed groups, in any order.
+template <class T, class F>
+__device__ __forceinline__ void each_listed(const SampleArgs& a, const Plan& p, const T* row, const uint16_t* list,
+                                            int n, F&& f) {
+  const int all = n << p.group_log;
+  each_of(a, row, (all + kBT - 1) / kBT,
+          [&](int i) {
+            const int q = i * kBT + (int)threadIdx.x;
+            if (q >= all) return -1;
+            const int at = ((int)list[q >> p.group_log] << p.group_log) + (q & ((1 << p.group_log) - 1));
+            return at < p.loads ? at : -1;
+          },
+          f);
+}
+
+template <class T>
+__global__ __launch_bounds__(kBT) void k_sample_max(SampleArgs a, Plan p) {
+  const int row = blockIdx.y;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    State* st = share<State>(p, row, 0);
+    st->first = a.vocab;
+    st->n_cand = 0;
+    st->cut_bin = -1;
+    st->mx = -INFINITY;
+  }
+  float* tops = share<float>(p, row, p.at_max);
+  const int g = 1 << p.group_log;
+  each_load(a, p, (const T*)a.logits + (int64_t)row * a.row_stride, [&](int at, const Vec<T>& v) {
+    float m = v.x[0];
+#pragma unroll
+    for (int e = 1; e < Vec<T>::N; ++e) m = __builtin_fmaxf(m, v.x[e]);
+    for (int x = 1; x < g; x *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, x));
+    if (at >= 0 && at % g == 0) tops[at >> p.group_log] = m;
+  });
+}
+
+// Tokens that a part of a row collects, handed on at once.
+struct Collected {
+  u64 place[kCand];
+  int n, base;
+};
+__device__ __forceinline__ void append(Collected& c, float x, int token) {
+  const int to = atomicAdd(&c.n, 1);
+  if (to < kCand) c.place[to] = place_of(x, token);
+}
+__device__ __forceinline__ void hand_on(Collected& c, State* st, u64* cand) {
+  __syncthreads();
+  const int n = c.n;
+  if (n == 0) return;
+  if (threadIdx.x == 0) c.base = atomicAdd(&st->n_cand, n);   // (beyond kCand: the slow way)
+  __syncthreads();
+  const int base = c.base;
+  for (int i = threadIdx.x; i < n && i < kCand; i += kBT)
+    if (base + i < kCand) cand[base + i] = c.place[i];
+}
+
+template <class T>
+__global__ __launch_bounds__(kBT) void k_sample_gather(SampleArgs a, Plan p) {
+  constexpr int N = Vec<T>::N, NW = kBT / 64;
+  __shared__ union {
+    Collected c;
+    u64 bins[kBins];
+  } sh;
+  __shared__ int steps[kSteps];
+  __shared__ uint16_t list[kGroups];
+  __shared__ int n_list;
+  __shared__ u64 sums[kWaves];
+  __shared__ float tops[kWaves];
+  __shared__ int sh_last;
+  const int tid = threadIdx.x, lane = tid & 63, row = blockIdx.y;
+  const T* logits = (const T*)a.logits + (int64_t)row * a.row_stride;
+  const float* group = share<float>(p, row, p.at_max);
+  State* st = share<State>(p, row, 0);
+  u64* cand = share<u64>(p, row, p.at_cand);
+  float g[kGroups / kBT], mine = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kGroups / kBT; ++i) {
+    const int at = tid + i * kBT;
+    g[i] = at < p.groups ? group[at] : -INFINITY;
+    mine = __builtin_fmaxf(mine, g[i]);
+  }
+  const Settings s = settings_of(a, row);
+  if (tid == 0) {
+    sh.c.n = 0;
+    n_list = 0;
+  }
+  const float mx = block_max<NW>(mine, tops);
+  if (blockIdx.x == 0 && tid == 0) st->mx = mx;
+  if (mx == -INFINITY || s.mode == kSlow) return;
+  const Row r = make_row(mx, s.temp, a.shift);
+  // the groups of this part whose largest logit passes, listed
+  const int g0 = (blockIdx.x * p.per * kBT) >> p.group_log;
+  const int g1 = ((blockIdx.x + 1) * p.per * kBT) >> p.group_log;
+  auto list_groups = [&](auto&& passes) {
+#pragma unroll
+    for (int i = 0; i < kGroups / kBT; ++i) {
+      const int at = tid + i * kBT;
+      if (at >= g0 && at < g1 && at < p.groups && passes(g[i])) list[atomicAdd(&n_list, 1)] = (uint16_t)at;
+    }
+    __syncthreads();
+    return n_list;
+  };
+
+  if (s.mode == kFirst) {
+    const int n = list_groups([&](float x) { return x == mx; });
+    each_listed(a, p, logits, list, n, [&](int, const Vec<T>& v) {
+      int first = a.vocab;
+#pragma unroll
+      for (int e = N - 1; e >= 0; --e) first = v.x[e] == mx ? v.first + e : first;
+      if (first < a.vocab) atomicMin(&st->first, first);
+    });
+  } else if (s.mode == kFewK) {
+    // a bound that k groups' largest logits reach: their places between the
+    // smallest finite one and the row's, in steps
+#pragma unroll
+    for (int i = 0; i < kSteps / kBT; ++i) steps[tid + i * kBT] = 0;
+    if (tid == 0) sh_last = -1;
+    float least = INFINITY;
+#pragma unroll
+    for (int i = 0; i < kGroups / kBT; ++i) least = __builtin_fminf(least, g[i] == -INFINITY ? INFINITY : g[i]);
+    const float low = -block_max<NW>(-least, tops);
+    const float unit = mx > low ? (float)(kSteps - 1) / (mx - low) : 0.0f;
+    auto step_of = [&](float x) {   // (fmax: 0 for the NaN of infinite logits)
+      return (int)__builtin_fminf(__builtin_fmaxf((mx - x) * unit, 0.0f), (float)(kSteps - 1));
+    };
+#pragma unroll
+    for (int i = 0; i < kGroups / kBT; ++i)
+      if (g[i] != -INFINITY) atomicAdd(&steps[step_of(g[i])], 1);
+    __syncthreads();
+    constexpr int C = kSteps / kBT;
+    int n[C], sum = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      n[c] = steps[C * tid + c];
+      sum += n[c];
+    }
+    u64 all;
+    int before = (int)block_scan<NW>((u64)sum, sums, all);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (before < s.k && before + n[c] >= s.k) sh_last = C * tid + c;
+      before += n[c];
+    }
+    __syncthreads();
+    const int last = sh_last;   // -1: fewer than k groups have a finite logit
+    auto in = [&](float x) { return x != -INFINITY && (last < 0 || (x >= low && step_of(x) <= last)); };
+    const int n_groups = list_groups(in);
+    each_listed(a, p, logits, list, n_groups, [&](int, const Vec<T>& v) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (in(v.x[e])) append(sh.c, v.x[e], v.first + e);
+    });
+    hand_on(sh.c, st, cand);
+  } else if (s.mode == kMinP) {
+    // a margin of 0.1 % for the 32-bit test; the weights decide later
+    const float far = (float)(log((double)s.mp) / r.inv_t) * 1.001f - 1e-30f;
+    auto in = [&](float x) { return x != -INFINITY && (x - mx >= far || x == mx); };
+    u64 sum = 0;   // of all weights, where top-p needs it
+    if (s.cut_p) {
+      each_load(a, p, logits, [&](int, const Vec<T>& v) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          sum += units(r, weight(r, v.x[e]));
+          if (in(v.x[e])) append(sh.c, v.x[e], v.first + e);
+        }
+      });
+    } else {
+      const int n = list_groups(in);
+      each_listed(a, p, logits, list, n, [&](int, const Vec<T>& v) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (in(v.x[e])) append(sh.c, v.x[e], v.first + e);
+      });
+    }
+    u64 all;
+    block_scan<NW>(sum, sums, all);
+    if (tid == 0) st->totals[blockIdx.x] = all;
+    hand_on(sh.c, st, cand);
+  } else if (s.mode == kTopP) {
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kBT) sh.bins[i] = 0;
+    __syncthreads();
+    const BinOf bin = bins_of(r, mx);
+    each_load(a, p, logits, [&](int, const Vec<T>& v) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const u64 w = units(r, weight(r, v.x[e]));
+        if (w > 0) atomicAdd(&sh.bins[bin(v.x[e])], w);
+      }
+    });
+    __syncthreads();
+    u64* out = share<u64>(p, row, p.at_bins) + blockIdx.x * kBins;
+    for (int i = tid; i < kBins; i += kBT) out[i] = sh.bins[i];
+  } else {
+    u64* out = share<u64>(p, row, p.at_sums);
+    each_load(a, p, logits, [&](int at, const Vec<T>& v) {
+      u64 sum = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum += units(r, weight(r, v.x[e]));
+      sum = wave_sum(sum);
+      if (lane == 0 && at >= 0) out[at / 64] = sum;
+    });
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kBT) void k_sample_border(SampleArgs a, Plan p) {
+  constexpr int N = Vec<T>::N, NW = kBT / 64, C = kBins / kBT;
+  __shared__ Collected c;
+  __shared__ u64 sums[kWaves];
+  __shared__ int sh_bin;
+  __shared__ u64 sh_base;
+  const int tid = threadIdx.x, lane = tid & 63, row = blockIdx.y;
+  const Settings s = settings_of(a, row);
+  State* st = share<State>(p, row, 0);
+  const float mx = st->mx;
+  if (s.mode != kTopP || mx == -INFINITY) return;
+  const Row r = make_row(mx, s.temp, a.shift);
+  const u64* bins = share<u64>(p, row, p.at_bins);
+  u64 n[C] = {}, sum = 0;
+#pragma unroll 8
+  for (int part = 0; part < p.parts; ++part)
+#pragma unroll
+    for (int i = 0; i < C; ++i) n[i] += bins[part * kBins + C * tid + i];
+#pragma unroll
+  for (int i = 0; i < C; ++i) sum += n[i];
+  if (tid == 0) c.n = 0;
+  u64 all;
+  u64 before = block_scan<NW>(sum, sums, all);
+  const double goal = (double)s.p * (double)all;
+  // the bin in which the running sum reaches the goal
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if (n[i] > 0 && (double)before < goal && !((double)(before + n[i]) < goal)) {
+      sh_bin = C * tid + i;
+      sh_base = before;
+    }
+    before += n[i];
+  }
+  __syncthreads();
+  const int cut = sh_bin;
+  if (blockIdx.x == 0 && tid == 0) {
+    st->cut_bin = cut;
+    st->base = sh_base;
+    st->goal = goal;
+  }
+  if (cut >= kBins - 1) return;
+  const BinOf bin = bins_of(r, mx);
+  u64* out = share<u64>(p, row, p.at_sums);
+  each_load(a, p, (const T*)a.logits + (int64_t)row * a.row_stride, [&](int at, const Vec<T>& v) {
+    u64 w = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int b = v.x[e] == -INFINITY ? kBins : bin(v.x[e]);
+      if (b < cut) w += units(r, weight(r, v.x[e]));
+      if (b == cut) append(c, v.x[e], v.first + e);
+    }
+    w = wave_sum(w);
+    if (lane == 0 && at >= 0) out[at / 64] = w;
+  });
+  hand_on(c, st, share<u64>(p, row, p.at_cand));
+}
+
+// Falling order of n different places.
+__device__ __forceinline__ void sort_down(u64* place, int n) {
+  if (n <= kNT) {   // each one's rank, counted by as many threads as there are to a place
+    int share_log = 0;
+    while (share_log < 5 && n << (share_log + 1) <= kNT) ++share_log;
+    const int per = 1 << share_log;
+    __syncthreads();
+    const int i = threadIdx.x >> share_log;
+    const u64 mine = i < n ? place[i] : 0;
+    int rank = 0;
+    if (i < n) {
+#pragma unroll 4
+      for (int j = threadIdx.x & (per - 1); j < n; j += per) rank += place[j] > mine;
+    }
+    for (int x = 1; x < per; x *= 2) rank += __shfl_xor(rank, x);
+    __syncthreads();
+    if (i < n && (threadIdx.x & (per - 1)) == 0) place[rank] = mine;
+    __syncthreads();
+    return;
+  }
+  int size = 64;
+  while (size < n) size *= 2;
+  __syncthreads();
+  for (int i = n + threadIdx.x; i < size; i += kNT) place[i] = 0;
+  for (int run = 2; run <= size; run *= 2)
+    for (int step = run / 2; step > 0; step /= 2) {
       __syncthreads();
-      for (int i = threadIdx.x; i < n / 2; i += kNT) {
+      for (int i = threadIdx.x; i < size / 2; i += kNT) {
         const int at = 2 * i - (i & (step - 1)), to = at + step;
-        const u64 x = key[at], y = key[to];
-        if ((x < y) == ((at & size) == 0)) {
-          key[at] = y;
-          key[to] = x;
+        const u64 x = place[at], y = place[to];
+        if ((x < y) == ((at & run) == 0)) {
+          place[at] = y;
+          place[to] = x;
         }
       }
     }
   __syncthreads();
 }
 
-constexpr int kCand = 4096;       // tokens that can be collected
-constexpr int kBins = 2048;       // weight bins, 64 to a power of two
-constexpr int kMaxRounds = 128;   // rounds of 1024 16-byte loads (vocab up to 2^19 fp32, 2^20 16-bit)
-
-// One 16-byte load of elements, or fewer at the row's end (-inf behind it).
 template <class T>
-struct Vec {
-  static constexpr int N = 16 / sizeof(T);
-  float x[N];
-  __device__ __forceinline__ void load(const T* row, int64_t at, int V) {
-    typedef uint32_t raw_t __attribute__((ext_vector_type(4)));
-    raw_t raw;
-    if (at + N <= V) {
-      __builtin_memcpy(&raw, row + at, 16);   // rows start anywhere
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const uint32_t w = raw[e * sizeof(T) / 4];
-        if constexpr (sizeof(T) == 4) x[e] = __builtin_bit_cast(float, w);
-        else x[e] = to_float(T{(uint16_t)(w >> (16 * (e % 2)))});
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) x[e] = at + e < V ? to_float(row[at + e]) : -INFINITY;
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = x[e] != x[e] ? -INFINITY : x[e];
-  }
-};
-
-template <class T>
-__global__ __launch_bounds__(kNT) void k_sample(SampleArgs a) {
+__global__ __launch_bounds__(kNT) void k_sample_pick(SampleArgs a, Plan p) {
   constexpr int N = Vec<T>::N;
   __shared__ Shared sh;
-  __shared__ u64 cand[kCand];     // key << 32 | ~index, falling: the order of the definition
-  __shared__ u64 wts[kCand];      // their weights; before that, the bins
-  __shared__ int n_cand, sh_bin, sh_first;
+  __shared__ u64 cand[kCand];
+  __shared__ u64 wts[kCand];   // weights of the collected, or sums of the stretches
+  __shared__ int sh_first;
   __shared__ u64 sh_base;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int V = a.vocab;
-  const T* row = (const T*)a.logits + (int64_t)blockIdx.x * a.row_stride;
-  const int rounds = (V + kNT * N - 1) / (kNT * N);
-  // f(first element of the load, its N values, round) for every load of the
-  // row, four in flight; every lane takes part in every one
-  auto each = [&](auto&& f) {
-    for (int i = 0; i < rounds; i += 4) {
-      Vec<T> v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u].load(row, ((int64_t)(i + u) * kNT + tid) * N, V);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u < rounds) f(((i + u) * kNT + tid) * N, v[u], i + u);
-    }
-  };
-
-  const float temp = a.temperature[blockIdx.x];
-  const int k = a.top_k ? a.top_k[blockIdx.x] : 0;
-  const float p = a.top_p ? a.top_p[blockIdx.x] : 1.0f;
-  const float mp = a.min_p ? a.min_p[blockIdx.x] : 0.0f;
-  const double u = (double)a.u[blockIdx.x];
-  if (tid == 0) {
-    n_cand = 0;
-    sh_first = V;
-  }
-  float mine = -INFINITY;
-  each([&](int, const Vec<T>& v, int) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) mine = __builtin_fmaxf(mine, v.x[e]);
-  });
-  const float mx = block_max(mine, sh);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, row = blockIdx.x;
+  const T* logits = (const T*)a.logits + (int64_t)row * a.row_stride;
+  const State* st = share<State>(p, row, 0);
+  const Settings s = settings_of(a, row);
+  const float mx = st->mx;
+  const int n_cand = st->n_cand;
+  const double u = (double)a.u[row];
   auto put = [&](int token, float logprob) {
-    a.tokens[blockIdx.x] = token;
-    if (a.logprobs) a.logprobs[blockIdx.x] = logprob;
+    a.tokens[row] = token;
+    if (a.logprobs) a.logprobs[row] = logprob;
   };
   if (mx == -INFINITY) {
     if (tid == 0) put(-1, -INFINITY);
     return;
   }
-  if (!(temp > 0.0f) || !(1.0f >= mp) || k == 1 || !(p > 0.0f)) {
-    // the first token alone
-    each([&](int at, const Vec<T>& v, int) {
-      int first = V;
-#pragma unroll
-      for (int e = N - 1; e >= 0; --e) first = v.x[e] == mx ? at + e : first;
-      if (first < V) atomicMin(&sh_first, first);
-    });
-    __syncthreads();
-    if (tid == 0) put(sh_first, 0.0f);
+  if (s.mode == kFirst) {
+    if (tid == 0) put(st->first, 0.0f);
     return;
   }
-  const Row r = make_row(mx, temp, a.shift);
-  const bool few_k = k > 0 && k < V && k <= 1024, all_k = k <= 0 || k >= V;
-  const bool cut_p = p < 1.0f, cut_m = mp > 0.0f;
-  if (!few_k && !all_k) {
+  if (s.mode == kSlow || n_cand > kCand || (s.mode == kTopP && st->cut_bin >= kBins - 1)) {
     sample_any<T>(a, sh, mx);
     return;
   }
+  const Row r = make_row(mx, s.temp, a.shift);
   auto log_prob = [&](float x, u64 all) {
     const double z = (double)x == r.top ? 0.0 : ((double)x - r.top) * r.inv_t;
     return (float)(z - log((double)all / r.one));
   };
-  auto value_of = [](uint32_t key) {
-    return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7fffffffu : ~key);
-  };
-  // Collects the tokens for which in(x) holds; false where they are too many.
-  auto collect = [&](auto&& in) {
-    each([&](int at, const Vec<T>& v, int) {
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (in(v.x[e])) {
-          const int to = atomicAdd(&n_cand, 1);
-          if (to < kCand) cand[to] = (u64)key_of(v.x[e]) << 32 | (uint32_t)~(uint32_t)(at + e);
-        }
-    });
-    __syncthreads();
-    return n_cand <= kCand;
-  };
-  auto pad_and_sort = [&](int n) {
-    int size = 64;
-    while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kNT) cand[i] = 0;
-    sort_down(cand, size);
-  };
+  constexpr int C = kCand / kNT;
+  u64 w[C], sum = 0, all;
+  int n = n_cand;
+  if (s.mode != kAll) {
+    const u64* from = share<u64>(p, row, p.at_cand);
+    for (int i = tid; i < n; i += kNT) cand[i] = from[i];
+    sort_down(cand, n);
+  }
 
-  if (few_k || cut_m) {
-    u64 total = 0;   // of all weights, where top-p needs it and top-k does not bound it
-    bool ok;
-    if (few_k) {
-      // a bound that k threads' own largest logits reach: their places between
-      // the smallest finite one and the row's, in 1024 steps
-      int* steps = reinterpret_cast<int*>(wts);
-      steps[tid] = 0;
-      if (tid == 0) sh_bin = -1;
-      const float low = -block_max(mine == -INFINITY ? -INFINITY : -mine, sh);
-      const float unit = mx > low ? 1023.0f / (mx - low) : 0.0f;
-      auto step_of = [&](float x) {   // (fmax: 0 for the NaN of infinite logits)
-        return (int)__builtin_fminf(__builtin_fmaxf((mx - x) * unit, 0.0f), 1023.0f);
-      };
-      if (mine != -INFINITY) atomicAdd(&steps[step_of(mine)], 1);
-      __syncthreads();
-      u64 all;
-      const u64 before = block_scan((u64)steps[tid], sh, all);
-      if (before < (u64)k && before + steps[tid] >= (u64)k) sh_bin = tid;
-      __syncthreads();
-      const int last = sh_bin;   // -1: fewer than k threads have a finite logit
-      __syncthreads();
-      ok = collect([&](float x) {
-        return x != -INFINITY && (last < 0 || (x >= low && step_of(x) <= last));
-      });
-    } else {
-      if (cut_p) {
-        u64 sum = 0;
-        each([&](int, const Vec<T>& v, int) {
+  if (s.mode == kFewK || s.mode == kMinP) {
+    u64 total = 0;   // of all weights, where top-k does not bound them
+    if (s.mode == kFewK) n = n < s.k ? n : s.k;
+    else if (s.cut_p) for (int i = 0; i < p.parts; ++i) total += st->totals[i];
+    if (n <= 64) {   // a lane each
+      if (wave != 0) return;
+      const u64 mine = lane < n ? cand[lane] : 0;
+      const double wd = lane < n ? weight(r, value_of(mine)) : 0.0;
+      const u64 w1 = units(r, wd);
+      u64 upto = w1;
 #pragma unroll
-          for (int e = 0; e < N; ++e) sum += units(r, weight(r, v.x[e]));
-        });
-        block_scan(sum, sh, total);
+      for (int m = 1; m < 64; m *= 2) {
+        const u64 o = __shfl_up(upto, m);
+        if (lane >= m) upto += o;
       }
-      // a margin of 0.1 % for the 32-bit test; the weights decide below
-      const float far = (float)(log((double)mp) / r.inv_t) * 1.001f - 1e-30f;
-      ok = collect([&](float x) { return x - mx >= far || x == mx; });
-    }
-    if (!ok) {
-      sample_any<T>(a, sh, mx);
+      const double goal = (double)s.p * (double)(s.mode == kFewK ? __shfl(upto, 63) : total);
+      const bool in = lane < n && (lane == 0 || ((!s.cut_p || (double)(upto - w1) < goal) &&
+                                                 (!s.cut_m || wd >= (double)s.mp)));
+      const int m = __popcll(__ballot(in));
+      all = __shfl(upto, m - 1);
+      const double reach = u * (double)all;
+      // in the order of the indices: the sum of the kept ones of no larger index
+      const uint32_t low = (uint32_t)mine;
+      wts[lane] = w1;
+      __builtin_amdgcn_wave_barrier();
+      u64 run = 0;
+      for (int j = 0; j < m; ++j) run += (uint32_t)cand[j] >= low ? wts[j] : 0;
+      if (in && w1 > 0 && ((double)run > reach ? !((double)(run - w1) > reach) : run == all))
+        put(token_of(mine), log_prob(value_of(mine), all));
       return;
     }
-    int n = n_cand;
-    pad_and_sort(n);
-    if (few_k && n > k) n = k;
     // weights in that order, four neighbours a thread; the prefix that stays
-    constexpr int C = kCand / kNT;
-    u64 w[C], sum = 0;
     double wd[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = C * tid + c;
-      wd[c] = j < n ? weight(r, value_of((uint32_t)(cand[j] >> 32))) : 0.0;
+      wd[c] = j < n ? weight(r, value_of(cand[j])) : 0.0;
       w[c] = units(r, wd[c]);
       sum += w[c];
     }
-    u64 all;
-    u64 before = block_scan(sum, sh, all);
-    const double goal = (double)p * (double)(few_k ? all : total);
-    int kept = 0;
+    u64 before = block_scan<kWaves>(sum, sh.sums, all);
+    const double goal = (double)s.p * (double)(s.mode == kFewK ? all : total);
+    u64 kept = 0;   // kept tokens
     sum = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = C * tid + c;
-      const bool in = j < n && (j == 0 || ((!cut_p || (double)before < goal) && (!cut_m || wd[c] >= (double)mp)));
+      const bool in = j < n && (j == 0 || ((!s.cut_p || (double)before < goal) && (!s.cut_m || wd[c] >= (double)s.mp)));
       before += w[c];
       kept += in;
       if (in) sum += w[c];
-      if (j < kCand) wts[j] = w[c];
+      wts[j] = w[c];
     }
-    u64 n_kept, kept_sum;
-    block_scan((u64)kept, sh, n_kept);
-    block_scan(sum, sh, kept_sum);
-    // by index: ~index falls as the index grows; the place in the order above
-    // rides along
+    u64 n_kept;
+    block_scan<kWaves>(kept, sh.sums, n_kept);
+    block_scan<kWaves>(sum, sh.sums, all);
     const int m = (int)n_kept;
-    u64 by_index[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int j = C * tid + c;
-      by_index[c] = j < m ? (cand[j] << 32) | (uint32_t)j : 0;
-    }
-    // the keys of the kept, before their places are overwritten
-    __syncthreads();
-    uint32_t keys[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) keys[c] = C * tid + c < m ? (uint32_t)(cand[C * tid + c] >> 32) : 0;
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (C * tid + c < m) cand[C * tid + c] = by_index[c];
-    pad_and_sort(m);
-    sum = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int j = C * tid + c;
-      w[c] = j < m ? wts[(uint32_t)cand[j]] : 0;
-      sum += w[c];
-    }
-    before = block_scan(sum, sh, all);
     const double reach = u * (double)all;
-    // the first whose running sum passes u * all, else the last with a weight
-    if (tid == 0) sh_first = -1;
-    __syncthreads();
-    int hit = -1, some = -1;
+    // In the order of the indices, the first whose running sum passes u * all,
+    // else the last with a weight.
+    if (m > 1024) {
+      // sorted by index (low words fall as the index grows), places riding along
+      u64 by_index[C];
 #pragma unroll
-    for (int c = C - 1; c >= 0; --c) {
-      u64 upto = before;
+      for (int c = 0; c < C; ++c) by_index[c] = C * tid + c < m ? cand[C * tid + c] << 32 | (uint32_t)(C * tid + c) : 0;
+      __syncthreads();
 #pragma unroll
-      for (int d = 0; d <= c; ++d) upto += w[d];
-      if (w[c] > 0) {
-        some = some < 0 ? C * tid + c : some;
-        if ((double)upto > reach) hit = C * tid + c;
+      for (int c = 0; c < C; ++c)
+        if (C * tid + c < m) cand[C * tid + c] = by_index[c];
+      sort_down(cand, m);
+      sum = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        w[c] = C * tid + c < m ? wts[(uint32_t)cand[C * tid + c]] : 0;
+        sum += w[c];
       }
+      u64 upto = block_scan<kWaves>(sum, sh.sums, all);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        upto += w[c];
+        if (w[c] > 0 && ((double)upto > reach ? !((double)(upto - w[c]) > reach) : upto == all)) {
+          const int token = token_of(cand[C * tid + c] >> 32);
+          const float x = to_float(logits[token]);
+          put(token, log_prob(x, all));
+        }
+      }
+      return;
     }
-    // smallest hit: hits are kept as ~place so that the maximum is the first
-    if (hit >= 0) atomicMax(&sh_first, 0x40000000 + (kCand - hit));
-    else if (some >= 0) atomicMax(&sh_first, some);
-    __syncthreads();
-    const int found = sh_first;
-    const int place = found >= 0x40000000 ? kCand - (found - 0x40000000) : found;
-    const u64 chosen = cand[place];
-    const int j = (int)(uint32_t)chosen;
-    if (j / C == tid)
-      put((int)~(uint32_t)(chosen >> 32), log_prob(value_of(keys[j % C]), all));
+    // by its running sum, which is that of the kept tokens of no larger index
+    for (int i0 = 0; i0 < m; i0 += kNT / 2) {
+      const int i = i0 + tid / 2;
+      const uint32_t low = i < m ? (uint32_t)cand[i] : 0;
+      u64 upto = 0;
+      if (i < m)
+        for (int j = tid % 2; j < m; j += 2) upto += (uint32_t)cand[j] >= low ? wts[j] : 0;
+      upto += __shfl_xor(upto, 1);
+      const u64 mine = i < m ? wts[i] : 0;
+      if (tid % 2 == 0 && mine > 0 &&
+          ((double)upto > reach ? !((double)(upto - mine) > reach) : upto == all))
+        put(token_of(cand[i]), log_prob(value_of(cand[i]), all));
+    }
     return;
   }
 
-  // The whole vocabulary, cut by top-p at most.
-  int cut_bin = kBins;             // bins below it are kept
-  u64 border = 0;                  // of the cut bin: tokens of at least this key << 32 | ~index
-  const float per_bin = (float)(r.scale * 64.0);
-  auto bin_of = [&](float x) {
-    const float at = (mx - x) * per_bin;   // inf * 0 and inf - inf: NaN, the last bin
-    return x == mx ? 0 : (at < (float)(kBins - 1) ? (int)at : kBins - 1);
-  };
-  if (cut_p) {
-    u64* bins = wts;
-    for (int i = tid; i < kBins; i += kNT) bins[i] = 0;
-    __syncthreads();
-    each([&](int, const Vec<T>& v, int) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const u64 w = units(r, weight(r, v.x[e]));
-        if (w > 0) atomicAdd(&bins[bin_of(v.x[e])], w);
-      }
-    });
-    __syncthreads();
-    const u64 b0 = bins[2 * tid], b1 = bins[2 * tid + 1];
-    u64 all;
-    const u64 before = block_scan(b0 + b1, sh, all);
-    const double goal = (double)p * (double)all;
-    // the bin in which the running sum reaches the goal
-    if (b0 > 0 && (double)before < goal && !((double)(before + b0) < goal)) {
-      sh_bin = 2 * tid;
-      sh_base = before;
-    }
-    if (b1 > 0 && (double)(before + b0) < goal && !((double)(before + b0 + b1) < goal)) {
-      sh_bin = 2 * tid + 1;
-      sh_base = before + b0;
-    }
-    __syncthreads();
-    cut_bin = sh_bin;
-    const u64 base = sh_base;
-    if (cut_bin >= kBins - 1 || !collect([&](float x) { return x != -INFINITY && bin_of(x) == cut_bin; })) {
-      sample_any<T>(a, sh, mx);
-      return;
-    }
-    const int n = n_cand;
-    pad_and_sort(n);
-    constexpr int C = kCand / kNT;
-    u64 w[C], sum = 0;
+  // Sums over the stretches, in the vocabulary's order.
+  u64 border = 0;   // tokens of the cut bin at or before this place are kept
+  const int cut = s.mode == kTopP ? st->cut_bin : kBins;
+  int n_kept = 0;
+  if (s.mode == kTopP) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = C * tid + c;
-      w[c] = j < n ? units(r, weight(r, value_of((uint32_t)(cand[j] >> 32)))) : 0;
+      w[c] = j < n ? units(r, weight(r, value_of(cand[j]))) : 0;
       sum += w[c];
     }
     u64 in_bin;
-    u64 at = base + block_scan(sum, sh, in_bin);
-    int kept = 0;
+    u64 at = st->base + block_scan<kWaves>(sum, sh.sums, in_bin);
+    const double goal = st->goal;
+    u64 kept = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       kept += C * tid + c < n && (double)at < goal;
       at += w[c];
     }
-    u64 n_kept;
-    block_scan((u64)kept, sh, n_kept);
-    // at least one: the running sum before the bin is below the goal
-    border = cand[(int)n_kept - 1];
+    u64 some;
+    block_scan<kWaves>(kept, sh.sums, some);
+    n_kept = (int)some;   // at least one: the running sum before the bin is below the goal
+    border = cand[n_kept - 1];
+  }
+  const u64* from = share<u64>(p, row, p.at_sums);
+  for (int i = tid; i < kCand; i += kNT) wts[i] = i < p.stretches ? from[i] : 0;
+  __syncthreads();
+  if (s.mode == kTopP) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = C * tid + c;
+      if (j < n_kept && w[c] > 0) atomicAdd(&wts[token_of(cand[j]) / (64 * N)], w[c]);
+    }
     __syncthreads();
   }
-  auto kept = [&](float x, int i) {
-    if (!cut_p) return x != -INFINITY;
-    const int b = bin_of(x);
-    return x != -INFINITY &&
-           (b < cut_bin || (b == cut_bin && ((u64)key_of(x) << 32 | (uint32_t)~(uint32_t)i) >= border));
-  };
-  // sums of the stretches (a wave's loads of one round), in the vocabulary's order
-  u64* segs = wts;
-  for (int i = tid; i < kMaxRounds * kWaves; i += kNT) segs[i] = 0;
-  __syncthreads();
-  each([&](int at, const Vec<T>& v, int round) {
-    u64 s = 0;
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (kept(v.x[e], at + e)) s += units(r, weight(r, v.x[e]));
-    s = wave_sum(s);
-    if (lane == 0) segs[round * kWaves + wave] = s;
-  });
-  __syncthreads();
-  constexpr int C = kMaxRounds * kWaves / kNT;
-  u64 w[C], sum = 0, all;
+  sum = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    w[c] = segs[C * tid + c];
+    w[c] = wts[C * tid + c];
     sum += w[c];
   }
-  u64 before = block_scan(sum, sh, all);
+  u64 before = block_scan<kWaves>(sum, sh.sums, all);
   const double reach = u * (double)all;
   if (tid == 0) sh_first = -1;
   __syncthreads();
@@ -773,11 +1049,12 @@ __global__ __launch_bounds__(kNT) void k_sample(SampleArgs a) {
       if (hit < 0 && (double)upto > reach) hit = C * tid + c;
     }
   }
-  if (hit >= 0) atomicMax(&sh_first, 0x40000000 + (kMaxRounds * kWaves - hit));
+  // the first hit, else the last with a weight
+  if (hit >= 0) atomicMax(&sh_first, 0x40000000 + (kCand - hit));
   else if (some >= 0) atomicMax(&sh_first, some);
   __syncthreads();
   const int found = sh_first;
-  const int seg = found >= 0x40000000 ? kMaxRounds * kWaves - (found - 0x40000000) : found;
+  const int seg = found >= 0x40000000 ? kCand - (found - 0x40000000) : found;
   if (seg / C == tid) {
     u64 b = before;
 #pragma unroll
@@ -787,9 +1064,18 @@ __global__ __launch_bounds__(kNT) void k_sample(SampleArgs a) {
   __syncthreads();
   if (wave != 0) return;
   // one stretch: 64 loads, a lane each
+  const BinOf bin = bins_of(r, mx);
+  auto kept = [&](float x, int i) {
+    if (x == -INFINITY) return false;
+    if (s.mode == kAll) return true;
+    const int b = bin(x);
+    return b < cut || (b == cut && place_of(x, i) >= border);
+  };
   Vec<T> v;
-  const int at = (seg / kWaves * kNT + seg % kWaves * 64 + lane) * N;
-  v.load(row, at, V);
+  const int load = seg * 64 + lane;
+  v.fetch(logits, load, load < p.loads, a.vocab);
+  v.finish(load, load < p.loads, a.vocab);
+  const int at = v.first;
   u64 mass[N], lanes = 0;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
@@ -822,14 +1108,14 @@ __global__ __launch_bounds__(kNT) void k_sample(SampleArgs a) {
   if (lane == who) put(hits ? token : last, log_prob(hits ? x : x_last, all));
 }
 
-// Vocabularies beyond k_sample's stretches.
+// Vocabularies beyond the groups.
 template <class T>
 __global__ __launch_bounds__(kNT) void k_sample_long(SampleArgs a) {
   __shared__ Shared sh;
   const T* row = (const T*)a.logits + (int64_t)blockIdx.x * a.row_stride;
   float mx = -INFINITY;
   for (int i = threadIdx.x; i < a.vocab; i += kNT) mx = __builtin_fmaxf(mx, logit(row, i));
-  mx = block_max(mx, sh);
+  mx = block_max<kWaves>(mx, sh.tops);
   if (mx == -INFINITY) {
     if (threadIdx.x == 0) {
       a.tokens[blockIdx.x] = -1;
@@ -840,12 +1126,63 @@ __global__ __launch_bounds__(kNT) void k_sample_long(SampleArgs a) {
   sample_any<T>(a, sh, mx);
 }
 
+constexpr int kBatch = 1024;   // rows of a launch
+
 template <class T>
-hipError_t launch_type(const SampleArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)a.rows), t(kNT);
-  if (a.vocab <= kMaxRounds * kNT * Vec<T>::N) hipLaunchKernelGGL((k_sample<T>), g, t, 0, s, a);
-  else hipLaunchKernelGGL((k_sample_long<T>), g, t, 0, s, a);
-  return hipGetLastError();
+hipError_t launch_type(const SampleArgs& all, hipStream_t s) {
+  constexpr int N = Vec<T>::N;
+  Plan p{};
+  p.loads = (all.vocab + N - 1) / N;
+  while (((p.loads - 1) >> p.group_log) + 1 > kGroups) ++p.group_log;
+  const bool is_long = p.group_log > 6;
+  const int batch = all.rows < kBatch ? all.rows : kBatch;
+  void* ws = nullptr;
+  if (!is_long) {
+    p.groups = ((p.loads - 1) >> p.group_log) + 1;
+    p.stretches = (p.loads + 63) / 64;
+    // workgroups: eight a CU
+    int parts = (2048 + batch - 1) / batch;
+    parts = parts < kParts ? parts : kParts;
+    p.per = (p.loads + kBT * parts - 1) / (kBT * parts);
+    p.parts = (p.loads + kBT * p.per - 1) / (kBT * p.per);
+    auto up = [](int bytes) { return (bytes + 255) / 256 * 256; };
+    p.at_max = up((int)sizeof(State));
+    p.at_sums = p.at_max + up(p.groups * 4);
+    p.at_bins = p.at_sums + up(p.stretches * 8);
+    p.at_cand = p.at_bins + p.parts * kBins * 8;
+    p.row_bytes = p.at_cand + kCand * 8;
+    const hipError_t e = workspace_acquire(&ws, (size_t)batch * p.row_bytes, s);
+    if (e != hipSuccess) return e;
+    p.ws = (char*)ws;
+  }
+  hipError_t e = hipSuccess;
+  for (int r0 = 0; r0 < all.rows && e == hipSuccess; r0 += batch) {
+    SampleArgs a = all;
+    a.rows = all.rows - r0 < batch ? all.rows - r0 : batch;
+    a.logits = (const T*)all.logits + r0 * all.row_stride;
+    a.temperature += r0;
+    a.u += r0;
+    a.tokens += r0;
+    if (a.top_k) a.top_k += r0;
+    if (a.top_p) a.top_p += r0;
+    if (a.min_p) a.min_p += r0;
+    if (a.logprobs) a.logprobs += r0;
+    const dim3 rows((unsigned)a.rows), parts((unsigned)p.parts, (unsigned)a.rows), t(kNT), bt(kBT);
+    if (is_long) {
+      hipLaunchKernelGGL((k_sample_long<T>), rows, t, 0, s, a);
+    } else {
+      hipLaunchKernelGGL((k_sample_max<T>), parts, bt, 0, s, a, p);
+      hipLaunchKernelGGL((k_sample_gather<T>), parts, bt, 0, s, a, p);
+      if (a.top_p) hipLaunchKernelGGL((k_sample_border<T>), parts, bt, 0, s, a, p);
+      hipLaunchKernelGGL((k_sample_pick<T>), rows, t, 0, s, a, p);
+    }
+    e = hipGetLastError();
+  }
+  if (ws) {
+    const hipError_t f = workspace_release(ws, s);
+    if (e == hipSuccess) e = f;
+  }
+  return e;
 }
 
 }  // namespace
