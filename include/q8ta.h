@@ -668,7 +668,8 @@ q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
  * logits: [rows, vocab] of `dtype`, rows row_stride elements apart;
  * temperature, top_p, min_p, u fp32 [rows]; top_k int32 [rows]; tokens int32 [rows];
  * logprobs fp32 [rows] or NULL.  Requirements: rows >= 0 (0 is a no-op), 1 <=
- * vocab <= 2^24, row_stride >= vocab (any for one row).
+ * vocab <= 2^24, row_stride >= vocab (any for one row).  Workspace: 0.05 to 0.7 MB
+ * a row, 110 MB at most.
  */
 q8ta_status q8ta_sample(const void* logits, int64_t row_stride, q8ta_dtype dtype, int64_t rows,
                         int64_t vocab, const float* temperature, const int32_t* top_k,

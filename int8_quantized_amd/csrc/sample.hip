@@ -10,7 +10,7 @@
 //  2. k_sample_gather: where the prefix is short -- top-k up to 1024, or min-p --
 //     the few tokens that can be in it: with top-k those at or above a bound that
 //     k of the groups reach, with min-p those of about its weight.  With top-p
-//     over the whole vocabulary, sums of weights in bins of 1/32 of a power of
+//     over the whole vocabulary, sums of weights in bins of 1/64 of a power of
 //     two; with no filter, sums over stretches of 64 loads.
 //  3. k_sample_border (top-p over the whole vocabulary): the bin in which the
 //     border lies, its tokens, and the sums over stretches of those above it.
@@ -18,7 +18,8 @@
 //     cut exactly in that order and drawn from in the order of their indices; with
 //     sums over stretches the stretch is found, then the token inside it.
 //  * What these do not take (more than 4096 tokens tied or collected, top-k
-//    beyond 1024, a border below 2^-32 of the largest weight) goes the slow way:
+//    beyond 1024, a border below 2^-32 of the largest weight, infinite logits)
+//    goes the slow way:
 //    selection digit by digit of the key (the logit's bits in an
 //    order-preserving form), on counts (top-k) and on sums of weights (top-p).
 //
@@ -63,10 +64,7 @@ __device__ __forceinline__ Row make_row(float top, float temp, int shift) {
 // 2^y for y <= 0: 2^n times a polynomial in the rest f of [-1/2, 1/2], 1 + f * q(f)
 // with q of degree 8 through (2^f - 1) / f at nine Chebyshev points (off by
 // 4e-14 at most; exactly 1 for y = 0).
-__device__ __forceinline__ double exp2_of(double y) {
-  y = __builtin_fmax(y, -1100.0);
-  const double n = __builtin_rint(y);
-  const double f = y - n;
+__device__ __forceinline__ double poly(double f) {
   double q = 0x1.b63880f16b7cap-24;
   q = __builtin_fma(q, f, 0x1.63d1363459636p-20);
   q = __builtin_fma(q, f, 0x1.ffcb95155d9ebp-17);
@@ -76,6 +74,13 @@ __device__ __forceinline__ double exp2_of(double y) {
   q = __builtin_fma(q, f, 0x1.c6b08d7047e52p-5);
   q = __builtin_fma(q, f, 0x1.ebfbdff823cedp-3);
   q = __builtin_fma(q, f, 0x1.62e42fefa39efp-1);
+  return q;
+}
+__device__ __forceinline__ double exp2_of(double y) {
+  y = __builtin_fmax(y, -1100.0);
+  const double n = __builtin_rint(y);
+  const double f = y - n;
+  const double q = poly(f);
   return __builtin_ldexp(__builtin_fma(q, f, 1.0), (int)n);
 }
 
@@ -90,6 +95,29 @@ __device__ __forceinline__ double weight(const Row& r, float x) {
 __device__ __forceinline__ u64 units(const Row& r, double w) {
   const double big = 4503599627370496.0;
   return __builtin_bit_cast(u64, __builtin_fma(w, r.one, big)) - __builtin_bit_cast(u64, big);
+}
+
+// The weight of a finite logit or -inf as a whole number of 2^-shift, where the
+// row's largest logit is finite, in one straight line (a branch an element costs
+// more than the weight): 2^shift goes on in the exponent, and y no lower than -8
+// leaves 0 in any case.
+struct UnitsOf {
+  double top, scale, shift;
+  __device__ __forceinline__ u64 operator()(float x) const {
+    const double magic = 6755399441055744.0;   // 1.5 * 2^52: the sum's low word is the nearest whole number
+    double y = __builtin_fma((double)x - top, scale, shift);
+    y = __builtin_fmax(y, -8.0);               // (also for the NaN of -inf * 0)
+    const double t = y + magic;
+    const double f = y - (t - magic);
+    const double q = __builtin_fma(poly(f), f, 1.0);
+    const uint32_t n = (uint32_t)__builtin_bit_cast(u64, t);
+    const u64 w = __builtin_bit_cast(u64, q) + ((u64)(n << 20) << 32);
+    const double big = 4503599627370496.0;     // 2^52 leaves the rounded value in the low bits
+    return __builtin_bit_cast(u64, __builtin_bit_cast(double, w) + big) - __builtin_bit_cast(u64, big);
+  }
+};
+__device__ __forceinline__ UnitsOf units_of(const Row& r, int shift) {
+  return UnitsOf{r.top, r.scale, (double)shift};
 }
 
 template <class V>
@@ -406,8 +434,10 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64 (&sums)[kWaves], u64& all) 
 }
 
 constexpr int kCand = 4096;     // tokens that can be collected
-constexpr int kBins = 1024;     // weight bins, 32 to a power of two
+constexpr int kBins = 2048;     // weight bins, 64 to a power of two
 constexpr int kGroups = 4096;   // groups of loads, at most
+constexpr int kCoarse = 64;     // sums of 32 neighbouring bins each
+constexpr int kSlot = kBins + kCoarse;   // what a part leaves of them
 constexpr int kSteps = 1024;    // steps between the groups' largest logits
 constexpr int kBT = 256;        // threads of a part of a row
 constexpr int kParts = 32;      // parts of a row, at most
@@ -471,6 +501,12 @@ struct State {
   double goal;     // top-p's share of all weights
   u64 totals[kParts];
 };
+// Workgroup (x, part): all rows' first parts before the second ones, since some
+// rows need fewer; the rows go round with the parts, so that a period of 8
+// among the rows' settings does not leave them to one XCD.
+__device__ __forceinline__ int row_of(int rows) {
+  return (int)((blockIdx.x + blockIdx.y) % (unsigned)rows);
+}
 template <class P>
 __device__ __forceinline__ P* share(const Plan& p, int row, int at) {
   return (P*)(p.ws + (int64_t)row * p.row_bytes + at);
@@ -539,7 +575,7 @@ __device__ __forceinline__ void each_of(const SampleArgs& a, const T* row, int n
 // All loads of a part, in the row's order; the first of a wave's is a multiple of 64.
 template <class T, class F>
 __device__ __forceinline__ void each_load(const SampleArgs& a, const Plan& p, const T* row, F&& f) {
-  const int first = blockIdx.x * p.per * kBT + threadIdx.x;
+  const int first = blockIdx.y * p.per * kBT + threadIdx.x;
   each_of(a, row, p.per, [&](int i) { return first + i * kBT < p.loads ? first + i * kBT : -1; }, f);
 }
 // The loads of the listed groups, in any order.
@@ -559,8 +595,8 @@ __device__ __forceinline__ void each_listed(const SampleArgs& a, const Plan& p, 
 
 template <class T>
 __global__ __launch_bounds__(kBT) void k_sample_max(SampleArgs a, Plan p) {
-  const int row = blockIdx.y;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
+  const int row = row_of(a.rows);
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
     State* st = share<State>(p, row, 0);
     st->first = a.vocab;
     st->n_cand = 0;
@@ -578,23 +614,30 @@ __global__ __launch_bounds__(kBT) void k_sample_max(SampleArgs a, Plan p) {
   });
 }
 
-// Tokens that a part of a row collects, handed on at once.
+// Tokens that a part of a row collects: the first kLocal are handed on at once,
+// any more one by one.  (More than kCand in all: the slow way.)
+constexpr int kLocal = 1024;
 struct Collected {
-  u64 place[kCand];
+  u64 place[kLocal];
   int n, base;
 };
-__device__ __forceinline__ void append(Collected& c, float x, int token) {
+__device__ __forceinline__ void append(Collected& c, State* st, u64* cand, float x, int token) {
   const int to = atomicAdd(&c.n, 1);
-  if (to < kCand) c.place[to] = place_of(x, token);
+  if (to < kLocal) {
+    c.place[to] = place_of(x, token);
+  } else {
+    const int at = atomicAdd(&st->n_cand, 1);
+    if (at < kCand) cand[at] = place_of(x, token);
+  }
 }
 __device__ __forceinline__ void hand_on(Collected& c, State* st, u64* cand) {
   __syncthreads();
-  const int n = c.n;
+  const int n = c.n < kLocal ? c.n : kLocal;
   if (n == 0) return;
-  if (threadIdx.x == 0) c.base = atomicAdd(&st->n_cand, n);   // (beyond kCand: the slow way)
+  if (threadIdx.x == 0) c.base = atomicAdd(&st->n_cand, n);
   __syncthreads();
   const int base = c.base;
-  for (int i = threadIdx.x; i < n && i < kCand; i += kBT)
+  for (int i = threadIdx.x; i < n; i += kBT)
     if (base + i < kCand) cand[base + i] = c.place[i];
 }
 
@@ -611,7 +654,16 @@ __global__ __launch_bounds__(kBT) void k_sample_gather(SampleArgs a, Plan p) {
   __shared__ u64 sums[kWaves];
   __shared__ float tops[kWaves];
   __shared__ int sh_last;
-  const int tid = threadIdx.x, lane = tid & 63, row = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, row = row_of(a.rows), part = blockIdx.y;
+  // where groups are picked out, as many parts as have something to do
+  const Settings s = settings_of(a, row);
+  const bool picks = s.mode == kFirst || s.mode == kFewK || (s.mode == kMinP && !s.cut_p);
+  int parts = p.parts;
+  if (picks) {
+    const int some = s.mode == kFirst ? 1 : (s.mode == kFewK ? 1 + s.k / 128 : 4);
+    parts = some < parts ? some : parts;
+  }
+  if (part >= parts) return;
   const T* logits = (const T*)a.logits + (int64_t)row * a.row_stride;
   const float* group = share<float>(p, row, p.at_max);
   State* st = share<State>(p, row, 0);
@@ -623,23 +675,22 @@ __global__ __launch_bounds__(kBT) void k_sample_gather(SampleArgs a, Plan p) {
     g[i] = at < p.groups ? group[at] : -INFINITY;
     mine = __builtin_fmaxf(mine, g[i]);
   }
-  const Settings s = settings_of(a, row);
   if (tid == 0) {
     sh.c.n = 0;
     n_list = 0;
   }
   const float mx = block_max<NW>(mine, tops);
-  if (blockIdx.x == 0 && tid == 0) st->mx = mx;
-  if (mx == -INFINITY || s.mode == kSlow) return;
+  if (part == 0 && tid == 0) st->mx = mx;
+  if (mx == -INFINITY || s.mode == kSlow || (mx == INFINITY && s.mode != kFirst)) return;
   const Row r = make_row(mx, s.temp, a.shift);
-  // the groups of this part whose largest logit passes, listed
-  const int g0 = (blockIdx.x * p.per * kBT) >> p.group_log;
-  const int g1 = ((blockIdx.x + 1) * p.per * kBT) >> p.group_log;
+  const UnitsOf un = units_of(r, a.shift);
+  // the groups of this part's share whose largest logit passes, listed
+  const int g0 = part * p.groups / parts, g1 = (part + 1) * p.groups / parts;
   auto list_groups = [&](auto&& passes) {
 #pragma unroll
     for (int i = 0; i < kGroups / kBT; ++i) {
       const int at = tid + i * kBT;
-      if (at >= g0 && at < g1 && at < p.groups && passes(g[i])) list[atomicAdd(&n_list, 1)] = (uint16_t)at;
+      if (at >= g0 && at < g1 && passes(g[i])) list[atomicAdd(&n_list, 1)] = (uint16_t)at;
     }
     __syncthreads();
     return n_list;
@@ -692,7 +743,7 @@ __global__ __launch_bounds__(kBT) void k_sample_gather(SampleArgs a, Plan p) {
     each_listed(a, p, logits, list, n_groups, [&](int, const Vec<T>& v) {
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (in(v.x[e])) append(sh.c, v.x[e], v.first + e);
+        if (in(v.x[e])) append(sh.c, st, cand, v.x[e], v.first + e);
     });
     hand_on(sh.c, st, cand);
   } else if (s.mode == kMinP) {
@@ -703,22 +754,22 @@ __global__ __launch_bounds__(kBT) void k_sample_gather(SampleArgs a, Plan p) {
     if (s.cut_p) {
       each_load(a, p, logits, [&](int, const Vec<T>& v) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          sum += units(r, weight(r, v.x[e]));
-          if (in(v.x[e])) append(sh.c, v.x[e], v.first + e);
-        }
+        for (int e = 0; e < N; ++e) sum += un(v.x[e]);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (in(v.x[e])) append(sh.c, st, cand, v.x[e], v.first + e);
       });
     } else {
       const int n = list_groups(in);
       each_listed(a, p, logits, list, n, [&](int, const Vec<T>& v) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
-          if (in(v.x[e])) append(sh.c, v.x[e], v.first + e);
+          if (in(v.x[e])) append(sh.c, st, cand, v.x[e], v.first + e);
       });
     }
     u64 all;
     block_scan<NW>(sum, sums, all);
-    if (tid == 0) st->totals[blockIdx.x] = all;
+    if (tid == 0) st->totals[part] = all;
     hand_on(sh.c, st, cand);
   } else if (s.mode == kTopP) {
     __syncthreads();
@@ -726,21 +777,29 @@ __global__ __launch_bounds__(kBT) void k_sample_gather(SampleArgs a, Plan p) {
     __syncthreads();
     const BinOf bin = bins_of(r, mx);
     each_load(a, p, logits, [&](int, const Vec<T>& v) {
+      u64 w[N];
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const u64 w = units(r, weight(r, v.x[e]));
-        if (w > 0) atomicAdd(&sh.bins[bin(v.x[e])], w);
-      }
+      for (int e = 0; e < N; ++e) w[e] = un(v.x[e]);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (w[e] > 0) atomicAdd(&sh.bins[bin(v.x[e])], w[e]);
     });
     __syncthreads();
-    u64* out = share<u64>(p, row, p.at_bins) + blockIdx.x * kBins;
+    u64* out = share<u64>(p, row, p.at_bins) + part * kSlot;
     for (int i = tid; i < kBins; i += kBT) out[i] = sh.bins[i];
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < kBins / kBT; ++i) sum += sh.bins[kBins / kBT * tid + i];
+    static_assert(kBT == 4 * kCoarse, "four threads a coarse sum");
+    sum += __shfl_xor(sum, 1);
+    sum += __shfl_xor(sum, 2);
+    if (tid % 4 == 0) out[kBins + tid / 4] = sum;
   } else {
     u64* out = share<u64>(p, row, p.at_sums);
     each_load(a, p, logits, [&](int at, const Vec<T>& v) {
       u64 sum = 0;
 #pragma unroll
-      for (int e = 0; e < N; ++e) sum += units(r, weight(r, v.x[e]));
+      for (int e = 0; e < N; ++e) sum += un(v.x[e]);
       sum = wave_sum(sum);
       if (lane == 0 && at >= 0) out[at / 64] = sum;
     });
@@ -749,60 +808,83 @@ __global__ __launch_bounds__(kBT) void k_sample_gather(SampleArgs a, Plan p) {
 
 template <class T>
 __global__ __launch_bounds__(kBT) void k_sample_border(SampleArgs a, Plan p) {
-  constexpr int N = Vec<T>::N, NW = kBT / 64, C = kBins / kBT;
+  constexpr int N = Vec<T>::N;
   __shared__ Collected c;
-  __shared__ u64 sums[kWaves];
+  __shared__ u64 split[kBT];
   __shared__ int sh_bin;
   __shared__ u64 sh_base;
-  const int tid = threadIdx.x, lane = tid & 63, row = blockIdx.y;
+  __shared__ double sh_goal;
+  const int tid = threadIdx.x, lane = tid & 63, row = row_of(a.rows), part = blockIdx.y;
   const Settings s = settings_of(a, row);
   State* st = share<State>(p, row, 0);
   const float mx = st->mx;
-  if (s.mode != kTopP || mx == -INFINITY) return;
+  if (s.mode != kTopP || !(__builtin_fabsf(mx) < INFINITY)) return;
   const Row r = make_row(mx, s.temp, a.shift);
+  const UnitsOf un = units_of(r, a.shift);
   const u64* bins = share<u64>(p, row, p.at_bins);
-  u64 n[C] = {}, sum = 0;
-#pragma unroll 8
-  for (int part = 0; part < p.parts; ++part)
+  // sums over the parts of `of` neighbouring sums from `from` on, one a lane of
+  // the first wave
+  auto over_parts = [&](int from, int of) {
+    const int i = tid & (of - 1);
+    u64 n = 0;
+#pragma unroll 4
+    for (int q = tid / of; q < p.parts; q += kBT / of) n += bins[q * kSlot + from + i];
+    __syncthreads();
+    split[tid] = n;
+    __syncthreads();
+    n = 0;
+    if (tid < of)
+      for (int q = tid; q < kBT; q += of) n += split[q];
+    return n;
+  };
+  // the sum in which the running one reaches the goal
+  auto find = [&](u64 n, u64 base, bool known) {
+    u64 upto = n;
 #pragma unroll
-    for (int i = 0; i < C; ++i) n[i] += bins[part * kBins + C * tid + i];
-#pragma unroll
-  for (int i = 0; i < C; ++i) sum += n[i];
-  if (tid == 0) c.n = 0;
-  u64 all;
-  u64 before = block_scan<NW>(sum, sums, all);
-  const double goal = (double)s.p * (double)all;
-  // the bin in which the running sum reaches the goal
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    if (n[i] > 0 && (double)before < goal && !((double)(before + n[i]) < goal)) {
-      sh_bin = C * tid + i;
-      sh_base = before;
+    for (int m = 1; m < 64; m *= 2) {
+      const u64 o = __shfl_up(upto, m);
+      if (lane >= m) upto += o;
     }
-    before += n[i];
-  }
+    if (!known && lane == 63) sh_goal = (double)s.p * (double)upto;
+    __builtin_amdgcn_wave_barrier();
+    const double goal = known ? sh_goal : (double)s.p * (double)__shfl(upto, 63);
+    upto += base;
+    if (n > 0 && (double)(upto - n) < goal && !((double)upto < goal)) {
+      sh_bin = lane;
+      sh_base = upto - n;
+    }
+  };
+  if (tid == 0) c.n = 0;
+  const u64 coarse = over_parts(kBins, kCoarse);
+  if (tid < 64) find(coarse, 0, false);
   __syncthreads();
-  const int cut = sh_bin;
-  if (blockIdx.x == 0 && tid == 0) {
+  const int from = sh_bin * (kBins / kCoarse);
+  const u64 fine = over_parts(from, kBins / kCoarse);
+  if (tid < 64) find(fine, sh_base, true);
+  __syncthreads();
+  const int cut = from + sh_bin;
+  if (part == 0 && tid == 0) {
     st->cut_bin = cut;
     st->base = sh_base;
-    st->goal = goal;
+    st->goal = sh_goal;
   }
   if (cut >= kBins - 1) return;
   const BinOf bin = bins_of(r, mx);
   u64* out = share<u64>(p, row, p.at_sums);
+  u64* cand = share<u64>(p, row, p.at_cand);
   each_load(a, p, (const T*)a.logits + (int64_t)row * a.row_stride, [&](int at, const Vec<T>& v) {
     u64 w = 0;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const int b = v.x[e] == -INFINITY ? kBins : bin(v.x[e]);
-      if (b < cut) w += units(r, weight(r, v.x[e]));
-      if (b == cut) append(c, v.x[e], v.first + e);
+      const u64 u = un(v.x[e]);
+      w += b < cut ? u : 0;
+      if (b == cut) append(c, st, cand, v.x[e], v.first + e);
     }
     w = wave_sum(w);
     if (lane == 0 && at >= 0) out[at / 64] = w;
   });
-  hand_on(c, st, share<u64>(p, row, p.at_cand));
+  hand_on(c, st, cand);
 }
 
 // Falling order of n different places.
@@ -871,11 +953,12 @@ __global__ __launch_bounds__(kNT) void k_sample_pick(SampleArgs a, Plan p) {
     if (tid == 0) put(st->first, 0.0f);
     return;
   }
-  if (s.mode == kSlow || n_cand > kCand || (s.mode == kTopP && st->cut_bin >= kBins - 1)) {
+  if (s.mode == kSlow || mx == INFINITY || n_cand > kCand || (s.mode == kTopP && st->cut_bin >= kBins - 1)) {
     sample_any<T>(a, sh, mx);
     return;
   }
   const Row r = make_row(mx, s.temp, a.shift);
+  const UnitsOf un = units_of(r, a.shift);
   auto log_prob = [&](float x, u64 all) {
     const double z = (double)x == r.top ? 0.0 : ((double)x - r.top) * r.inv_t;
     return (float)(z - log((double)all / r.one));
@@ -897,7 +980,7 @@ __global__ __launch_bounds__(kNT) void k_sample_pick(SampleArgs a, Plan p) {
       if (wave != 0) return;
       const u64 mine = lane < n ? cand[lane] : 0;
       const double wd = lane < n ? weight(r, value_of(mine)) : 0.0;
-      const u64 w1 = units(r, wd);
+      const u64 w1 = lane < n ? un(value_of(mine)) : 0;
       u64 upto = w1;
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) {
@@ -926,7 +1009,7 @@ __global__ __launch_bounds__(kNT) void k_sample_pick(SampleArgs a, Plan p) {
     for (int c = 0; c < C; ++c) {
       const int j = C * tid + c;
       wd[c] = j < n ? weight(r, value_of(cand[j])) : 0.0;
-      w[c] = units(r, wd[c]);
+      w[c] = j < n ? un(value_of(cand[j])) : 0;
       sum += w[c];
     }
     u64 before = block_scan<kWaves>(sum, sh.sums, all);
@@ -1001,7 +1084,7 @@ __global__ __launch_bounds__(kNT) void k_sample_pick(SampleArgs a, Plan p) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = C * tid + c;
-      w[c] = j < n ? units(r, weight(r, value_of(cand[j]))) : 0;
+      w[c] = j < n ? un(value_of(cand[j])) : 0;
       sum += w[c];
     }
     u64 in_bin;
@@ -1079,7 +1162,7 @@ __global__ __launch_bounds__(kNT) void k_sample_pick(SampleArgs a, Plan p) {
   u64 mass[N], lanes = 0;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    mass[e] = kept(v.x[e], at + e) ? units(r, weight(r, v.x[e])) : 0;
+    mass[e] = kept(v.x[e], at + e) ? un(v.x[e]) : 0;
     lanes += mass[e];
   }
   u64 run = lanes;
@@ -1140,7 +1223,8 @@ hipError_t launch_type(const SampleArgs& all, hipStream_t s) {
   if (!is_long) {
     p.groups = ((p.loads - 1) >> p.group_log) + 1;
     p.stretches = (p.loads + 63) / 64;
-    // workgroups: eight a CU
+    // eight workgroups a CU (256 rows x 131072: 65 us, 71 with four, 99 with
+    // two; 24 x 100003: 41 us with any)
     int parts = (2048 + batch - 1) / batch;
     parts = parts < kParts ? parts : kParts;
     p.per = (p.loads + kBT * parts - 1) / (kBT * parts);
@@ -1149,7 +1233,7 @@ hipError_t launch_type(const SampleArgs& all, hipStream_t s) {
     p.at_max = up((int)sizeof(State));
     p.at_sums = p.at_max + up(p.groups * 4);
     p.at_bins = p.at_sums + up(p.stretches * 8);
-    p.at_cand = p.at_bins + p.parts * kBins * 8;
+    p.at_cand = p.at_bins + p.parts * kSlot * 8;
     p.row_bytes = p.at_cand + kCand * 8;
     const hipError_t e = workspace_acquire(&ws, (size_t)batch * p.row_bytes, s);
     if (e != hipSuccess) return e;
@@ -1167,7 +1251,7 @@ hipError_t launch_type(const SampleArgs& all, hipStream_t s) {
     if (a.top_p) a.top_p += r0;
     if (a.min_p) a.min_p += r0;
     if (a.logprobs) a.logprobs += r0;
-    const dim3 rows((unsigned)a.rows), parts((unsigned)p.parts, (unsigned)a.rows), t(kNT), bt(kBT);
+    const dim3 rows((unsigned)a.rows), parts((unsigned)a.rows, (unsigned)p.parts), t(kNT), bt(kBT);
     if (is_long) {
       hipLaunchKernelGGL((k_sample_long<T>), rows, t, 0, s, a);
     } else {
