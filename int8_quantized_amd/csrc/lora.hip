@@ -14,8 +14,8 @@
 // adapter's own 16-bit values the products are exact and the sums 32-bit.
 //
 // k_lora_rows: 16 * MT rows by 16 * FN channels, for the row counts of decode
-// steps, where the weight stream is what has to be paid: the four waves take
-// every fourth 64-byte step of K, weight and activation fragments come
+// steps, where the weight stream is what has to be paid: the waves take
+// every WAVES-th 64-byte step of K, weight and activation fragments come
 // straight from memory into the operands of v_mfma_i32_16x16x64_i8 (16
 // bytes a lane, the next step's loads ahead of this step's products), and
 // their integer sums meet in LDS.
@@ -173,28 +173,38 @@ __device__ __forceinline__ float half_at(uint32_t w, int hi) {
   return to_float(AT{(uint16_t)(hi ? w >> 16 : w)});
 }
 
-// sum_r B[ad, n, r] t[r] over the adapter's rank.
+// sum_r B[ad, n, r] t[r] over the adapter's rank.  Rows of 16-byte chunks: the
+// first kAhead come loaded (ahead: ready before t and the sums are), the others
+// as many at once.
+constexpr int kAhead = 4;
 template <class AT>
-__device__ __forceinline__ float up_dot(const LoraArgs& a, int ad, int64_t n, const float* t) {
-  const int rank = rank_of(a, ad);
-  const AT* b = (const AT*)a.b + ((int64_t)ad * a.lin.N + n) * a.rank;
-  float s = 0.0f;
-  if (a.rank % 8 == 0 && ((uintptr_t)a.b & 15) == 0) {
-    for (int r = 0; r < rank; r += 8) {   // t is 0 past the rank
-      const v4u w = *reinterpret_cast<const v4u*>(b + r);
-      const v4f t0 = *reinterpret_cast<const v4f*>(t + r);
-      const v4f t1 = *reinterpret_cast<const v4f*>(t + r + 4);
+__device__ __forceinline__ const AT* up_row(const LoraArgs& a, int ad, int64_t n) {
+  return (const AT*)a.b + ((int64_t)ad * a.lin.N + n) * a.rank;
+}
+__device__ __forceinline__ void up_load(const void* row, int r, int rank, v4u (&w)[kAhead]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool in0 = r + 2 * i < rank, in1 = r + 2 * i + 1 < rank;
-        const float ta = i < 2 ? t0[2 * i] : t1[2 * i - 4];
-        const float tb = i < 2 ? t0[2 * i + 1] : t1[2 * i - 3];
-        s = __builtin_fmaf(in0 ? half_at<AT>(w[i], 0) : 0.0f, ta, s);
-        s = __builtin_fmaf(in1 ? half_at<AT>(w[i], 1) : 0.0f, tb, s);
-      }
+  for (int i = 0; i < kAhead; ++i) {
+    w[i] = v4u{0, 0, 0, 0};
+    if (r + 8 * i < rank) w[i] = *reinterpret_cast<const v4u*>((const uint16_t*)row + r + 8 * i);
+  }
+}
+template <class AT>
+__device__ __forceinline__ float up_sum(const v4u (&w)[kAhead], int r, int rank, const float* t, float s) {
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int at = r + 8 * j;
+    if (at >= rank) break;   // t is 0 past the rank, up to a multiple of 16
+    const v4f t0 = *reinterpret_cast<const v4f*>(t + at);
+    const v4f t1 = *reinterpret_cast<const v4f*>(t + at + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in0 = at + 2 * i < rank, in1 = at + 2 * i + 1 < rank;
+      const float ta = i < 2 ? t0[2 * i] : t1[2 * i - 4];
+      const float tb = i < 2 ? t0[2 * i + 1] : t1[2 * i - 3];
+      const uint32_t pair = w[j][i];
+      s = __builtin_fmaf(in0 ? half_at<AT>(pair, 0) : 0.0f, ta, s);
+      s = __builtin_fmaf(in1 ? half_at<AT>(pair, 1) : 0.0f, tb, s);
     }
-  } else {
-    for (int r = 0; r < rank; ++r) s = __builtin_fmaf(to_float(b[r]), t[r], s);
   }
   return s;
 }
@@ -265,11 +275,27 @@ __global__ __launch_bounds__(64 * WAVES) void k_lora_rows(LoraArgs a) {
     ws[i] += __shfl_xor(ws[i], 32);
     if (g == 0) wsum[wave][16 * i + n] = ws[i];
   }
+  // this thread's outputs; the first chunks of their adapters' rows are on
+  // their way while the waves' sums meet
+  constexpr int E = (BM * BN + 64 * WAVES - 1) / (64 * WAVES);
+  const bool vec = a.rank % 8 == 0 && ((uintptr_t)a.b & 15) == 0;
+  int ad[E], rank[E];
+  v4u ahead[E][kAhead];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int e = tid + i * 64 * WAVES;
+    const int64_t m = m0 + e / BN, ch = n0 + e % BN;
+    ad[i] = e < BM * BN && m < M && ch < N ? adapter_of(a, m) : -1;
+    rank[i] = ad[i] >= 0 ? rank_of(a, ad[i]) : 0;
+    if (vec) up_load(up_row<AT>(a, ad[i] >= 0 ? ad[i] : 0, ch < N ? ch : 0), 0, rank[i], ahead[i]);
+  }
   __syncthreads();
-  for (int e = tid; e < BM * BN; e += 64 * WAVES) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int e = tid + i * 64 * WAVES;
     const int row = e / BN, c = e % BN;
     const int64_t m = m0 + row, ch = n0 + c;
-    if (m >= M || ch >= N) continue;
+    if (e >= BM * BN || m >= M || ch >= N) continue;
     int32_t s = 0, w = 0;
 #pragma unroll
     for (int v = 0; v < WAVES; ++v) {
@@ -280,8 +306,22 @@ __global__ __launch_bounds__(64 * WAVES) void k_lora_rows(LoraArgs a) {
     y = y * a.lin.rq.s_in;
     y = y * a.lin.wscale[ch];
     y = y + (a.lin.bias ? a.lin.bias[ch] : 0.0f);
-    const int ad = adapter_of(a, m);
-    if (ad >= 0) y = y + up_dot<AT>(a, ad, ch, a.t + m * a.rank_pad);
+    if (rank[i] > 0) {
+      const AT* b = up_row<AT>(a, ad[i], ch);
+      const float* t = a.t + m * a.rank_pad;
+      float up = 0.0f;
+      if (vec) {
+        up = up_sum<AT>(ahead[i], 0, rank[i], t, up);
+        for (int r = 8 * kAhead; r < rank[i]; r += 8 * kAhead) {
+          v4u more[kAhead];
+          up_load(b, r, rank[i], more);
+          up = up_sum<AT>(more, r, rank[i], t, up);
+        }
+      } else {
+        for (int r = 0; r < rank[i]; ++r) up = __builtin_fmaf(to_float(b[r]), t[r], up);
+      }
+      y = y + up;
+    }
     if (a.relu) y = y < 0.0f ? 0.0f : y;
     ((YT*)a.y)[m * N + ch] = from_float<YT>(y);
   }
@@ -326,15 +366,41 @@ hipError_t launch_shape(const LoraArgs& a, hipStream_t s) {
 
 template <class AT, class YT>
 hipError_t launch_rows(const LoraArgs& a, hipStream_t s) {
-  if (a.lin.M <= 16) return launch_shape<AT, YT, 1, 1, 16, 4>(a, s);
-  if (a.lin.M <= 32) return launch_shape<AT, YT, 2, 2, 8, 4>(a, s);
-  return launch_shape<AT, YT, 4, 2, 8, 3>(a, s);
+  // Channels of a workgroup, in sixteens: the fewest rounds of 256 workgroups
+  // times what one of them takes, which is about c + 1 (it reads its channels and
+  // all rows).  4096 x 11008 with 24 adapters, 64 rows: 48 channels 39 us, 32 48, 16
+  // 53; 4096 x 16384: 64, 50, 67; 4096 x 4096: 38, 31, 26.
+  int c = 1;
+  int64_t least = INT64_MAX;
+  for (int i = 1; i <= 3; ++i) {
+    const int64_t groups = (a.lin.N + 16 * i - 1) / (16 * i), cost = (groups + 255) / 256 * (i + 1);
+    if (cost <= least) {
+      least = cost;
+      c = i;
+    }
+  }
+  if (a.lin.M <= 16) {
+    if (c == 1) return launch_shape<AT, YT, 1, 1, 16, 4>(a, s);
+    if (c == 2) return launch_shape<AT, YT, 1, 2, 8, 4>(a, s);
+    return launch_shape<AT, YT, 1, 3, 8, 4>(a, s);
+  }
+  if (a.lin.M <= 32) {
+    if (c == 1) return launch_shape<AT, YT, 2, 1, 8, 4>(a, s);
+    if (c == 2) return launch_shape<AT, YT, 2, 2, 8, 4>(a, s);
+    return launch_shape<AT, YT, 2, 3, 16, 2>(a, s);
+  }
+  if (c == 1) return launch_shape<AT, YT, 4, 1, 16, 2>(a, s);
+  if (c == 2) return launch_shape<AT, YT, 4, 2, 8, 2>(a, s);
+  return launch_shape<AT, YT, 4, 3, 8, 2>(a, s);
 }
 
 template <class AT>
 hipError_t launch_down(const LoraArgs& a, hipStream_t s) {
   const unsigned tiles = (unsigned)((a.lin.M + 15) / 16);
-  const int rb = a.rank_pad > 16 ? 2 : 1;
+  // 32 ranks a workgroup where there are many tiles (x is read once for them:
+  // 2048 rows 17.8 us against 21.6), 16 with twice the loads in flight where a
+  // launch is a chain of latencies (50 rows 10.0 against 13.4)
+  const int rb = a.rank_pad > 16 && a.lin.M > 64 ? 2 : 1;
   const unsigned z = (unsigned)((a.rank_pad + 16 * rb - 1) / (16 * rb));
   // workgroups a tile's adapters are dealt over: up to 16, fewer where the
   // tiles alone fill the card
