@@ -8,12 +8,12 @@
 // tokens (the cache's next rows), those whose bit is set in the token's mask.
 //
 // One pass over the keys with the running maximum and sum of the softmax, on
-// the 16x16x32 fp16 matrix instruction.  A wave takes 64 keys per step for up to
-// 16 * QT rows of one key head; the waves of a workgroup take every WAVES-th
-// step and join their sums in LDS at the end; the keys of all requests are dealt
-// out evenly over the workgroups, and k_attn_join joins what was cut.  No wave waits for another inside
-// the loop: with few rows the step is as long as its loads, and with many the
-// widening of the codes, which every wave does for itself, is the smaller part.
+// the 16x16x32 fp16 matrix instruction.  A wave takes 16 * TL keys per step for
+// up to 16 * QT rows of one key head; the waves of a workgroup take every
+// WAVES-th step and join their sums in LDS at the end; the keys of all requests
+// are dealt out evenly over the workgroups, and k_attn_join joins what was cut.
+// No wave waits for another inside the loop: with few rows the step is as long
+// as its loads, and with many every wave widens the codes for itself.
 //  * Codes are whole numbers of [-128, 127] and exact in fp16.  A key's byte b ^
 //    0x80 under the exponent byte 0x64 is 1024 + 128 + code, less 1152; a value's
 //    under a zero byte is the subnormal (128 + code) * 2^-24, less 128 * 2^-24,
@@ -44,6 +44,15 @@
 //  * 2^(s - m) is taken straight from the products; the maximum m is renewed
 //    only when one passes 2^4, the values' power of two when a scale passes
 //    twice it: most steps need no exchange between lanes and no rescaling.
+//  * What bounds it: single tokens over long contexts, the cache's bytes (32
+//    requests x up to 24k keys x 8 heads x 128: 1.22 GB in 228 us, 5.3 TB/s; a copy
+//    runs at 4.9).  Trees, the vector instructions that widen codes and form the
+//    softmax beside the matrix instructions, about three to one, at the two
+//    waves a SIMD that the registers leave: 24 tokens x 4 heads of a group x 16
+//    requests x 4k in 77 us and 11 for the join, 64 x 8 x 4 x 16k in 100 and 8
+//    (four row tiles a wave, which halve the widening, spill and take 98).  One
+//    token over 700 keys is eight workgroups and a chain of latencies (page
+//    table, keys, join in LDS): 14.6 us.
 //  * A step's registers are loaded again for the next one as soon as it has
 //    used them (keys after the first product, values after the second), so
 //    loads are in flight through all of a step.
