@@ -51,8 +51,7 @@
 //    waves a SIMD that the registers leave: 24 tokens x 4 heads of a group x 16
 //    requests x 4k in 77 us and 11 for the join, 64 x 8 x 4 x 16k in 100 and 8
 //    (four row tiles a wave, which halve the widening, spill and take 98).  One
-//    token over 700 keys is eight workgroups and a chain of latencies (page
-//    table, keys, join in LDS): 14.6 us.
+//    token over 700 keys is a chain of latencies (page table, keys, joins): 13 us.
 //  * A step's registers are loaded again for the next one as soon as it has
 //    used them (keys after the first product, values after the second), so
 //    loads are in flight through all of a step.
@@ -804,7 +803,13 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
   // tiles a wave where there are more than 16 rows (24-token trees x 16 x 4k 80
   // us against 113 with one tile, 64-token trees x 4 x 16k 102 against 141)
   if (rows <= 16) {
-    if (keys <= 128 * SW) return launch_shape<T, DP, SW, 1, 2>(a, 0, s);
+    // One workgroup of more waves a unit and no joining launch, where a few steps a
+    // wave cost less than that: 8 heads, 1 request: 250 keys 10.7 us against 12.7,
+    // 500 12.5 and 12.7, 700 14.7 and 13.1; 8 requests: 700 14.7 and 16.3; 64: 1000
+    // 35 and 40.  Up to 128 keys four waves do without the join too (64 requests
+    // x 100: 10.9 us against 16.2 with eight).
+    const int64_t units = (int64_t)a.batch * a.kv_heads;
+    if (keys > 128 && keys <= (units < 64 ? 64 : 128) * SW) return launch_shape<T, DP, SW, 1, 2>(a, 0, s);
     return launch_shape<T, DP, 4, 1, 2>(a, kTwo, s);
   }
   if constexpr (DP == 256) return launch_shape<T, DP, 4, 1, 2>(a, kTwo, s);
