@@ -14,7 +14,8 @@
 // adapter's own 16-bit values the products are exact and the sums 32-bit.
 //
 // k_lora_rows: 16 * MT rows by 16 * FN channels, for the row counts of decode
-// steps, where the weight stream is what has to be paid: the waves take
+// steps, where the weight stream is what has to be paid, and for products of few
+// large tiles: the waves take
 // every WAVES-th 64-byte step of K, weight and activation fragments come
 // straight from memory into the operands of v_mfma_i32_16x16x64_i8 (16
 // bytes a lane, the next step's loads ahead of this step's products), and
@@ -379,7 +380,7 @@ hipError_t launch_rows(const LoraArgs& a, hipStream_t s) {
   int c = 1;
   int64_t least = INT64_MAX;
   for (int i = 1; i <= 3; ++i) {
-    const int64_t groups = (a.lin.N + 16 * i - 1) / (16 * i), cost = (groups + 255) / 256 * (i + 1);
+    const int64_t groups = (a.lin.N + 16 * i - 1) / (16 * i) * ((a.lin.M + 63) / 64), cost = (groups + 255) / 256 * (i + 1);
     if (cost <= least) {
       least = cost;
       c = i;
@@ -429,9 +430,13 @@ hipError_t launch_few(const LoraArgs& a, hipStream_t s) {
 }
 
 // Which product: the eight-wave GEMM, the two-workgroup GEMM, or k_lora_rows.
+// The GEMMs' tiles of 256 x 256 and 256 x 128 leave most of the card idle where there
+// are few: up to about one round of k_lora_rows' workgroups that is the faster
+// (K 4096: 128 x 2048 22 us against 50, 168 x 4113, 258 groups, 40 and 51, 256 x
+// 4113, 344 groups, 56 and 48; K 1024: 1024 x 512 15 and 20).
 char product_of(const LinearArgs& a) {
-  if (a.M > 64 && gemm_w8_preferred(a)) return 'w';
-  return a.M > 64 ? 'x' : 'r';
+  if ((a.M + 63) / 64 * ((a.N + 47) / 48) <= 300 || a.M <= 64) return 'r';
+  return gemm_w8_preferred(a) ? 'w' : 'x';
 }
 
 }  // namespace

@@ -161,6 +161,29 @@ def test_linear_lora_adapter_that_is_no_number_spoils_its_own_rows_only(M, N, ou
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ad", ["fp16", "bf16"])
+@pytest.mark.parametrize("out", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("M,K,N,offset", [(1100, 1037, 1100, 0), (1030, 1024, 1111, 3), (2100, 1024, 4200, 0),
+                                          (2050, 1100, 4199, 0)])
+def test_linear_lora_large_products_in_detail(M, K, N, offset, out, ad):
+    """What the small sizes above cover, where the product is a GEMM of large tiles."""
+    na, r = 5, 32
+    c = make(M, K, N, r, na, in_runs(M, na, 40, 1), ad, out, seed=9, ranks=[0, 3, 16, 40, 32], scales=False,
+             bias=False, offset=offset)
+    c["a"][1, 3:] = float("nan")
+    c["b"][1, :, 3:] = float("nan")
+    c["b"][2, :, 16:] = float("inf")
+    check(c)
+    check(c, "relu")
+    want = run(c)
+    own = c["ids"] == 4
+    c["b"][4, ::3, 5] = float("inf")
+    got = run(c)
+    assert torch.equal(got[~own], want[~own])
+    assert not torch.isfinite(got[own][:, ::3]).any() and torch.isfinite(got[own][:, 2::3]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 40, 520])
 @pytest.mark.parametrize("zp", [-128, 127])
 def test_linear_lora_zero_points_and_far_adapters(M, zp):
