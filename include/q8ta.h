@@ -559,12 +559,12 @@ q8ta_status q8ta_conv2d_acc(const int8_t* x, int64_t N, int64_t IC,
  * [adapters] or NULL: an adapter's own rank within `rank`, what lies past it is
  * not read as numbers (an adapter value that is not finite makes outputs of its
  * own rows not finite, and no others); adapter_ids: int32 [M]; out: dense [M, N] of
- * out_dtype.  Requirements: as for q8ta_linear, M <= 2^21, N and K
- * <= 2^30, 1 <= rank <= 512, 1 <= adapters <= 2^24.  Any K and alignment: where K is no multiple of 16 or x,
- * weight or lora_a are not 16-byte aligned, they are first copied into rows
- * that are (workspace: (M + N + 2 * adapters * rank) * K bytes, K rounded up to
- * 64).  Workspace otherwise: 4 bytes for each row and rank (rounded up to
- * 16).
+ * out_dtype.  Requirements: as for q8ta_linear, M <= 2^21, N and K <= 2^30,
+ * 1 <= rank <= 512, 1 <= adapters <= 2^24.  Any K and alignment: where K is no
+ * multiple of 16 or x, weight or lora_a are not 16-byte aligned, they are first
+ * copied into rows that are (workspace: (M + N + 2 * adapters * rank) * K bytes, K rounded up to
+ * 64).  Workspace otherwise: up to 6 bytes for each row and rank (rounded
+ * up to 16).
  */
 q8ta_status q8ta_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_scale,
                              int64_t input_zero_point, const int8_t* weight, int64_t N,
