@@ -625,7 +625,8 @@ q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_he
  * chain: token i sees drafted tokens 0 .. i); out: dense, of `dtype`; lse: fp32
  * [batch, tokens, heads] or NULL.
  * Scores, the softmax's maximum and sum and the output's sums are held in 32
- * bits; probabilities are rounded to fp16 for the product with the values.
+ * bits; for the product with the values probabilities are rounded to fp16
+ * (bf16 outputs) or to two fp16 parts, 22 bits (fp16 outputs).
  * Cache rows that no token of the request sees may hold anything, and a drafted
  * token's scale that is not finite spoils the tokens that see it alone; value
  * scales below 2^-24 of the largest that the request's tokens see lose bits.  lens and counts are taken

@@ -35,9 +35,13 @@
 //    query's maximum, sum and rescaling are its lanes' own.
 //  * Values: lane (i, g) loads VB = DP / 16 bytes of each of four neighbouring keys
 //    and transposes them with the byte permutes that widen them.
-//  * Probabilities are rounded to fp16 for the second product (half a step is
-//    2^-12 of each, against 2^-9 or 2^-12 of the output's own rounding; the sum
-//    that divides them stays 32-bit).  The value's scale goes onto its
+//  * Probabilities go into the second product as fp16: with bf16 outputs
+//    rounded to it (half a step is 2^-12 of each, against 2^-9 of the output's own
+//    rounding), with fp16 outputs as two parts that hold 22 bits (rounded to
+//    one, the errors of the outputs against 64 bits are 1.42 to 1.47 times those of
+//    their own rounding, with two 1.00; 24-token trees x 16 x 4k 90.6 us against
+//    86.2, and nothing where the cache's bytes bound it).  The sum that divides them
+//    stays 32-bit.  The value's scale goes onto its
 //    probability, divided by a power of two near the largest scale so far and
 //    times 2^10: products up to 2^15 leave fp16's range below for weights down
 //    to 2^-34 of the largest, whatever the scales are.
@@ -49,7 +53,7 @@
 //    runs at 4.9).  Trees, the vector instructions that widen codes and form the
 //    softmax beside the matrix instructions, about three to one, at the two
 //    waves a SIMD that the registers leave: 24 tokens x 4 heads of a group x 16
-//    requests x 4k in 77 us and 11 for the join, 64 x 8 x 4 x 16k in 100 and 8
+//    requests x 4k in 81 us and 11 for the join, 64 x 8 x 4 x 16k in 100 and 8
 //    (four row tiles a wave, which halve the widening, spill and take 98).  One
 //    token over 700 keys is a chain of latencies (page table, keys, joins): 13 us.
 //  * A step's registers are loaded again for the next one as soon as it has
@@ -262,6 +266,7 @@ template <class T, int DP, int WAVES, int QT, int TL>
 __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs a) {
   constexpr int U = DP / 64, VB = DP / 16, R = 16 * QT, kStep = 16 * TL;
   constexpr bool kBf = std::is_same<T, Bfloat>::value;
+  constexpr int kParts = kBf ? 1 : 2;   // of a probability
   __shared__ __attribute__((aligned(16))) float merge[WAVES][R][DP];
   __shared__ float2 stats[WAVES][R];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -516,7 +521,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
     }
 #pragma unroll
     for (int t = 0; t < TL; ++t) vs[t] = vs[t] * inv_unit;
-    Frag p[QT][TL / 2];
+    Frag p[QT][TL / 2][kParts];
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
       // e = 2^(s - m)
@@ -584,8 +589,19 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
 #pragma unroll
           for (int r = 0; r < 4; ++r) x[r] = (seen >> (4 * t + r)) & 1 ? x[r] : 0.0f;
         }
-        p[i][t / 2].u[2 * (t % 2)] = pack_half(x[0], x[1]);
-        p[i][t / 2].u[2 * (t % 2) + 1] = pack_half(x[2], x[3]);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {   // each the rounding of what is left
+          const uint32_t p01 = pack_half(x[0], x[1]), p23 = pack_half(x[2], x[3]);
+          p[i][t / 2][h].u[2 * (t % 2)] = p01;
+          p[i][t / 2][h].u[2 * (t % 2) + 1] = p23;
+          if (h + 1 < kParts) {
+            const v2h h01 = __builtin_bit_cast(v2h, p01), h23 = __builtin_bit_cast(v2h, p23);
+            x[0] -= (float)h01[0];
+            x[1] -= (float)h01[1];
+            x[2] -= (float)h23[0];
+            x[3] -= (float)h23[1];
+          }
+        }
       }
     }
 #pragma unroll
@@ -607,7 +623,9 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
         }
 #pragma unroll
         for (int i = 0; i < QT; ++i)
-          o[i][w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.h, p[i][h].h, o[i][w], 0, 0, 0);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part)
+            o[i][w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.h, p[i][h][part].h, o[i][w], 0, 0, 0);
       }
     }
     if (more) {
