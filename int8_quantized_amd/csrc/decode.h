@@ -139,6 +139,7 @@ struct LoraArgs {
   bool relu;
   void* y;
   int y_type;
+  int64_t n0 = 0;           // first channel of a launch of the row kernel
   // t[m, r] = adapter_scale * s_in * sum_k A[r, k] (x[m, k] - zp) of the row's
   // adapter (0 past its rank), [M, rank_pad]; rows without one are not written.
   // With parts > 0, as that many bf16 values whose sum it is, [parts, M,

@@ -226,7 +226,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_lora_rows(LoraArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int64_t M = a.lin.M, N = a.lin.N, K = a.lin.K;
-  const int64_t n0 = (int64_t)blockIdx.x * BN, m0 = (int64_t)blockIdx.y * BM;
+  const int64_t n0 = a.n0 + (int64_t)blockIdx.x * BN, m0 = (int64_t)blockIdx.y * BM;
   const int8_t* wp[FN];
   const int8_t* xp[MT];
 #pragma unroll
@@ -355,20 +355,36 @@ __global__ __launch_bounds__(256) void k_pad_rows(const int8_t* __restrict__ src
   *reinterpret_cast<v4u*>(dst + i * 16) = v;
 }
 
+// A launch has fewer than 2^32 threads in x (more are cut off without an
+// error); what takes more goes in launches of up to this many.
+constexpr int64_t kMostThreads = (int64_t)1 << 31;
+
 hipError_t pad_rows(const void* src, int64_t rows, int64_t bytes, int64_t padded, int8_t* dst,
                     hipStream_t s) {
-  const int64_t n = rows * (padded / 16);
-  hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
-                     (const int8_t*)src, rows, bytes, padded, dst);
-  return hipGetLastError();
+  const int64_t most = kMostThreads / (padded / 16);   // (a row of 2^31 bytes is 2^27 chunks)
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    const int64_t part = rows - r0 < most ? rows - r0 : most, n = part * (padded / 16);
+    hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+                       (const int8_t*)src + r0 * bytes, part, bytes, padded, dst + r0 * padded);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <class AT, class YT, int MT, int FN, int WAVES, int D>
-hipError_t launch_shape(const LoraArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)((a.lin.N + 16 * FN - 1) / (16 * FN)),
-               (unsigned)((a.lin.M + 16 * MT - 1) / (16 * MT)));
-  hipLaunchKernelGGL((k_lora_rows<AT, YT, MT, FN, WAVES, D>), g, dim3(64 * WAVES), 0, s, a);
-  return hipGetLastError();
+hipError_t launch_shape(LoraArgs a, hipStream_t s) {
+  constexpr int64_t BN = 16 * FN, most = kMostThreads / (64 * WAVES);
+  const int64_t tiles = (a.lin.N + BN - 1) / BN;
+  for (int64_t t0 = 0; t0 < tiles; t0 += most) {
+    a.n0 = t0 * BN;
+    const dim3 g((unsigned)(tiles - t0 < most ? tiles - t0 : most),
+                 (unsigned)((a.lin.M + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL((k_lora_rows<AT, YT, MT, FN, WAVES, D>), g, dim3(64 * WAVES), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <class AT, class YT>
