@@ -665,7 +665,8 @@ q8ta_status q8ta_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
  * = 62 - ceil(log2 vocab), at most 50), so that the sums, and the token, do not depend on an
  * order.  -inf logits are never taken (NaN counts as -inf); +inf logits share the
  * weight alone; a row with nothing but -inf gets token -1 and logprob -inf.
- * u: in [0, 1); at 1 and beyond the last kept token is taken.
+ * u: in [0, 1); below 0 as 0; at 1 and beyond, and for a NaN, the last kept
+ * token of a weight above 0 is taken.
  * logits: [rows, vocab] of `dtype`, rows row_stride elements apart;
  * temperature, top_p, min_p, u fp32 [rows]; top_k int32 [rows]; tokens int32 [rows];
  * logprobs fp32 [rows] or NULL.  Requirements: rows >= 0 (0 is a no-op), 1 <=

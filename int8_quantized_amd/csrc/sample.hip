@@ -58,6 +58,13 @@ __device__ __forceinline__ float logit(const T* row, int i) {
   return x != x ? -INFINITY : x;
 }
 
+// The row's number: below 0 as 0 (no sum is below a negative goal); a NaN stays and
+// passes no sum, as numbers from 1 on.
+__device__ __forceinline__ double number_of(const SampleArgs& a, int row) {
+  const float u = a.u[row];
+  return u < 0.0f ? 0.0 : (double)u;
+}
+
 struct Row {
   double top, inv_t;   // largest logit, 1 / temperature
   double scale;        // log2(e) / temperature
@@ -346,7 +353,7 @@ __device__ void sample_any(const SampleArgs& a, Shared& sh, float mx) {
         all += mass(w, left);
         left -= counts[w] < left ? counts[w] : left;
       }
-      goal = (double)a.u[blockIdx.x] * (double)all;
+      goal = number_of(a, blockIdx.x) * (double)all;
     }
     int pick = -1;
     u64 pick_base = base, run = base;
@@ -947,7 +954,7 @@ __global__ __launch_bounds__(kNT) void k_sample_pick(SampleArgs a, Plan p) {
   const Settings s = settings_of(a, row);
   const float mx = st->mx;
   const int n_cand = st->n_cand;
-  const double u = (double)a.u[row];
+  const double u = number_of(a, row);
   auto put = [&](int token, float logprob) {
     a.tokens[row] = token;
     if (a.logprobs) a.logprobs[row] = logprob;
