@@ -234,26 +234,40 @@ constexpr size_t kWsGrain = (size_t)1 << 20;
 // A cached workspace buffer.  While `busy` it belongs to one call (between its
 // workspace_acquire and workspace_release); `done` is recorded on that call's
 // stream at release, after the call's kernels, so that the next holder --
-// on any stream -- is ordered after them.  The default stream is never
-// destroyed, so after a call on it (on_default) the event is recorded only when
-// another stream takes the buffer; calls that follow one another on the
-// default stream need none (recording and waiting cost a short call ~5 us of
-// its ~10).
+// on any stream -- is ordered after them and after nothing else.  The default
+// stream is never destroyed, so calls that follow one another on it need no
+// event (recording and waiting cost a short call ~5 us of its ~10): none is
+// recorded there until another stream has found no buffer of its own
+// (shared), and a buffer without one (!recorded) stays the default stream's.
 struct WsSlot {
   void* ptr = nullptr;
   size_t bytes = 0;
   hipEvent_t done = nullptr;
+  hipStream_t stream = nullptr;   // of the last use
+  bool recorded = false;          // done holds the last use
   bool busy = false;
-  bool on_default = false;
 };
 struct WsDevice {
   WsSlot slot[kWsSlots];
+  bool shared = false;            // there are more streams than buffers
 };
 
 // Guards the slot tables only (lookups and flag updates); never held across
 // a HIP call that waits or launches.
 std::mutex g_ws_mu;
 std::map<int, WsDevice> g_ws;
+
+// How well a free buffer suits a call on stream s, smaller is better: the
+// stream's own, which it need not wait for (one that fits, else one to grow), a
+// slot without a buffer, then another stream's; -1: not at all.
+constexpr int kWsNew = 2;   // rank of a slot without a buffer
+int ws_rank(const WsSlot& c, size_t bytes, hipStream_t s) {
+  if (c.busy) return -1;
+  if (!c.ptr) return kWsNew;
+  const bool own = c.stream == s;
+  if (!c.recorded && !(own && s == nullptr)) return -1;
+  return (own ? 0 : kWsNew + 1) + (c.bytes >= bytes ? 0 : 1);
+}
 
 }  // namespace
 
@@ -279,13 +293,16 @@ hipError_t workspace_acquire(void** p, size_t bytes, hipStream_t s) {
   {
     std::lock_guard<std::mutex> g(g_ws_mu);
     WsDevice& d = g_ws[dev];
-    // the smallest free buffer that fits, else the largest free one (to grow)
+    int best = -1;
     for (WsSlot& c : d.slot) {
-      if (c.busy) continue;
-      if (!sl) { sl = &c; continue; }
-      const bool c_fits = c.bytes >= bytes, s_fits = sl->bytes >= bytes;
-      if (c_fits ? (!s_fits || c.bytes < sl->bytes) : (!s_fits && c.bytes > sl->bytes)) sl = &c;
+      const int rank = ws_rank(c, bytes, s);
+      // of one rank the smallest that fits, or the largest to grow
+      if (rank < 0 || (sl && rank > best)) continue;
+      if (sl && rank == best && (c.bytes >= bytes ? c.bytes >= sl->bytes : c.bytes <= sl->bytes)) continue;
+      sl = &c;
+      best = rank;
     }
+    if (best < 0 || best > kWsNew) d.shared = true;
     if (sl) {
       sl->busy = true;
       mine = *sl;
@@ -294,13 +311,8 @@ hipError_t workspace_acquire(void** p, size_t bytes, hipStream_t s) {
   if (!sl) return pool_alloc(p, bytes, s);
 
   if (!mine.done) e = hipEventCreateWithFlags(&mine.done, hipEventDisableTiming);
-  if (e == hipSuccess && mine.ptr && mine.on_default) {
-    if (s != nullptr) {
-      e = hipEventRecord(mine.done, nullptr);
-      if (e == hipSuccess) e = hipStreamWaitEvent(s, mine.done, 0);
-    }
-  } else if (e == hipSuccess && mine.ptr) {
-    const hipError_t q = hipEventQuery(mine.done);   // never recorded: hipSuccess
+  if (e == hipSuccess && mine.ptr && mine.recorded && !(s == nullptr && mine.stream == nullptr)) {
+    const hipError_t q = hipEventQuery(mine.done);
     if (q == hipErrorNotReady) e = hipStreamWaitEvent(s, mine.done, 0);
     else if (q != hipSuccess) e = q;
   }
@@ -328,14 +340,15 @@ hipError_t workspace_acquire(void** p, size_t bytes, hipStream_t s) {
 }
 
 // Returns a buffer from workspace_acquire once the call's kernels are queued
-// on s: a cached one is marked free after its event is recorded on s, any
-// other is freed in stream order.
+// on s: a cached one is marked free after its event is recorded on s (where one
+// is needed), any other is freed in stream order.
 hipError_t workspace_release(void* p, hipStream_t s) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   WsSlot* sl = nullptr;
   hipEvent_t done = nullptr;
+  bool record = s != nullptr;
   {
     std::lock_guard<std::mutex> g(g_ws_mu);
     auto it = g_ws.find(dev);
@@ -344,13 +357,15 @@ hipError_t workspace_release(void* p, hipStream_t s) {
         if (c.busy && c.ptr == p) {
           sl = &c;
           done = c.done;
+          record = record || it->second.shared;
           break;
         }
   }
   if (!sl) return p ? hipFreeAsync(p, s) : hipSuccess;
-  if (s != nullptr) e = hipEventRecord(done, s);
+  if (record) e = hipEventRecord(done, s);
   std::lock_guard<std::mutex> g(g_ws_mu);
-  sl->on_default = s == nullptr;
+  sl->stream = s;
+  sl->recorded = record && e == hipSuccess;
   sl->busy = false;
   return e;
 }

@@ -38,3 +38,63 @@ def test_linear_lora_copies_hold_every_row():
         chunks = sum(math.ceil(n * kp * e / 16 / 256) for n, e in ((M, 1), (N, 1), (2 * 8, 2)))
         assert all(g[0] * g[3] < 2 ** 32 for g in pads)
         assert chunks <= sum(g[0] for g in pads) <= chunks + len(pads)
+
+
+# q8ta_linear_lora takes a workspace on every call: its waits are those of the workspaces.
+WORK = LORA + """
+A, B, C, D, E = (ctypes.c_void_p(v << 12) for v in range(1, 6))
+def call(s, M=4):
+    rc, lines = lora(M, 64, 64, s=s)
+    assert rc == 0
+    return [x for x in lines if x[0] != "launch"]
+"""
+
+
+def test_workspace_calls_on_the_default_stream_need_no_events():
+    got = recorded(WORK + "result = [call(None) for _ in range(4)] + [call(None, M=1 << 16), call(None)]")
+    assert [x[0] for x in got[0]] == ["malloc"] and got[1:4] == [[], [], []]
+    assert [x[0] for x in got[4]] == ["free", "malloc"] and got[5] == []      # grown, in the stream's order
+
+
+def test_workspace_of_a_side_stream_leaves_the_default_stream_alone():
+    """No call on a side stream records on the default stream or waits for it as a whole."""
+    got = recorded(WORK + """
+rec.recorder_pending(1)     # everything queued is still running
+result = [call(None), call(A), call(A), call(None), call(B), call(None)]""")
+    none = "(nil)"
+    assert not any(x[0] in ("record", "wait") and x[2] == none for part in (got[1], got[2], got[4]) for x in part)
+    assert [x[0] for x in got[1]] == ["malloc", "record"] and got[1][1][2] == "0x1000"
+    assert not any(x[0] == "malloc" for x in got[2])                  # its own buffer again
+    assert [x[0] for x in got[4]] == ["malloc", "record"]
+    assert got[3] == got[5] == []                                     # the default stream needs none still
+
+
+def test_workspace_shared_by_more_streams_than_buffers():
+    """With every buffer in some stream's name, a further stream waits for one use of one of them."""
+    got = recorded(WORK + """
+rec.recorder_pending(1)
+result = [call(s) for s in (A, None, B, C, D, D, None, None, E, E)]""")
+    assert [x[0] for x in got[4]] == ["query", "wait", "record"]
+    assert got[4][1][1] == got[4][0][1] and got[4][1][2] == got[4][2][2] == "0x4000"
+    assert [x[0] for x in got[5]] == ["query", "wait", "record"]
+    # from then on the default stream records its uses too (without waiting for its own)
+    assert [(x[0], x[2]) for x in got[6] + got[7]] == [("record", "(nil)")] * 2
+    # released on a side stream, an event is waited for by whoever comes next
+    got = recorded(WORK + "result = [call(s) for s in (None, A, B, C, D)]")
+    assert [x[0] for x in got[4]] == ["query", "record"]               # (ready: no wait)
+
+
+def test_workspace_of_the_default_stream_without_an_event_is_not_handed_on():
+    """Its event (the first) is neither recorded for nor asked for by another stream."""
+    got = recorded(WORK + "result = [call(s) for s in (None, A, B, C, D, E)]")
+    events = [[x[1] for x in part if x[0] in ("record", "query", "wait")] for part in got]
+    assert events[0] == [] and all(part and "0x1" not in part for part in events[1:])
+
+
+def test_workspace_under_capture_is_the_calls_own():
+    got = recorded(WORK + """
+call(None)
+rec.recorder_capture(1)
+result = [call(A), call(None)]""")
+    for part in got:
+        assert [x[0] for x in part] == ["malloc", "free"] and part[0][1] == part[1][1]
