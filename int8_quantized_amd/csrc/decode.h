@@ -124,6 +124,8 @@ struct SampleArgs {
 };
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
 
+constexpr int kLoraParts = 3;   // 3 x 8 bits and their signs hold fp32's 24
+
 // The linear with low-rank adapters: lin holds x, w, the scales, bias, sizes
 // and the input zero point (lin.rq.s_in the input scale); row m adds
 // adapter_scale * B (A (x - zp) s_in) of adapter ids[m].
@@ -142,11 +144,11 @@ struct LoraArgs {
   int64_t n0 = 0;           // first channel of a launch of the row kernel
   // t[m, r] = adapter_scale * s_in * sum_k A[r, k] (x[m, k] - zp) of the row's
   // adapter (0 past its rank), [M, rank_pad]; rows without one are not written.
-  // With parts > 0, as that many bf16 values whose sum it is, [parts, M,
+  // With in_parts, as kLoraParts bf16 values whose sum it is, [kLoraParts, M,
   // rank_pad], instead.
   float* t = nullptr;
   uint16_t* tp = nullptr;
-  int parts = 0;
+  bool in_parts = false;
 };
 // The adapter of row m, -1 for none (any id outside [0, adapters)).
 __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t m) {

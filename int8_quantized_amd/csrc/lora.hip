@@ -159,10 +159,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
         const float f = a.lin.rq.s_in * (a.ad_scales ? a.ad_scales[ad] : 1.0f);
         const int64_t at = (m0 + row) * a.rank_pad + r0 + r;
         float t = r0 + r < rank ? s * f : 0.0f;
-        if (a.parts == 0) {
+        if (!a.in_parts) {
           a.t[at] = t;
         } else {
-          for (int q = 0; q < a.parts; ++q) {   // each the rounding of what is left
+          for (int q = 0; q < kLoraParts; ++q) {   // each the rounding of what is left
             const Bfloat h = from_float<Bfloat>(t);
             a.tp[q * M * a.rank_pad + at] = h.bits;
             t = t - to_float(h);
@@ -466,9 +466,9 @@ hipError_t launch_linear_lora(LoraArgs a, hipStream_t s) {
   const bool pad = K % 16 != 0 ||
                    (((uintptr_t)a.lin.x | (uintptr_t)a.lin.w | (uintptr_t)a.a) & 15) != 0;
   const char product = product_of(pad ? whole : a.lin);
-  a.parts = product == 'r' ? 0 : (a.y_type == Q8TA_F32 ? 3 : 2);
+  a.in_parts = product != 'r';
   const size_t t_bytes =
-      ((size_t)M * a.rank_pad * (a.parts ? 2 * a.parts : 4) + 255) / 256 * 256;
+      ((size_t)M * a.rank_pad * (a.in_parts ? 2 * kLoraParts : 4) + 255) / 256 * 256;
   const size_t bytes = t_bytes + (pad ? (size_t)(M + N + 2 * at) * kp : 0);
   void* ws = nullptr;
   hipError_t e = workspace_acquire(&ws, bytes, s);

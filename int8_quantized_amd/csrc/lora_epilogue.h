@@ -70,17 +70,17 @@ __device__ __forceinline__ uint32_t not_finite(const lora_v4u& w) {
 
 // y += t B^T for the 64 rows and 32 * FN channels of a wave's fragments.  The
 // rows' adapters are taken one after the other; rows of another adapter have a
-// t of zero.  t comes as P bf16 parts (its rounding to 2^-17 for two, 2^-25 for
-// three), B goes on as one part where it is bf16 and as two, which hold all of
-// its 11 bits, where it is fp16: bf16 has fp32's range, so t needs no scaling.
-// Products of parts beyond 2^-8P of the whole are left out.  Operands come
-// straight from memory (16 bytes a lane), those of H blocks of 16 ranks at once
-// (as many as fit the registers beside the sums).
-template <class AT, int P, int FN>
+// t of zero.  t comes as three bf16 parts, which hold all of its 24 bits (two hold
+// 17: 2048 x 4096 x 11008 with rank 64 3 us less of 151, but outputs whose rank
+// terms cancel are off by up to 70 times what 32 bits leave), B goes on as one part where it is bf16
+// and as two, which hold all of its 11 bits, where it is fp16: bf16 has fp32's
+// range, so t needs no scaling.  Products of parts below 2^-24 of the whole are
+// left out.  Operands come straight from memory (16 bytes a lane).
+template <class AT, int FN>
 __device__ __forceinline__ void lora_add(const LoraArgs& l, lora_v16f (&y)[FN][2], int64_t row0,
                                          int64_t ch0, int lane) {
   constexpr int Q = std::is_same<AT, Half>::value ? 2 : 1;
-  constexpr int H = P == 2 ? 2 : 1;
+  constexpr int P = kLoraParts;
   const int lrow = lane & 31, kg = lane >> 5;
   const int64_t N = l.lin.N, plane = l.lin.M * l.rank_pad;
   const bool vec = l.rank % 8 == 0 && ((uintptr_t)l.b & 15) == 0;
@@ -96,70 +96,58 @@ __device__ __forceinline__ void lora_add(const LoraArgs& l, lora_v16f (&y)[FN][2
     const uint16_t* t = l.tp + (row0 + lrow) * l.rank_pad + 8 * kg;
     const bool in0 = (mine >> lrow) & 1, in1 = (mine >> (32 + lrow)) & 1;
     uint32_t odd = 0;   // bit i: this lane's channel of fragment i has such a value
-    for (int r0 = 0; r0 < rank; r0 += 16 * H) {
-      lora_v4u tf[H][2][P], w[H][FN];
+    for (int r0 = 0; r0 < rank; r0 += 16) {
+      lora_v4u tf[2][P], w[FN];
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const bool more = r0 + 16 * h < rank;   // rank_pad holds the block
+      for (int p = 0; p < P; ++p) {
+        tf[0][p] = zero;
+        tf[1][p] = zero;
+        if (in0) tf[0][p] = *reinterpret_cast<const lora_v4u*>(t + p * plane + r0);
+        if (in1) tf[1][p] = *reinterpret_cast<const lora_v4u*>(t + p * plane + 32 * l.rank_pad + r0);
+      }
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          tf[h][0][p] = zero;
-          tf[h][1][p] = zero;
-          if (more && in0) tf[h][0][p] = *reinterpret_cast<const lora_v4u*>(t + p * plane + r0 + 16 * h);
-          if (more && in1)
-            tf[h][1][p] = *reinterpret_cast<const lora_v4u*>(t + p * plane + 32 * l.rank_pad + r0 + 16 * h);
-        }
-#pragma unroll
-        for (int i = 0; i < FN; ++i) {
-          const int64_t n = ch0 + 32 * i + lrow < N ? ch0 + 32 * i + lrow : N - 1;
-          w[h][i] = lora_b8<AT>(bb + n * l.rank, r0 + 16 * h + 8 * kg, rank, vec);
-        }
+      for (int i = 0; i < FN; ++i) {
+        const int64_t n = ch0 + 32 * i + lrow < N ? ch0 + 32 * i + lrow : N - 1;
+        w[i] = lora_b8<AT>(bb + n * l.rank, r0 + 8 * kg, rank, vec);
       }
       // a value that is not finite would spoil the tile's rows of other
       // adapters (0 * inf): left out here, and its own rows become NaN below
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-#pragma unroll
-        for (int i = 0; i < FN; ++i) {
-          const uint32_t bad = not_finite<AT>(w[h][i]);
-          if (__any(bad != 0)) {
-            if (bad) w[h][i] = zero;
-            odd |= bad ? 1u << i : 0u;
-          }
+      for (int i = 0; i < FN; ++i) {
+        const uint32_t bad = not_finite<AT>(w[i]);
+        if (__any(bad != 0)) {
+          if (bad) w[i] = zero;
+          odd |= bad ? 1u << i : 0u;
         }
       }
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        if (r0 + 16 * h >= rank) break;
+      for (int i = 0; i < FN; ++i) {
+        lora_v4u bf[Q];
+        if constexpr (Q == 1) {
+          bf[0] = w[i];
+        } else {
 #pragma unroll
-        for (int i = 0; i < FN; ++i) {
-          lora_v4u bf[Q];
-          if constexpr (Q == 1) {
-            bf[0] = w[h][i];
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t pair = w[h][i][e];
-              const float lo = to_float(Half{(uint16_t)pair});
-              const float hi = to_float(Half{(uint16_t)(pair >> 16)});
-              const Bfloat l0 = from_float<Bfloat>(lo), h0 = from_float<Bfloat>(hi);
-              const Bfloat l1 = from_float<Bfloat>(lo - to_float(l0));
-              const Bfloat h1 = from_float<Bfloat>(hi - to_float(h0));
-              bf[0][e] = (uint32_t)l0.bits | (uint32_t)h0.bits << 16;
-              bf[1][e] = (uint32_t)l1.bits | (uint32_t)h1.bits << 16;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t pair = w[i][e];
+            const float lo = to_float(Half{(uint16_t)pair});
+            const float hi = to_float(Half{(uint16_t)(pair >> 16)});
+            const Bfloat l0 = from_float<Bfloat>(lo), h0 = from_float<Bfloat>(hi);
+            const Bfloat l1 = from_float<Bfloat>(lo - to_float(l0));
+            const Bfloat h1 = from_float<Bfloat>(hi - to_float(h0));
+            bf[0][e] = (uint32_t)l0.bits | (uint32_t)h0.bits << 16;
+            bf[1][e] = (uint32_t)l1.bits | (uint32_t)h1.bits << 16;
           }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-              for (int q = 0; q < Q && p + q < P; ++q) {
-                const lora_v4u tv = tf[h][j][p], bv = bf[q];
-                y[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(lora_v8b, tv), __builtin_bit_cast(lora_v8b, bv), y[i][j], 0, 0, 0);
-              }
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int q = 0; q < Q && p + q < P; ++q) {
+              const lora_v4u tv = tf[j][p], bv = bf[q];
+              y[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(lora_v8b, tv), __builtin_bit_cast(lora_v8b, bv), y[i][j], 0, 0, 0);
+            }
       }
     }
     if (__any(odd != 0)) {
@@ -239,7 +227,7 @@ __device__ __forceinline__ void lora_finish(const LoraArgs& l, const lora_v16i (
         v = v * sc[i];
         y[i][j][r] = v + bi[i];
       }
-  lora_add<AT, std::is_same<YT, float>::value ? 3 : 2>(l, y, row0, ch0, lane);
+  lora_add<AT>(l, y, row0, ch0, lane);
   lora_put<YT>(l, y, row0, ch0, lane);
 }
 
