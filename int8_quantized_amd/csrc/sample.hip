@@ -1223,7 +1223,8 @@ __global__ __launch_bounds__(kNT) void k_sample_long(SampleArgs a) {
   sample_any<T>(a, sh, mx);
 }
 
-constexpr int kBatch = 1024;   // rows of a launch
+constexpr int kBatch = 1024;   // rows of a launch, and bytes of its workspace (110 MB in whole MiB), at most
+constexpr int kWorkspace = 104 << 20;
 
 template <class T>
 hipError_t launch_type(const SampleArgs& all, hipStream_t s) {
@@ -1232,7 +1233,7 @@ hipError_t launch_type(const SampleArgs& all, hipStream_t s) {
   p.loads = (all.vocab + N - 1) / N;
   while (((p.loads - 1) >> p.group_log) + 1 > kGroups) ++p.group_log;
   const bool is_long = p.group_log > 6;
-  const int batch = all.rows < kBatch ? all.rows : kBatch;
+  int batch = all.rows < kBatch ? all.rows : kBatch;
   void* ws = nullptr;
   if (!is_long) {
     p.groups = ((p.loads - 1) >> p.group_log) + 1;
@@ -1249,6 +1250,7 @@ hipError_t launch_type(const SampleArgs& all, hipStream_t s) {
     p.at_bins = p.at_sums + up(p.stretches * 8);
     p.at_cand = p.at_bins + p.parts * kSlot * 8;
     p.row_bytes = p.at_cand + kCand * 8;
+    batch = batch < kWorkspace / p.row_bytes ? batch : kWorkspace / p.row_bytes;
     const hipError_t e = workspace_acquire(&ws, (size_t)batch * p.row_bytes, s);
     if (e != hipSuccess) return e;
     p.ws = (char*)ws;

@@ -98,3 +98,37 @@ rec.recorder_capture(1)
 result = [call(A), call(None)]""")
     for part in got:
         assert [x[0] for x in part] == ["malloc", "free"] and part[0][1] == part[1][1]
+
+
+def test_sample_workspace_is_what_the_header_states():
+    """0.05 to 0.7 MB a row and 110 MB at most (with a cached buffer's rounding), whatever the rows,
+    the vocabulary and the type; every launch group holds all its rows."""
+    rows = [1, 2, 63, 64, 65, 300, 1000, 1022, 1023, 1024, 1025, 2047, 2048, 5000]
+    vocabs = [1, 33, 1000, 32000, 100003, 131072, 262144, 262145, 500000, (1 << 20) - 1, 1 << 20, (1 << 20) + 1,
+              1 << 21, (1 << 21) + 1, 1 << 24]
+    cases = [(b, v, t) for b in rows for v in vocabs for t in (0, 2)]
+    got = recorded("""
+def sample(rows, vocab, dtype):
+    rc = l.q8ta_sample(F, vocab, dtype, rows, vocab, F, F, F, F, F, F, F, None)
+    return rc, calls()
+result = []
+for c in %r:
+    rec.recorder_capture(1)      # the call's own allocation, as large as it asks for
+    own = sample(*c)
+    rec.recorder_capture(0)
+    result.append((own, sample(*c)))""" % cases)
+    cached = 0
+    for (b, v, t), ((rc, own), (rc2, lines)) in zip(cases, got):
+        assert rc == rc2 == 0
+        n = 16 // (4 if t == 0 else 2)
+        picks = launches(own, "k_sample_pick") + launches(own, "k_sample_long")
+        assert sum(g[0] for g in picks) == b
+        size = [int(x[2]) for x in own if x[0] == "malloc"]
+        if v > n << 18:
+            assert size == []
+        else:
+            batch = max(g[0] for g in picks)
+            assert 0.05e6 <= size[0] / batch <= 0.7e6 and size[0] <= 110e6, (b, v, t, size)
+        cached += sum(int(x[2]) for x in lines if x[0] == "malloc")
+        assert all(int(x[2]) <= 110e6 for x in lines if x[0] == "malloc"), (b, v, t, lines)
+    assert cached > 0
