@@ -1,4 +1,4 @@
-"""q8ta_tree_attention: the precision of its probabilities.
+"""q8ta_tree_attention: the precision of its probabilities, many requests, queries at odd addresses.
 
 With fp16 outputs a probability is held in two fp16 parts (2^-22 of it) and everything else in 32
 bits, so that an output is off by its own rounding and little else: the tests below leave half a step
@@ -7,7 +7,8 @@ of the type, and of sums over n keys (n / 8 + 64) * 2^-24 of sum |p v|.
 import numpy as np
 import pytest
 
-from test_tree_attention import make, definition, run
+import int8_quantized_amd as q8
+from test_tree_attention import check, definition, make, run
 
 torch = pytest.importorskip("torch")
 
@@ -54,3 +55,50 @@ def test_tree_attention_fp16_error_is_that_of_rounding_the_exact_outputs(size):
     got = run(c)[0].double().cpu().numpy()
     rounded = want.astype(np.float16).astype(np.float64)
     assert np.linalg.norm(got - want) <= 1.05 * np.linalg.norm(rounded - want)
+
+
+def ragged(B, most, seed):
+    """Context lengths of B requests, one in five of them none."""
+    g = np.random.default_rng(seed)
+    n = g.integers(1, most, B)
+    n[g.permutation(B)[:B // 5]] = 0
+    return n.tolist()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [63, 64, 65, 128, 130, 200])
+@pytest.mark.parametrize("T,hk,most,spare", [(1, 2, 300, 1), (3, 1, 150, 90), (20, 1, 120, 1), (1, 1, 90, 1)])
+def test_tree_attention_more_requests_than_a_round(B, T, hk, most, spare):
+    """The requests' lengths are summed 64 at a time: units that are cut across those borders, and the
+    forms without cuts (the first and the last)."""
+    c = make(B, T, 2 * hk, hk, 64, 16, ragged(B, most, B + T), seed=B, spare=spare,
+             counts=[(T * 7 + b) % (T + 1) for b in range(B)] if T > 1 else None)
+    check(c)
+
+
+@pytest.mark.gpu
+def test_tree_attention_requests_of_very_different_length():
+    """One long request among 150 short and empty ones: most of the runs are its own."""
+    n = ragged(150, 20, 3)
+    n[97] = 9000
+    check(make(150, 1, 4, 1, 64, 64, n, seed=6))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("T,d,hq,odd", [(1, 64, 4, 1), (5, 128, 8, 3), (20, 80, 4, 7), (2, 256, 4, 5), (1, 64, 4, 8)])
+def test_tree_attention_queries_at_odd_addresses_and_strides(T, d, hq, odd, dtype):
+    """Rows that do not start on 16 bytes, heads and tokens an odd number of elements apart."""
+    c = make(2, T, hq, 2, d, 16, [70, 9], seed=T + d, dtype=dtype)
+    out, lse = check(c)
+    q = c["q"].cuda()
+    B, (heads, tokens) = 2, (d + odd, (hq + 1) * (d + odd) + odd)
+    flat = torch.full((odd + B * T * tokens + 1000,), 3.0, dtype=q.dtype, device="cuda")
+    view = flat[odd:].as_strided((B, T, hq, d), (T * tokens, tokens, heads, 1))
+    view.copy_(q)
+    assert torch.equal(view, q)
+    dev = {k: None if v is None else torch.from_numpy(v).cuda() for k, v in c.items() if k not in ("q", "scale")}
+    again, lse2 = torch.empty_like(out), torch.empty_like(lse)
+    q8.q8ta_tree_attention(view, dev["cache"], dev["scales"], dev["table"], dev["lens"], dev["counts"],
+                           dev["mask"], c["scale"], again, lse2)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
