@@ -580,7 +580,7 @@ q8ta_status q8ta_linear_lora(const int8_t* x, int64_t M, int64_t K, double input
  * 64 bits, the pair p of each query and key head's first rot elements,
  *   (x[p], x[rot/2 + p])  or, interleaved,  (x[2p], x[2p + 1]) = (a, b),
  * becomes factor * (a cos - b sin, b cos + a sin); elements past rot stay.
- *   q_out = the turned queries, rounded once to the type;
+ *   q_out = the turned queries, rounded to fp32 and from there to the type;
  *   cache row of slots[t]: keys turned, values as they are, each head's row
  *   of dim elements with scale = amax / 127 (rounded to fp32) and codes
  *   rint(x * 127 / amax) (all 0 for a row of zeros), formed in 64 bits.
