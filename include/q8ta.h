@@ -591,12 +591,13 @@ q8ta_status q8ta_linear_lora(const int8_t* x, int64_t M, int64_t K, double input
  * layout), finite; interleaved: 0 or 1; q_out dense [tokens, heads, dim], may
  * be q itself where that is dense.
  * A slot outside [0, pages * page_size) stores nothing for its token (padding
- * tokens: -1); slots that appear twice leave either token's row.  tokens == 0
- * is a no-op.  Requirements: heads, kv_heads, dim, pages, page_size >= 1, dim
- * <= 65536, heads + 2 * kv_heads <= 65535, rot even in [0, dim] (inv_freq may
- * be NULL for 0), tokens < 2^31.  Any alignment; dim % 8 == 0 and rot % 8 == 0
- * up to dim 512 with strides of whole groups of four elements and bases
- * aligned to such groups take the vector kernel.
+ * tokens: -1).  A slot of the cache stands at most once in slots: tokens with one
+ * slot are stored at the same time, and its rows end up with bytes of one and
+ * of the other.  tokens == 0 is a no-op.  Requirements: heads, kv_heads, dim,
+ * pages, page_size >= 1, dim <= 65536, heads + 2 * kv_heads <= 65535, rot even
+ * in [0, dim] (inv_freq may be NULL for 0), tokens < 2^31.  Any alignment; dim %
+ * 8 == 0 and rot % 8 == 0 up to dim 512 with strides of whole groups of four
+ * elements and bases aligned to such groups take the vector kernel.
  */
 q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                              const void* k, int64_t k_token_stride, int64_t k_head_stride,

@@ -613,7 +613,7 @@ def q8ta_rope_append(q, k, v, positions, slots, inv_freq, factor, interleaved, q
     """Rotary positions on q and k, and the append of k and v to the paged int8 cache.
 
     q [T, heads, dim], k and v [T, kv_heads, dim] (fp32, fp16 or bf16, any token and head
-    strides), positions int32 [T], slots int64 [T] (negative: not stored), inv_freq fp64
+    strides), positions int32 [T], slots int64 [T] (negative: not stored, else each once), inv_freq fp64
     [rot / 2]; q_out like q, dense; cache int8 [pages, 2, kv_heads, page, dim] and cache_scales
     fp32 [pages, 2, kv_heads, page].  ``interleaved`` pairs neighbours, else the two halves of
     the rotated part; ``factor`` multiplies cos and sin.  Returns q_out."""
