@@ -295,7 +295,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
   const int kvh = unit_at / a.row_blocks, row0 = (unit_at - kvh * a.row_blocks) * R;
   const Span sp = span_of(a, b);
   const int k_begin = g0 * a.grain;
-  const int k_end = sp.total - k_begin < (g1 - g0) * a.grain ? sp.total : g1 * a.grain;
+  const int k_end = grains_end(sp.total, of_b, a.grain, g1);
   const bool whole = g0 == 0 && g1 == of_b;
   const int64_t slot = 2 * run + (g0 == 0 ? 1 : 0);
 

@@ -34,6 +34,12 @@ __host__ __device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv&
   return (uint32_t)(((uint64_t)n * f.mul) >> f.shift);
 }
 
+// Where the keys of a request's grains up to g1 (not included) end: `total` keys
+// in `grains` grains of `grain`.  (The last grain's end may pass 2^31.)
+__host__ __device__ __forceinline__ int grains_end(int total, int grains, int grain, int g1) {
+  return g1 == grains ? total : g1 * grain;
+}
+
 // 16-bit floating-point values by their bits.
 struct Half {
   uint16_t bits;
