@@ -560,11 +560,11 @@ q8ta_status q8ta_conv2d_acc(const int8_t* x, int64_t N, int64_t IC,
  * not read as numbers (an adapter value that is not finite makes outputs of its
  * own rows not finite, and no others); adapter_ids: int32 [M]; out: dense [M, N] of
  * out_dtype.  Requirements: as for q8ta_linear, M <= 2^21, N and K <= 2^30,
- * 1 <= rank <= 512, 1 <= adapters <= 2^24.  Any K and alignment: where K is no
- * multiple of 16 or x, weight or lora_a are not 16-byte aligned, they are first
- * copied into rows that are (workspace: (M + N + 2 * adapters * rank) * K bytes, K rounded up to
- * 64).  Workspace otherwise: up to 6 bytes for each row and rank (rounded
- * up to 16).
+ * 1 <= rank <= 512, 1 <= adapters <= 2^24, the elements of each tensor <= 2^40.
+ * Any K and alignment: where K is no multiple of 16 or x, weight or lora_a are
+ * not 16-byte aligned, they are first copied into rows that are (workspace:
+ * (M + N + 2 * adapters * rank) * K bytes, K rounded up to 64).  Workspace
+ * otherwise: up to 6 bytes for each row and rank (rounded up to 16).
  */
 q8ta_status q8ta_linear_lora(const int8_t* x, int64_t M, int64_t K, double input_scale,
                              int64_t input_zero_point, const int8_t* weight, int64_t N,
@@ -595,7 +595,8 @@ q8ta_status q8ta_linear_lora(const int8_t* x, int64_t M, int64_t K, double input
  * slot are stored at the same time, and its rows end up with bytes of one and
  * of the other.  tokens == 0 is a no-op.  Requirements: heads, kv_heads, dim,
  * pages, page_size >= 1, dim <= 65536, heads + 2 * kv_heads <= 65535, rot even
- * in [0, dim] (inv_freq may be NULL for 0), tokens < 2^31.  Any alignment; dim %
+ * in [0, dim] (inv_freq may be NULL for 0), tokens < 2^31, tokens * heads * dim
+ * and the cache's elements <= 2^40.  Any alignment; dim %
  * 8 == 0 and rot % 8 == 0 up to dim 512 with strides of whole groups of four
  * elements and bases aligned to such groups take the vector kernel.
  */
@@ -634,11 +635,12 @@ q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_he
  * into [0, table_pages * page_size] and [0, tokens], keys past the table's pages
  * are not there, and a page number outside [0, pages) makes its keys unseen.
  * Requirements: batch, tokens, heads, kv_heads, dim, pages, page_size and
- * table_pages >= 1, tokens <= 64, heads a multiple of kv_heads, batch <= 65535,
- * batch * kv_heads * ceil(tokens * heads / kv_heads / 16) <= 2^29,
- * table_pages * page_size <= 2^31 - 1024, softmax_scale finite and > 0
- * (Q8TA_ERR_QPARAM); dim a multiple of 16 up to 256, page_size a multiple of
- * 16 and 16-byte aligned cache and cache_scales (else Q8TA_ERR_UNSUPPORTED).
+ * table_pages >= 1, tokens <= 64, heads <= 65535 and a multiple of kv_heads,
+ * batch <= 65535, r = kv_heads * ceil(tokens * heads / kv_heads / 16) <= 65535,
+ * batch * r <= 2^29, table_pages * page_size <= 2^31 - 1024, the cache's elements
+ * <= 2^40, softmax_scale finite and > 0 (Q8TA_ERR_QPARAM); dim a multiple of 16
+ * up to 256, page_size a multiple of 16 and 16-byte aligned cache and
+ * cache_scales (else Q8TA_ERR_UNSUPPORTED).
  * batch == 0 is a no-op.  Workspace, but for caches of few keys: 4 * (dim +
  * 2) bytes for each of up to 32768 partial rows.
  */
