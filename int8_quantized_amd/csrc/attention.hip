@@ -121,9 +121,12 @@ __device__ __forceinline__ float finite_size(float x) {
   const float y = __builtin_fabsf(x);
   return y < __builtin_inff() ? y : 0.0f;
 }
-// Exponent of x >= 0, kept in [-110, 110].
+// Exponent of a finite x >= 0 (-127 for 0), and kept in [-110, 110].
+__device__ __forceinline__ int exponent_of(float x) {
+  return (int)(__builtin_bit_cast(uint32_t, x) >> 23) - 127;
+}
 __device__ __forceinline__ int unit_exponent(float x) {
-  const int e = (int)(__builtin_bit_cast(uint32_t, x) >> 23) - 127;
+  const int e = exponent_of(x);
   return e < -110 ? -110 : (e > 110 ? 110 : e);
 }
 
@@ -412,7 +415,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attn(AttnArgs
         top = __builtin_fmaxf(top, __shfl_xor(top, 16));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
         // (rows below 2^-40, whose scores are none, by as much as that)
-        const int e = unit_exponent(top), sh = 14 - (e < -40 ? -40 : e);
+        const int e = exponent_of(top), sh = 14 - (e < -40 ? -40 : e);
         up = pow2f(sh);
         less[i] = sh - last;
         last = sh;

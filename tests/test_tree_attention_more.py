@@ -102,3 +102,30 @@ def test_tree_attention_queries_at_odd_addresses_and_strides(T, d, hq, odd, dtyp
     q8.q8ta_tree_attention(view, dev["cache"], dev["scales"], dev["table"], dev["lens"], dev["counts"],
                            dev["mask"], c["scale"], again, lse2)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 20])
+def test_tree_attention_powers_of_two_move_from_keys_to_queries(T):
+    """Queries of any bf16 size: what a power of two takes from the keys' scales and gives to the queries
+    leaves every score, and so every bit, as it is."""
+    c = make(2, T, 4, 2, 64, 16, [300, 9], seed=31)
+    want = run(c)
+    for e in (-20, 60, 110, 116, 118):
+        moved = dict(c, q=(c["q"].float() * 2.0 ** e).to(c["q"].dtype), scales=c["scales"].copy())
+        moved["scales"][:, 0] *= np.float32(2.0 ** -e)
+        assert torch.isfinite(moved["q"].float()).all() and (moved["scales"][:, 0] > 2.0 ** -126).all()
+        got = run(moved)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), e
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("e", [-80, -30, 60, 84])
+def test_tree_attention_value_scales_over_the_stated_range(T, e):
+    """Powers of two on all value scales come out on the outputs, exactly."""
+    c = make(2, T, 4, 2, 64, 16, [900, 9], seed=32)
+    want, lse = run(c)
+    c["scales"][:, 1] *= np.float32(2.0 ** e)
+    got, lse2 = run(c)
+    assert torch.equal(got.double(), want.double() * 2.0 ** e) and torch.equal(lse, lse2)
