@@ -630,10 +630,13 @@ q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_he
  * bits; for the product with the values probabilities are rounded to fp16
  * (bf16 outputs) or to two fp16 parts, 22 bits (fp16 outputs).
  * Cache rows that no token of the request sees may hold anything, and a drafted
- * token's scale that is not finite spoils the tokens that see it alone; value
- * scales below 2^-24 of the largest that the request's tokens see lose bits.  lens and counts are taken
- * into [0, table_pages * page_size] and [0, tokens], keys past the table's pages
- * are not there, and a page number outside [0, pages) makes its keys unseen.
+ * token's scale that is not finite spoils the tokens that see it alone.  Value
+ * scales below 2^-24 of the largest that the request's tokens see, or below
+ * 2^-100, lose bits; ones above 2^86 may make outputs infinite or NaN (the sums
+ * that are divided last hold up to 16 times the keys seen).  lens and counts are
+ * taken into [0, table_pages * page_size] and [0, tokens], keys past the table's
+ * pages are not there, and a page number outside [0, pages) makes its keys
+ * unseen.
  * Requirements: batch, tokens, heads, kv_heads, dim, pages, page_size and
  * table_pages >= 1, tokens <= 64, heads <= 65535 and a multiple of kv_heads,
  * batch <= 65535, r = kv_heads * ceil(tokens * heads / kv_heads / 16) <= 65535,
