@@ -329,14 +329,16 @@ def main():
                     default=None, help="turn two rocprofv3 --pmc counter CSVs (FETCH_SIZE, "
                     "WRITE_SIZE) into profiles/traffic_<--traffic-of>.json")
     ap.add_argument("--traffic-of", choices=sorted(TRAFFIC), default="gemm_w8")
-    ap.add_argument("--command", default="", help="with --summarize-counters: the profiling "
-                    "command, recorded in the summary")
+    ap.add_argument("--command", default="", help="with --summarize-counters (required): the "
+                    "profiling command, recorded in the summary")
     args = ap.parse_args()
 
     if args.summarize_trace:
         print(summarize_trace(args.summarize_trace, args.kernel, args.window, args.before))
         return
     if args.summarize_counters:
+        if not args.command:
+            ap.error("--summarize-counters needs --command, the profiling command that it records")
         print(summarize_counters(*args.summarize_counters, args.traffic_of, args.command))
         return
 
