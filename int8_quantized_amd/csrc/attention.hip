@@ -49,12 +49,13 @@
 //    only when one passes 2^4, the values' power of two when a scale passes
 //    twice it: most steps need no exchange between lanes and no rescaling.
 //  * What bounds it: single tokens over long contexts, the cache's bytes (32
-//    requests x up to 24k keys x 8 heads x 128: 1.22 GB in 228 us, 5.3 TB/s; a copy
-//    runs at 4.9).  Trees, the vector instructions that widen codes and form the
+//    requests x up to 24k keys x 8 heads x 128: 1.22 GB in 228 us with the join,
+//    5.3 TB/s; a bare read of as much takes 176, a copy runs at 4.9 TB/s).  Trees, the
+//    vector instructions that widen codes and form the
 //    softmax beside the matrix instructions, about three to one, at the two
 //    waves a SIMD that the registers leave: 24 tokens x 4 heads of a group x 16
-//    requests x 4k in 81 us and 11 for the join, 64 x 8 x 4 x 16k in 100 and 8
-//    (four row tiles a wave, which halve the widening, spill and take 98).  One
+//    requests x 4k (fp16) in 85 us and 11 for the join, 64 x 8 x 4 x 16k (bf16) in 102 and
+//    8 (four row tiles a wave, which halve the widening, spill and take 98).  One
 //    token over 700 keys is a chain of latencies (page table, keys, joins): 13 us.
 //  * A step's registers are loaded again for the next one as soon as it has
 //    used them (keys after the first product, values after the second), so
@@ -821,8 +822,9 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
   constexpr int kTwo = DP == 256 ? 256 : 512;   // workgroups of four waves at once on 256 CUs
   // 32 keys a step: 64 fit fewer registers beside the loads in flight (32
   // requests x 24k keys 227 against 244 us, 1 x 700 15.0 against 15.8); two row
-  // tiles a wave where there are more than 16 rows (24-token trees x 16 x 4k 80
-  // us against 113 with one tile, 64-token trees x 4 x 16k 102 against 141)
+  // tiles a wave where there are more than 16 rows (probabilities of one part,
+  // 24-token trees x 16 x 4k 80 us against 113 with one tile, 64-token trees x 4 x
+  // 16k 102 against 141)
   if (rows <= 16) {
     // One workgroup of more waves a unit and no joining launch, where a few steps a
     // wave cost less than that: 8 heads, 1 request: 250 keys 10.7 us against 12.7,

@@ -21,11 +21,11 @@
 // bytes a lane, the next step's loads ahead of this step's products), and
 // their integer sums meet in LDS.
 //
-// Measured: 1 x 4096 x 4096, rank 16: down 6.5 us and rows 6.2 (17 MB, 3.5 us at
-// the copy rate: two launches of one round trip each); 50 x 4096 x 11008 with 24
-// adapters of rank 32: 10 and 27 us (68 MB, 14 us: every workgroup reads all
+// Measured: 1 x 4096 x 4096, rank 16: down 6.6 us and rows 6.3 (17 MB, 2.5 us at
+// the rate of a bare read: two launches of one round trip each); 50 x 4096 x 11008
+// with 24 adapters: 10 and 27 us (68 MB, 10 us: every workgroup reads all
 // rows of x from its L2, and the adapters' rows are 64 bytes each); 2048 x 4096 x
-// 11008, rank 64: down 18 us, GEMM with the epilogue 129 (103 without adapters).
+// 11008, rank 64: down 20 us, GEMM with the epilogue 144 (108 without adapters).
 #include <type_traits>
 
 #include "decode.h"

@@ -29,12 +29,12 @@
 // weight of 1 is 2^shift), which makes every sum exact and independent of the
 // order in which lanes and atomics add.
 //
-// Measured (256 rows x 131072 fp32, each filter): the first reading 25 us, which
-// is the memory's rate (134 MB at 5.4 TB/s); gathering 5 us greedy, 13 top-k, 10
-// min-p, 50 where all weights are summed (21 instructions of 4 cycles a weight
-// are 18 us of it), 66 for bins; the border 57; the pick 3 to 12.  24 x 100003 bf16
-// by top-p: 5 + 13 + 13 + 15 us; 1 x 32000 with top-k 50: 3 + 9 + 2 + 4 us, a chain of
-// latencies.
+// Measured (256 rows x 131072 fp32, each filter): the first reading 25 us (134 MB
+// at 5.4 TB/s; a bare read of large buffers runs at 6.9); gathering 5 us greedy, 13
+// top-k, 10 min-p, 50 where all weights are summed (21 instructions of 4 cycles a
+// weight are 18 us of it), 69 for bins; the border 57; the pick 3 to 12.  24 x 100003
+// bf16 by top-p: 4 + 12 + 13 + 16 us; 1 x 32000 with top-k 50: 3 + 9 + 2 + 4 us, a chain
+// of latencies.
 #include <cmath>
 
 #include "decode.h"
