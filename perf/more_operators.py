@@ -508,7 +508,7 @@ def _plain_fork(s):
     need = (want - first).clamp(min=0)
     before = need.cumsum(0) - need
     free = torch.argsort((refs > 0).int(), stable=True).int()
-    served = before + need <= (refs <= 0).sum()
+    served = (need == 0) | (before + need <= (refs <= 0).sum())
     at = j - first.unsqueeze(1)
     new = (at >= 0) & (at < need.unsqueeze(1)) & served.unsqueeze(1)
     picked = free[(before.unsqueeze(1) + at).clamp(0, refs.numel() - 1)]
@@ -669,7 +669,7 @@ def _exact_fork(case, s):
     for r in range(len(lens)):
         first = int((table[r] >= 0).sum())
         need = max(0, -(-int(lens[r] + more[r]) // page) - first) if more[r] > 0 else 0
-        served.append(int(spent + need <= len(free)))
+        served.append(int(need == 0 or spent + need <= len(free)))
         if served[-1]:
             table[r, first:first + need] = free[spent:spent + need]
             refs[free[spent:spent + need]] = 1
