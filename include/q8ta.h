@@ -684,6 +684,173 @@ q8ta_status q8ta_sample(const void* logits, int64_t row_stride, q8ta_dtype dtype
                         const float* top_p, const float* min_p, const float* u, int32_t* tokens,
                         float* logprobs, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * q8ta_norm_quantize: what stands between two blocks, with the codes that the
+ * next projection takes and one scale a token.  For token t, with rms(v) =
+ * 1 / sqrt(mean v^2 + eps) over its N elements, in 64 bits:
+ *   b = x * rms(x) * post_weight     (post_weight NULL: x)
+ *   h = residual_scale * residual + gate * b, rounded to fp32 and from there to
+ *       the type                     (residual NULL: gate * b; gate NULL: 1)
+ *   z = h * rms(h) * weight          (weight NULL: h)
+ *   residual_out = h;  scales[t] = max |z| / 127, rounded to fp32;
+ *   codes = rint(z * 127 / max |z|)  (all 0, with scale 0, for a row of zeros)
+ * A row whose z holds a value that is not finite gets the scale NaN and codes 0.
+ * x, residual, gate: [tokens, N] of `dtype`, inner stride 1, any row stride
+ * (gate_stride 0: one row of N for all tokens); post_weight, weight: fp32 [N];
+ * residual_out: dense, of `dtype`, may be NULL, or x or residual itself where that is
+ * dense; codes dense.  tokens == 0 is a no-op.  Requirements: 1 <= N <= 2^30,
+ * tokens < 2^31, tokens * N and tokens * strides <= 2^40, residual_scale finite,
+ * eps finite and > 0 where there is a norm (Q8TA_ERR_QPARAM).  Any alignment; N and
+ * strides of whole groups of eight elements and bases aligned to 16 bytes take the
+ * vector form.  Rows of up to 16384 elements are read once.
+ *
+ * q8ta_quantize_per_token: x's own codes (no norm, no residual).
+ */
+q8ta_status q8ta_norm_quantize(const void* x, int64_t x_stride, const void* residual,
+                               int64_t residual_stride, q8ta_dtype dtype, int64_t tokens, int64_t N,
+                               const float* post_weight, const void* gate, int64_t gate_stride,
+                               double residual_scale, const float* weight, double eps,
+                               void* residual_out, int8_t* codes, float* scales, hipStream_t stream);
+
+q8ta_status q8ta_quantize_per_token(const void* x, int64_t x_stride, q8ta_dtype dtype, int64_t tokens,
+                                    int64_t N, int8_t* codes, float* scales, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * q8ta_linear_per_token: the int8 product with a scale for each token and
+ * channel, symmetric codes and a floating-point output:
+ *   acc[m, n] = sum_k x[m, k] * weight[n, k]                          (int32)
+ *   y = ((float)acc * x_scales[m]) * weight_scales[n] + bias[n]
+ *   out[m, n] = y, or max(y, 0) for "relu", rounded once to out_dtype.
+ * x: int8 [M, K], weight: int8 [N, K], x_scales fp32 [M], weight_scales fp32 [N],
+ * bias fp32 [N] or NULL; out: dense [M, N].  Requirements: M <= 2^21, N and K <=
+ * 2^30, the elements of each tensor <= 2^40.  Any K and alignment: where K is no
+ * multiple of 16 or x or a weight is not 16-byte aligned, they are first copied into
+ * rows that are (workspace: (M + N) * K bytes, K rounded up to 16); none otherwise.
+ *
+ * q8ta_gated_linear: two such products and the gate between them in one launch:
+ *   out[m, n] = act(y_gate[m, n]) * y_up[m, n], rounded once to out_dtype,
+ * both in 32 bits; activation "silu", "gelu" (by erf), "gelu_tanh" or "relu".
+ * gate_weight and up_weight: int8 [N, K] each, with scales [N] and biases [N] (or NULL)
+ * of their own; the rest as above (workspace, where needed: (M + 2 * N) * K).
+ */
+q8ta_status q8ta_linear_per_token(const int8_t* x, int64_t M, int64_t K, const float* x_scales,
+                                  const int8_t* weight, int64_t N, const float* weight_scales,
+                                  const float* bias, const char* activation, void* out,
+                                  q8ta_dtype out_dtype, hipStream_t stream);
+
+q8ta_status q8ta_gated_linear(const int8_t* x, int64_t M, int64_t K, const float* x_scales,
+                              const int8_t* gate_weight, const float* gate_scales, const float* gate_bias,
+                              const int8_t* up_weight, const float* up_scales, const float* up_bias,
+                              int64_t N, const char* activation, void* out, q8ta_dtype out_dtype,
+                              hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * q8ta_verify_drafts: which drafted tokens the target keeps, from given random
+ * numbers, and the token that follows them.  The tokens are those of
+ * q8ta_tree_attention's tree, with its mask and counts: token 0 is the last one
+ * known, token i's parent the highest j < i whose bit is set in mask[b, i] (mask
+ * NULL: a chain, parent i - 1); one without a parent is never reached.
+ * logits[b, i] are the target's after token i, p = softmax(logits / T).  From token
+ * 0 on, the children of the current token are tried in their order:
+ *   draft_logits NULL (drafts that were not drawn, as the drafter's most likely): child
+ *     c is kept if  u[b, c] * left < p(ids[b, c]),  left = 1 less the p of the
+ *     children tried before; one that is not kept has p 0 from there on;
+ *   draft_logits (chains): c was drawn from q = softmax(draft_logits[b, c - 1] /
+ *     T'); kept if  u[b, c] * q(ids[b, c]) < p(ids[b, c]),  else p becomes max(p - q,
+ *     0) and the walk ends.
+ * A kept child is the next current token; where none is kept the walk ends:
+ *   path[b] = 0 and the kept tokens in order, then -1;  accepted[b] = their number, 0 included;
+ *   next[b] = the first index whose running sum of what is left of p passes u[b, 0] times
+ *     all that is left.
+ * Kept tokens and next are distributed as tokens sampled from p one after the
+ * other.  T <= 0 (or NaN) is greedy: a child is kept if it is the target's
+ * largest (the first of equal ones), and next is that.  T' = draft_temperature[b], or T
+ * where draft_temperature is NULL; T' <= 0 puts all of q on its largest.
+ * Sums and weights are 64-bit and added in an order that depends on vocab alone.
+ * A NaN logit counts as -inf; +inf logits share the weight alone; where all
+ * logits are -inf the walk ends, with next -1.  An id outside [0, vocab) has p and q 0.
+ * u: in [0, 1); below 0 as 0; a NaN or one of 1 and beyond keeps no drawn child with p <=
+ * q and takes the last index with anything left.  A request with counts[b] <= 0 gets
+ * accepted 0 and next -1.
+ * logits [batch, tokens, vocab], draft_logits [batch, tokens - 1, vocab], both of
+ * `dtype`, inner stride 1, any other strides; ids int32 [batch, tokens]; counts int32
+ * [batch] or NULL; mask int64 [batch, tokens] or NULL; temperature,
+ * draft_temperature fp32 [batch]; u fp32 [batch, tokens]; path int32 [batch, tokens];
+ * accepted, next int32 [batch].  batch == 0 is a no-op.  Requirements: batch <=
+ * 65535, 1 <= tokens <= 64, 1 <= vocab <= 2^24; draft_logits and mask not both
+ * (Q8TA_ERR_UNSUPPORTED).  Workspace: 16 bytes for each 4096 logits and some hundred
+ * for each request, 33 MB at most.
+ */
+q8ta_status q8ta_verify_drafts(const void* logits, int64_t batch_stride, int64_t token_stride,
+                               const void* draft_logits, int64_t draft_batch_stride,
+                               int64_t draft_token_stride, q8ta_dtype dtype, int64_t batch, int64_t tokens,
+                               int64_t vocab, const int32_t* ids, const int32_t* counts, const int64_t* mask,
+                               const float* temperature, const float* draft_temperature, const float* u,
+                               int32_t* path, int32_t* accepted, int32_t* next, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The pages of the cache, kept on the device (so that a captured step can take and
+ * free them).  table: int32 [requests, table_pages], a request's pages in
+ * the order of its rows and below 0 behind them; lens: int32 [requests], its rows; refs:
+ * int32 [pages], how many tables hold each page.  A page is free where refs <= 0.
+ * One table serves the caches of all layers.
+ *
+ * q8ta_pages_take: room for more[b] rows behind lens[b]: the entries from the first
+ *   below 0 (at or behind entry lens[b] / page_size) to the last that those rows
+ *   need get the lowest free pages, in the requests' order.  more[b] <= 0 asks for none.
+ *   granted[b]: 1, or 0 where there are too few free pages (then all later requests
+ *   that ask for any get none either) or the table has too few entries.
+ * q8ta_pages_fork: request dst[i] becomes a copy of request src[i], for i in [0, n): whole pages
+ *   of its lens rows are shared, the rows of a last page in part get the lowest free
+ *   page, in order of i; entries behind are -1, lens[dst[i]] = lens[src[i]].  copy_src,
+ *   copy_dst, copy_rows [n]: the page to copy from, the new page and its rows, as
+ *   q8ta_pages_copy takes them for each layer's cache (copy_dst -1 where there is
+ *   nothing to copy).  granted[i]: as above; 0 leaves dst[i] as it is, also where src[i]
+ *   or dst[i] is no request or the two are the same.  A request stands at most once in dst
+ *   and not in src beside it; its old pages are not released.
+ * q8ta_pages_release: request rows[i] (rows NULL: request i, n = requests) gives up its
+ *   pages behind the first keep[i] rows (keep NULL: all): entries from ceil(keep / page_size)
+ *   on become -1, refs goes down by one for each, lens to min(lens, keep).  A row
+ *   outside [0, requests) is skipped; one that stands twice gives up a page once.
+ * q8ta_pages_copy: page src[i] of a cache is copied to page dst[i], the first rows[i] rows
+ *   of each head (rows NULL: all).  Pages outside [0, pages) and pairs of the same page
+ *   are skipped.  A page stands at most once in dst and not in src beside it.
+ * q8ta_cache_compact: row base[b] + path[b, i] of request b moves to row base[b] + i, for i
+ *   < counts[b]: with q8ta_verify_drafts' path and accepted and base = the context's
+ *   length, the kept tokens' rows close up behind the context.  path rises (path[b, i] >=
+ *   i), n entries a request; rows with path[b, i] <= i, outside the table or on a page that
+ *   is none stay.  Rows behind the kept ones are left as they are.
+ *
+ * The cache's layout and slots as above, any dim, page_size and alignment (multiples of 16
+ * bytes move in 16-byte chunks).  lens outside [0, table_pages * page_size] are
+ * taken into it.  Entries of 0 (requests, n, batch) are no-ops.  Requirements: requests, batch and
+ * n <= 2^24 (copy and compact: n < 2^31), pages < 2^31, table_pages * page_size < 2^31,
+ * requests * table_pages and batch * n <= 2^40, kv_heads <= 65535, dim <= 65536, the
+ * cache's elements <= 2^40.  Workspace of take and fork: 16 bytes an entry and 8
+ * for each 4096 pages.
+ */
+q8ta_status q8ta_pages_take(int32_t* table, int64_t requests, int64_t table_pages, int64_t page_size,
+                            const int32_t* lens, const int32_t* more, int32_t* refs, int64_t pages,
+                            int32_t* granted, hipStream_t stream);
+
+q8ta_status q8ta_pages_fork(int32_t* table, int64_t requests, int64_t table_pages, int64_t page_size,
+                            int32_t* lens, const int32_t* src, const int32_t* dst, int64_t n, int32_t* refs,
+                            int64_t pages, int32_t* granted, int32_t* copy_src, int32_t* copy_dst,
+                            int32_t* copy_rows, hipStream_t stream);
+
+q8ta_status q8ta_pages_release(int32_t* table, int64_t requests, int64_t table_pages, int64_t page_size,
+                               int32_t* lens, const int32_t* rows, const int32_t* keep, int64_t n,
+                               int32_t* refs, int64_t pages, hipStream_t stream);
+
+q8ta_status q8ta_pages_copy(int8_t* cache, float* cache_scales, int64_t pages, int64_t page_size,
+                            int64_t kv_heads, int64_t dim, const int32_t* src, const int32_t* dst,
+                            const int32_t* rows, int64_t n, hipStream_t stream);
+
+q8ta_status q8ta_cache_compact(int8_t* cache, float* cache_scales, int64_t pages, int64_t page_size,
+                               int64_t kv_heads, int64_t dim, const int32_t* table, int64_t batch,
+                               int64_t table_pages, const int32_t* base, const int32_t* path, int64_t n,
+                               const int32_t* counts, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

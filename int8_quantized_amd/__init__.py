@@ -106,6 +106,21 @@ SIGNATURES = {
     "q8ta_linear_lora": ([_P, _I64, _I64, _DBL, _I64, _P, _I64, _P, _P, _P, _P, _I, _I64, _I64, _P,
                           _P, _P, _S, _P, _I, _P], ctypes.c_int),
     "q8ta_sample": ([_P, _I64, _I, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "q8ta_norm_quantize": ([_P, _I64, _P, _I64, _I, _I64, _I64, _P, _P, _I64, _DBL, _P, _DBL, _P, _P,
+                            _P, _P], ctypes.c_int),
+    "q8ta_quantize_per_token": ([_P, _I64, _I, _I64, _I64, _P, _P, _P], ctypes.c_int),
+    "q8ta_linear_per_token": ([_P, _I64, _I64, _P, _P, _I64, _P, _P, _S, _P, _I, _P], ctypes.c_int),
+    "q8ta_gated_linear": ([_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _S, _P, _I, _P],
+                          ctypes.c_int),
+    "q8ta_verify_drafts": ([_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P,
+                            _P, _P, _P, _P, _P], ctypes.c_int),
+    "q8ta_pages_take": ([_P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P], ctypes.c_int),
+    "q8ta_pages_fork": ([_P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P],
+                        ctypes.c_int),
+    "q8ta_pages_release": ([_P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _P], ctypes.c_int),
+    "q8ta_pages_copy": ([_P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P], ctypes.c_int),
+    "q8ta_cache_compact": ([_P, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P],
+                           ctypes.c_int),
 }
 
 _lib = None
@@ -742,6 +757,241 @@ def q8ta_linear_lora(x, input_scale, input_zero_point, weight, weight_scales, bi
     return out
 
 
+def q8ta_norm_quantize(x, residual, post_weight, gate, residual_scale, weight, eps, residual_out, codes,
+                       scales, stream=None):
+    """Norms before and after a block with its gate and scaled residual, and the next projection's codes.
+
+    x and residual [T, N] (fp32, fp16 or bf16, rows may be strided), residual may be None; post_weight
+    and weight fp32 [N] or None (no norm of x, or of the sum); gate [T, N] or [1, N] or None;
+    residual_out like x, dense, or None: residual_scale * residual + gate * norm(x); codes int8 [T, N]
+    and scales fp32 [T]: the norm of that in int8, one scale a token.  Returns codes."""
+    torch = _torch()
+    xp, xs, xt = _view(x, "x", 2)
+    T, N = xs
+    rp = gp = None
+    rt = gt = (0, 1)
+    dtype = x.dtype
+    if residual is not None:
+        rp, rs, rt = _view(residual, "residual", 2)
+        if rs != xs or residual.dtype is not dtype:
+            raise ValueError(f"residual must be {dtype} {tuple(xs)} (got {residual.dtype} {tuple(rs)})")
+    if gate is not None:
+        gp, gs, gt = _view(gate, "gate", 2)
+        if gs[1] != N or gs[0] not in (1, T) or gate.dtype is not dtype:
+            raise ValueError(f"gate must be {dtype} [{T} or 1, {N}] (got {gate.dtype} {tuple(gs)})")
+        if gs[0] == 1:
+            gt = (0, 1)
+    for name, t in (("post_weight", post_weight), ("weight", weight)):
+        if t is not None and t.shape != (N,):
+            raise ValueError(f"{name} must be [{N}] (got {tuple(t.shape)})")
+    if codes.shape != xs or scales.shape != (T,) or (residual_out is not None and residual_out.shape != xs):
+        raise ValueError(f"codes and residual_out must be {tuple(xs)} and scales [{T}]")
+    f32 = torch.float32
+    _check(lib().q8ta_norm_quantize(
+        xp, xt[0], rp, rt[0], _code(x, "x"), T, N, _opt_ptr(post_weight, f32, "post_weight"), gp, gt[0],
+        residual_scale, _opt_ptr(weight, f32, "weight"), eps,
+        _opt_ptr(residual_out, dtype, "residual_out"), _ptr(codes, torch.int8, "codes"),
+        _ptr(scales, f32, "scales"), _stream(stream)))
+    return codes
+
+
+def q8ta_quantize_per_token(x, codes, scales, stream=None):
+    """x [T, N] (fp32, fp16 or bf16, rows may be strided) in int8 codes [T, N] with one scale a token,
+    scales fp32 [T]: max |x| / 127.  Returns codes."""
+    torch = _torch()
+    xp, xs, xt = _view(x, "x", 2)
+    T, N = xs
+    if codes.shape != xs or scales.shape != (T,):
+        raise ValueError(f"codes must be {tuple(xs)} and scales [{T}] (got {tuple(codes.shape)}, "
+                         f"{tuple(scales.shape)})")
+    _check(lib().q8ta_quantize_per_token(xp, xt[0], _code(x, "x"), T, N, _ptr(codes, torch.int8, "codes"),
+                                         _ptr(scales, torch.float32, "scales"), _stream(stream)))
+    return codes
+
+
+def q8ta_linear_per_token(x, x_scales, weight, weight_scales, bias, activation, out, stream=None):
+    """The int8 product with a scale for each token and channel, floating-point out.
+
+    x int8 [M, K], x_scales fp32 [M], weight int8 [N, K], weight_scales fp32 [N], bias fp32 [N] or None;
+    activation "none" or "relu"; out [M, N] fp32, fp16 or bf16.  Returns out."""
+    torch = _torch()
+    xs, wsh = x.shape, weight.shape
+    if len(xs) != 2 or len(wsh) != 2 or wsh[1] != xs[1] or out.shape != (xs[0], wsh[0]):
+        raise ValueError(f"x [M, K], weight [N, K] and out [M, N] expected (got {tuple(xs)}, {tuple(wsh)}, "
+                         f"{tuple(out.shape)})")
+    (M, K), N = xs, wsh[0]
+    if x_scales.shape != (M,) or weight_scales.shape != (N,) or (bias is not None and bias.shape != (N,)):
+        raise ValueError(f"x_scales must be [{M}], weight_scales and bias [{N}]")
+    f32, i8 = torch.float32, torch.int8
+    _check(lib().q8ta_linear_per_token(
+        _ptr(x, i8, "x"), M, K, _ptr(x_scales, f32, "x_scales"), _ptr(weight, i8, "weight"), N,
+        _ptr(weight_scales, f32, "weight_scales"), _opt_ptr(bias, f32, "bias"), _act(activation),
+        _ptr(out, out.dtype, "out"), _code(out, "out"), _stream(stream)))
+    return out
+
+
+def q8ta_gated_linear(x, x_scales, gate_weight, gate_scales, gate_bias, up_weight, up_scales, up_bias,
+                      activation, out, stream=None):
+    """The gated feed-forward block's first half: act(x gate^T) * (x up^T) in one launch.
+
+    x int8 [M, K], x_scales fp32 [M]; gate_weight and up_weight int8 [N, K], each with scales fp32 [N]
+    and a bias fp32 [N] or None; activation "silu", "gelu", "gelu_tanh" or "relu"; out [M, N] fp32, fp16
+    or bf16.  Returns out."""
+    torch = _torch()
+    xs, wsh = x.shape, gate_weight.shape
+    if (len(xs) != 2 or len(wsh) != 2 or wsh[1] != xs[1] or up_weight.shape != wsh or
+            out.shape != (xs[0], wsh[0])):
+        raise ValueError(f"x [M, K], gate_weight and up_weight [N, K] and out [M, N] expected (got {tuple(xs)}, "
+                         f"{tuple(wsh)}, {tuple(up_weight.shape)}, {tuple(out.shape)})")
+    (M, K), N = xs, wsh[0]
+    if x_scales.shape != (M,):
+        raise ValueError(f"x_scales must be [{M}] (got {tuple(x_scales.shape)})")
+    for name, t in (("gate_scales", gate_scales), ("gate_bias", gate_bias), ("up_scales", up_scales),
+                    ("up_bias", up_bias)):
+        if t is not None and t.shape != (N,):
+            raise ValueError(f"{name} must be [{N}] (got {tuple(t.shape)})")
+    f32, i8 = torch.float32, torch.int8
+    _check(lib().q8ta_gated_linear(
+        _ptr(x, i8, "x"), M, K, _ptr(x_scales, f32, "x_scales"), _ptr(gate_weight, i8, "gate_weight"),
+        _ptr(gate_scales, f32, "gate_scales"), _opt_ptr(gate_bias, f32, "gate_bias"),
+        _ptr(up_weight, i8, "up_weight"), _ptr(up_scales, f32, "up_scales"),
+        _opt_ptr(up_bias, f32, "up_bias"), N, _act(activation), _ptr(out, out.dtype, "out"),
+        _code(out, "out"), _stream(stream)))
+    return out
+
+
+def q8ta_verify_drafts(logits, draft_logits, ids, counts, mask, temperature, draft_temperature, u, path,
+                       accepted, next_ids, stream=None):
+    """Which drafted tokens the target keeps, from given random numbers, and the token after them.
+
+    logits [B, T, V] (fp32, fp16 or bf16, any outer strides): the target's after each token of a chain or
+    tree, ids int32 [B, T] (token 0: the last one known), counts and mask as for q8ta_tree_attention;
+    draft_logits [B, T - 1, V] or None: what the drafts of a chain were drawn from (None: they were not
+    drawn); temperature and draft_temperature fp32 [B] (the second may be None: the first); u fp32 [B, T]:
+    u[:, i] keeps token i, u[:, 0] draws the next one.  path int32 [B, T]: the kept tokens' places, then -1,
+    accepted int32 [B]: their number, next_ids int32 [B].  Returns next_ids."""
+    torch = _torch()
+    lp, ls, lt = _view(logits, "logits", 3)
+    B, T, V = ls
+    dp, dt = None, (0, 0, 1)
+    if draft_logits is not None:
+        dp, ds, dt = _view(draft_logits, "draft_logits", 3)
+        if ds != (B, T - 1, V) or draft_logits.dtype is not logits.dtype:
+            raise ValueError(f"draft_logits must be {logits.dtype} [{B}, {T - 1}, {V}] (got "
+                             f"{draft_logits.dtype} {tuple(ds)})")
+        dp = dp or lp   # (no rows of a single token's chain: a pointer that is not read)
+    for name, t, shape in (("ids", ids, (B, T)), ("u", u, (B, T)), ("path", path, (B, T)),
+                           ("mask", mask, (B, T)), ("counts", counts, (B,)),
+                           ("temperature", temperature, (B,)), ("accepted", accepted, (B,)),
+                           ("draft_temperature", draft_temperature, (B,)), ("next_ids", next_ids, (B,))):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)} (got {tuple(t.shape)})")
+    f32, i32 = torch.float32, torch.int32
+    _check(lib().q8ta_verify_drafts(
+        lp, lt[0], lt[1], dp, dt[0], dt[1], _code(logits, "logits"), B, T, V, _ptr(ids, i32, "ids"),
+        _opt_ptr(counts, i32, "counts"), _opt_ptr(mask, torch.int64, "mask"),
+        _ptr(temperature, f32, "temperature"), _opt_ptr(draft_temperature, f32, "draft_temperature"),
+        _ptr(u, f32, "u"), _ptr(path, i32, "path"), _ptr(accepted, i32, "accepted"),
+        _ptr(next_ids, i32, "next_ids"), _stream(stream)))
+    return next_ids
+
+
+def _table(table, lens, refs):
+    """Pointers and sizes of a block table, its requests' rows and its pages' holders."""
+    torch = _torch()
+    i32 = torch.int32
+    ts, ps = table.shape, refs.shape
+    if len(ts) != 2 or lens.shape != (ts[0],) or len(ps) != 1:
+        raise ValueError("table [requests, table_pages], lens [requests] and refs [pages] expected")
+    return (_ptr(table, i32, "table"), ts[0], ts[1], _ptr(lens, i32, "lens"), _ptr(refs, i32, "refs"), ps[0],
+            i32)
+
+
+def _each(n, **lists):
+    for name, t in lists.items():
+        if t is not None and t.shape != (n,):
+            raise ValueError(f"{name} must be [{n}] (got {tuple(t.shape)})")
+
+
+def q8ta_pages_take(table, lens, page_size, more, refs, granted, stream=None):
+    """The lowest free pages for more [R] rows behind each request's lens.
+
+    table int32 [R, table_pages], lens, more and granted int32 [R], refs int32 [pages]: how many tables
+    hold each page (0: free).  granted: 1 where a request got what it asked for.  Returns table."""
+    tp, R, width, lp, rp, pages, i32 = _table(table, lens, refs)
+    _each(R, more=more, granted=granted)
+    _check(lib().q8ta_pages_take(tp, R, width, page_size, lp, _ptr(more, i32, "more"), rp, pages,
+                                 _ptr(granted, i32, "granted"), _stream(stream)))
+    return table
+
+
+def q8ta_pages_fork(table, lens, page_size, src, dst, refs, granted, copy_src, copy_dst, copy_rows,
+                    stream=None):
+    """Request dst[i] becomes a copy of request src[i]: whole pages shared, a page of its own for the rest.
+
+    All int32: table [R, table_pages], lens [R], refs [pages]; src, dst and the outputs granted, copy_src,
+    copy_dst and copy_rows [n]: what q8ta_pages_copy has to copy in each layer's cache.  Returns table."""
+    tp, R, width, lp, rp, pages, i32 = _table(table, lens, refs)
+    n = src.shape[0] if src.dim() == 1 else -1
+    _each(n, src=src, dst=dst, granted=granted, copy_src=copy_src, copy_dst=copy_dst, copy_rows=copy_rows)
+    _check(lib().q8ta_pages_fork(tp, R, width, page_size, lp, _ptr(src, i32, "src"), _ptr(dst, i32, "dst"), n, rp,
+                                 pages, _ptr(granted, i32, "granted"), _ptr(copy_src, i32, "copy_src"),
+                                 _ptr(copy_dst, i32, "copy_dst"), _ptr(copy_rows, i32, "copy_rows"),
+                                 _stream(stream)))
+    return table
+
+
+def q8ta_pages_release(table, lens, page_size, rows, keep, refs, stream=None):
+    """Requests rows [n] (None: all) give up their pages behind the first keep [n] rows (None: all pages).
+
+    All int32: table [R, table_pages], lens [R], refs [pages].  Returns table."""
+    tp, R, width, lp, rp, pages, i32 = _table(table, lens, refs)
+    n = R if rows is None else (rows.shape[0] if rows.dim() == 1 else -1)
+    _each(n, rows=rows, keep=keep)
+    _check(lib().q8ta_pages_release(tp, R, width, page_size, lp, _opt_ptr(rows, i32, "rows"),
+                                    _opt_ptr(keep, i32, "keep"), n, rp, pages, _stream(stream)))
+    return table
+
+
+def _cache(cache, cache_scales):
+    torch = _torch()
+    cs = cache.shape
+    if len(cs) != 5 or cs[1] != 2 or cs[:4] != cache_scales.shape:
+        raise ValueError("cache [pages, 2, kv_heads, page, dim] and cache_scales [pages, 2, "
+                         "kv_heads, page] expected")
+    return (_ptr(cache, torch.int8, "cache"), _ptr(cache_scales, torch.float32, "cache_scales"), cs[0], cs[3],
+            cs[2], cs[4])
+
+
+def q8ta_pages_copy(cache, cache_scales, src, dst, rows=None, stream=None):
+    """Pages src [n] of the int8 cache are copied to pages dst [n] (int32, negative: none), of each the
+    first rows [n] rows, or all.  Returns cache."""
+    i32 = _torch().int32
+    args = _cache(cache, cache_scales)
+    n = src.shape[0] if src.dim() == 1 else -1
+    _each(n, src=src, dst=dst, rows=rows)
+    _check(lib().q8ta_pages_copy(*args, _ptr(src, i32, "src"), _ptr(dst, i32, "dst"), _opt_ptr(rows, i32, "rows"),
+                                 n, _stream(stream)))
+    return cache
+
+
+def q8ta_cache_compact(cache, cache_scales, table, base, path, counts, stream=None):
+    """Row base[b] + path[b, i] of request b moves to row base[b] + i, for i < counts[b].
+
+    cache and cache_scales as q8ta_rope_append fills them, table int32 [B, table_pages], base and counts
+    int32 [B], path int32 [B, n], rising (q8ta_verify_drafts' path and accepted).  Returns cache."""
+    i32 = _torch().int32
+    args = _cache(cache, cache_scales)
+    ts, ps = table.shape, path.shape
+    if len(ts) != 2 or len(ps) != 2 or ps[0] != ts[0]:
+        raise ValueError("table [B, table_pages] and path [B, n] expected")
+    _each(ts[0], base=base, counts=counts)
+    _check(lib().q8ta_cache_compact(*args, _ptr(table, i32, "table"), ts[0], ts[1], _ptr(base, i32, "base"),
+                                    _ptr(path, i32, "path"), ps[1], _ptr(counts, i32, "counts"),
+                                    _stream(stream)))
+    return cache
+
+
 __all__ = [
     "Q8taError", "lib", "q8ta_last_error", "q8ta_quantize_per_tensor", "q8ta_dequantize_per_tensor",
     "q8ta_linear", "q8ta_linear_gemv", "q8ta_linear_dq", "q8ta_linear_acc", "q8ta_conv2d_transposed",
@@ -754,4 +1004,7 @@ __all__ = [
     "q8ta_conv2d_transposed_weight_prepack", "q8ta_conv2d_transposed_prepacked",
     "q8ta_quantize_conv2d_transposed_prepacked",
     "q8ta_linear_lora", "q8ta_rope_append", "q8ta_tree_attention", "q8ta_sample",
+    "q8ta_norm_quantize", "q8ta_quantize_per_token", "q8ta_linear_per_token", "q8ta_gated_linear",
+    "q8ta_verify_drafts", "q8ta_pages_take", "q8ta_pages_fork", "q8ta_pages_release", "q8ta_pages_copy",
+    "q8ta_cache_compact",
 ]

@@ -3,34 +3,110 @@
 #include <cmath>
 #include <cstring>
 
-#include "decode.h"
+#include "api_checks.h"
 
 using namespace q8ta;
 
 namespace {
 
-constexpr int64_t kMaxElems = (int64_t)1 << 40;
-
-q8ta_status hip_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return Q8TA_OK;
-  return report(Q8TA_ERR_HIP, "%s: HIP error %d (%s)", what, (int)e, hipGetErrorString(e));
+// The checks of q8ta_norm_quantize and q8ta_quantize_per_token.
+q8ta_status norm_quantize(const char* op, NormArgs a, hipStream_t stream) {
+  if (!dtype_ok(a.dtype)) return report(Q8TA_ERR_UNSUPPORTED, "%s: unknown dtype %d", op, a.dtype);
+  if (a.tokens < 0 || a.tokens >= ((int64_t)1 << 31))
+    return report(Q8TA_ERR_SHAPE, "%s: tokens out of range (%lld)", op, (long long)a.tokens);
+  if (a.n < 1 || a.n > ((int64_t)1 << 30) || (a.tokens > 0 && !fits({a.tokens, a.n})))
+    return report(Q8TA_ERR_SHAPE, "%s: N must be in [1, 2^30] and tokens * N <= 2^40 (got %lld, %lld)", op,
+                  (long long)a.n, (long long)a.tokens);
+  for (int64_t st : {a.x_stride, a.residual_stride, a.gate_stride})
+    if (st < 0 || st > kMaxElems || (a.tokens > 0 && st > kMaxElems / a.tokens))
+      return report(Q8TA_ERR_SHAPE, "%s: strides must be >= 0 and tokens * stride <= 2^40 (got %lld)", op,
+                    (long long)st);
+  if (!std::isfinite(a.residual_scale))
+    return report(Q8TA_ERR_QPARAM, "%s: residual_scale must be finite (got %g)", op, a.residual_scale);
+  if ((a.post_weight || a.weight) && !(std::isfinite(a.eps) && a.eps > 0.0))
+    return report(Q8TA_ERR_QPARAM, "%s: eps must be finite and > 0 (got %g)", op, a.eps);
+  if (a.tokens == 0) return Q8TA_OK;
+  if (!a.x || !a.codes || !a.scales)
+    return report(Q8TA_ERR_NULL, "%s: x, codes and scales must not be NULL", op);
+  return hip_status(launch_norm_quantize(a, stream), op);
 }
 
-bool dtype_ok(int d) { return d == Q8TA_F32 || d == Q8TA_F16 || d == Q8TA_BF16; }
-
-// a * b * .. <= 2^40 for factors >= 1.
-bool fits(std::initializer_list<int64_t> f) {
-  int64_t left = kMaxElems;
-  for (int64_t x : f) {
-    if (x > left) return false;
-    left /= x;
-  }
-  return true;
+// The checks of q8ta_linear_per_token and q8ta_gated_linear.
+q8ta_status scaled_linear(const char* op, const ScaledArgs& a, q8ta_dtype out_dtype, hipStream_t stream) {
+  if (!a.x || !a.xs || !a.w[0] || !a.ws[0] || !a.y || (a.mats == 2 && (!a.w[1] || !a.ws[1])))
+    return report(Q8TA_ERR_NULL, "%s: a required pointer is NULL", op);
+  if (a.M < 1 || a.K < 1 || a.N < 1)
+    return report(Q8TA_ERR_SHAPE, "%s: M, K, N must be >= 1 (got %lld, %lld, %lld)", op, (long long)a.M,
+                  (long long)a.K, (long long)a.N);
+  const int64_t lim = (int64_t)1 << 30;
+  if (a.M > ((int64_t)1 << 21) || a.N > lim || a.K > lim || !fits({a.M, a.K}) || !fits({a.N, a.K}) ||
+      !fits({a.M, a.N}))
+    return report(Q8TA_ERR_SHAPE, "%s: sizes too large", op);
+  if (!dtype_ok(out_dtype))
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: unknown output dtype %d", op, (int)out_dtype);
+  return hip_status(launch_scaled(a, stream), op);
 }
 
 }  // namespace
 
 extern "C" {
+
+q8ta_status q8ta_norm_quantize(const void* x, int64_t x_stride, const void* residual,
+                               int64_t residual_stride, q8ta_dtype dtype, int64_t tokens, int64_t N,
+                               const float* post_weight, const void* gate, int64_t gate_stride,
+                               double residual_scale, const float* weight, double eps,
+                               void* residual_out, int8_t* codes, float* scales, hipStream_t stream) {
+  NormArgs a{};
+  a.x = x; a.x_stride = x_stride; a.residual = residual; a.residual_stride = residual ? residual_stride : 0;
+  a.gate = gate; a.gate_stride = gate ? gate_stride : 0; a.dtype = dtype; a.tokens = tokens; a.n = N;
+  a.post_weight = post_weight; a.weight = weight; a.residual_scale = residual_scale; a.eps = eps;
+  a.sum = residual_out; a.codes = codes; a.scales = scales;
+  return norm_quantize("q8ta_norm_quantize", a, stream);
+}
+
+q8ta_status q8ta_quantize_per_token(const void* x, int64_t x_stride, q8ta_dtype dtype, int64_t tokens,
+                                    int64_t N, int8_t* codes, float* scales, hipStream_t stream) {
+  NormArgs a{};
+  a.x = x; a.x_stride = x_stride; a.dtype = dtype; a.tokens = tokens; a.n = N; a.residual_scale = 1.0;
+  a.codes = codes; a.scales = scales;
+  return norm_quantize("q8ta_quantize_per_token", a, stream);
+}
+
+q8ta_status q8ta_linear_per_token(const int8_t* x, int64_t M, int64_t K, const float* x_scales,
+                                  const int8_t* weight, int64_t N, const float* weight_scales,
+                                  const float* bias, const char* activation, void* out,
+                                  q8ta_dtype out_dtype, hipStream_t stream) {
+  const char* op = "q8ta_linear_per_token";
+  if (!activation || (strcmp(activation, "none") != 0 && strcmp(activation, "relu") != 0))
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: activation \"%.64s\" is not supported (\"none\" or "
+                  "\"relu\")", op, activation ? activation : "NULL");
+  ScaledArgs a{};
+  a.x = x; a.xs = x_scales; a.w[0] = weight; a.ws[0] = weight_scales; a.bias[0] = bias; a.mats = 1;
+  a.act = strcmp(activation, "relu") == 0 ? kActRelu : kActNone; a.M = M; a.N = N; a.K = K; a.y = out;
+  a.y_type = out_dtype;
+  return scaled_linear(op, a, out_dtype, stream);
+}
+
+q8ta_status q8ta_gated_linear(const int8_t* x, int64_t M, int64_t K, const float* x_scales,
+                              const int8_t* gate_weight, const float* gate_scales, const float* gate_bias,
+                              const int8_t* up_weight, const float* up_scales, const float* up_bias,
+                              int64_t N, const char* activation, void* out, q8ta_dtype out_dtype,
+                              hipStream_t stream) {
+  const char* op = "q8ta_gated_linear";
+  static const struct { const char* name; int act; } kinds[] = {
+      {"silu", kActSilu}, {"gelu", kActGelu}, {"gelu_tanh", kActGeluTanh}, {"relu", kActRelu}};
+  int act = -1;
+  for (const auto& k : kinds)
+    if (activation && strcmp(activation, k.name) == 0) act = k.act;
+  if (act < 0)
+    return report(Q8TA_ERR_UNSUPPORTED, "%s: activation \"%.64s\" is not supported (\"silu\", \"gelu\", "
+                  "\"gelu_tanh\" or \"relu\")", op, activation ? activation : "NULL");
+  ScaledArgs a{};
+  a.x = x; a.xs = x_scales; a.w[0] = gate_weight; a.ws[0] = gate_scales; a.bias[0] = gate_bias;
+  a.w[1] = up_weight; a.ws[1] = up_scales; a.bias[1] = up_bias; a.mats = 2; a.act = act; a.M = M; a.N = N;
+  a.K = K; a.y = out; a.y_type = out_dtype;
+  return scaled_linear(op, a, out_dtype, stream);
+}
 
 q8ta_status q8ta_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                              const void* k, int64_t k_token_stride, int64_t k_head_stride,

@@ -1,6 +1,8 @@
 // Arguments and launchers of the decode-step operators: rotary positions with
 // the int8 cache append, tree attention over that cache, the linear with
-// low-rank adapters, and token sampling.
+// low-rank adapters, token sampling; norms with the codes of the next
+// projection, the linear and the gated block with scales per token, the
+// verification of drafted tokens, and the pages of the cache.
 #pragma once
 
 #include "../../include/q8ta.h"
@@ -171,5 +173,92 @@ hipError_t launch_linear_lora(LoraArgs a, hipStream_t s);
 // alignment as for launch_gemm_w8 / launch_gemm_mx.
 hipError_t launch_gemm_w8_lora(const LoraArgs& a, hipStream_t s);
 hipError_t launch_gemm_mx_lora(const LoraArgs& a, hipStream_t s);
+
+// Rows of `bytes` bytes at any address into rows of `padded` bytes (a multiple of
+// 16), zero past the row (lora.hip).
+hipError_t pad_rows(const void* src, int64_t rows, int64_t bytes, int64_t padded, int8_t* dst,
+                    hipStream_t s);
+
+struct NormArgs {
+  const void* x;              // [tokens, n], row stride in elements
+  const void* residual;       // or NULL
+  const void* gate;           // row stride 0: one row for all; or NULL
+  int64_t x_stride, residual_stride, gate_stride;
+  int dtype;
+  int64_t tokens, n;
+  const float* post_weight;   // or NULL
+  const float* weight;        // or NULL
+  double residual_scale, eps;
+  void* sum;                  // dense, or NULL
+  int8_t* codes;
+  float* scales;
+};
+hipError_t launch_norm_quantize(const NormArgs& a, hipStream_t s);
+
+enum Activation { kActNone, kActRelu, kActSilu, kActGelu, kActGeluTanh };
+
+// The linear with scales per token and channel (mats 1), and the gated block
+// act(x w[0]) * (x w[1]) of two of them (mats 2).
+struct ScaledArgs {
+  const int8_t* x;            // [M, K]
+  const float* xs;            // [M]
+  const int8_t* w[2];         // [N, K] each
+  const float* ws[2];         // [N] each
+  const float* bias[2];       // [N] each, or NULL
+  int mats, act;
+  int64_t M, N, K;
+  void* y;                    // [M, N]
+  int y_type;
+  int64_t n0 = 0;             // first channel of a launch of the row kernel
+};
+hipError_t launch_scaled(ScaledArgs a, hipStream_t s);
+// K a multiple of 16 and 16-byte aligned x and w.
+hipError_t launch_scaled_tiles(const ScaledArgs& a, hipStream_t s);
+
+struct VerifyArgs {
+  const void* logits;         // [batch, tokens, vocab], unit inner stride
+  int64_t bs, ts;
+  const void* draft;          // [batch, tokens - 1, vocab], or NULL
+  int64_t dbs, dts;
+  int dtype, batch, tokens, vocab;
+  const int32_t* ids;         // [batch, tokens]
+  const int32_t* counts;      // [batch] or NULL
+  const int64_t* mask;        // [batch, tokens] or NULL
+  const float *temperature, *draft_temperature;   // [batch]; the second may be NULL
+  const float* u;             // [batch, tokens]
+  int32_t *path, *accepted, *next;
+};
+hipError_t launch_verify_drafts(const VerifyArgs& a, hipStream_t s);
+
+// The block tables and holders of the cache's pages.
+struct PagesArgs {
+  int32_t* table;             // [requests, table_pages]
+  int64_t requests, table_pages;
+  int32_t* lens;              // [requests]
+  int64_t page;
+  int32_t* refs;              // [pages]
+  int64_t pages;
+  const int32_t *a, *b;       // take: more; fork: src, dst; release: rows, keep
+  int64_t n;                  // entries of a and b
+  int32_t* granted;
+  int32_t *copy_src, *copy_dst, *copy_rows;
+};
+hipError_t launch_pages_take(const PagesArgs& a, hipStream_t s);
+hipError_t launch_pages_fork(const PagesArgs& a, hipStream_t s);
+hipError_t launch_pages_release(const PagesArgs& a, hipStream_t s);
+
+struct CacheArgs {
+  int8_t* cache;              // [pages, 2, kv_heads, page, dim]
+  float* scales;              // [pages, 2, kv_heads, page]
+  int64_t pages, page;
+  int kv_heads, dim;
+  const int32_t *src, *dst, *rows;   // copy: [n] each, rows may be NULL
+  int64_t n;
+  const int32_t* table;       // compact: [batch, table_pages]
+  int64_t batch, table_pages;
+  const int32_t *base, *path, *counts;   // [batch], [batch, n], [batch]
+};
+hipError_t launch_pages_copy(const CacheArgs& a, hipStream_t s);
+hipError_t launch_cache_compact(const CacheArgs& a, hipStream_t s);
 
 }  // namespace q8ta

@@ -1,0 +1,329 @@
+// q8ta_norm_quantize and q8ta_quantize_per_token: what stands between two
+// blocks, and the codes that the next projection takes, one scale a token.
+//
+//   b = x, or x / rms(x) * post_weight          rms(v) = sqrt(mean v^2 + eps)
+//   h = residual_scale * residual + gate * b    rounded to the type: the new residual
+//   z = h, or h / rms(h) * weight
+//   scale = max |z| / 127,  code = rint(z * 127 / max |z|)
+//
+// Everything between the loads and the stores is 64-bit: a 16-bit value times
+// 127 over another is a tie of the codes often enough that 32 bits would turn
+// it the wrong way, and the sum h is what later blocks add to.  (64-bit
+// multiply-adds run at the rate of 32-bit ones here.)  The division is a
+// product with 127 / max, but next to a tie, where it is carried out.
+//
+// A workgroup takes one row and holds it in registers (8 * C elements a
+// thread): x, residual and gate are read once, the sum and the codes written
+// once, and the two or three sums over the row meet in LDS.  Rows too long for
+// that are read again for each sum (k_norm_long).
+#include "decode.h"
+
+namespace q8ta {
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxThreads = 1024;
+
+// Eight elements from p on; `live` of them where not VEC.
+template <bool VEC>
+__device__ __forceinline__ void load8(const float* p, int live, float (&x)[8]) {
+  if constexpr (VEC) {
+    const v4f a = *reinterpret_cast<const v4f*>(p), b = *reinterpret_cast<const v4f*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = a[i];
+      x[4 + i] = b[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < live ? p[i] : 0.0f;
+  }
+}
+template <bool VEC, class T>
+__device__ __forceinline__ void load8(const T* p, int live, float (&x)[8]) {
+  if constexpr (VEC) {
+    const v4u v = *reinterpret_cast<const v4u*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_float(T{(uint16_t)(v[i / 2] >> (16 * (i % 2)))});
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < live ? to_float(p[i]) : 0.0f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float* p, int live, const float (&x)[8]) {
+  if constexpr (VEC) {
+    *reinterpret_cast<v4f*>(p) = v4f{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<v4f*>(p + 4) = v4f{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < live) p[i] = x[i];
+  }
+}
+// (x is of the type already: no rounding)
+template <bool VEC, class T>
+__device__ __forceinline__ void store8(T* p, int live, const float (&x)[8]) {
+  if constexpr (VEC) {
+    v4u v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = (uint32_t)from_float<T>(x[2 * i]).bits | (uint32_t)from_float<T>(x[2 * i + 1]).bits << 16;
+    *reinterpret_cast<v4u*>(p) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < live) p[i] = from_float<T>(x[i]);
+  }
+}
+
+// The larger magnitude; a NaN on either side stays (fmax would drop it).
+__device__ __forceinline__ double top_of(double a, double b) { return a > b || a != a ? a : b; }
+__device__ __forceinline__ double plus_of(double a, double b) { return a + b; }
+
+template <int CTRL>
+__device__ __forceinline__ double row_move64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)row_move<CTRL>((int32_t)(uint32_t)b);
+  const uint32_t hi = (uint32_t)row_move<CTRL>((int32_t)(uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane64(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int32_t)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int32_t)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// v of all threads of the workgroup by `f`, in a fixed order, the same in every
+// thread.  `sh`: kMaxThreads / 64 doubles that no other call uses.
+template <class F>
+__device__ __forceinline__ double over_row(double v, double* sh, F&& f) {
+  v = f(v, row_move64<kDppMirror16>(v));
+  v = f(v, row_move64<kDppMirror8>(v));
+  v = f(v, row_move64<kDppRev4>(v));
+  v = f(v, row_move64<kDppSwap1>(v));
+  v = f(f(lane64(v, 0), lane64(v, 16)), f(lane64(v, 32), lane64(v, 48)));
+  const int waves = blockDim.x / 64;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x / 64] = v;
+  __syncthreads();
+  v = sh[0];
+  for (int w = 1; w < waves; ++w) v = f(v, sh[w]);
+  return v;
+}
+
+// rint(z * 127 / top), inv = 127 / top: the quotient's rounding differs from
+// the product's by 2^-52 of it, which matters next to a tie.
+__device__ __forceinline__ int code_of(double z, double top, double inv) {
+  double q = z * inv;
+  double r = __builtin_rint(q);
+  if (__builtin_fabs(q - r) > 0.499999) {
+    q = z * 127.0 / top;
+    r = __builtin_rint(q);
+  }
+  return (int)r;
+}
+
+// The row's scale and 127 / max; a row with a value that is not finite has the
+// scale NaN and codes 0, as has one of zeros with the scale 0.
+struct Scale {
+  double top, inv;
+  float scale;
+};
+__device__ __forceinline__ Scale scale_of(double top) {
+  Scale s{top, 0.0, 0.0f};
+  if (top > 0.0) {
+    s.inv = 127.0 / top;
+    s.scale = (float)(top / 127.0);
+  }
+  if (!(top < (double)__builtin_inff())) {
+    s.inv = 0.0;
+    s.scale = __builtin_nanf("");
+  }
+  return s;
+}
+
+// h = residual_scale * residual + gate * b as it is stored.
+template <class T>
+__device__ __forceinline__ float sum_of(double b, bool has_gate, float gate, bool has_res, float res,
+                                        double res_scale) {
+  if (has_gate) b = b * (double)gate;
+  if (has_res) b = b + (double)res * res_scale;
+  return to_float(from_float<T>((float)b));
+}
+
+// C: groups of 8 elements a thread.
+template <class T, int C, bool VEC>
+__global__ __launch_bounds__(kMaxThreads) void k_norm(NormArgs a) {
+  __shared__ double sh[3][kMaxThreads / 64];
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int64_t t = blockIdx.x;
+  const int n = (int)a.n;
+  const T* x = (const T*)a.x + t * a.x_stride;
+  const T* res = (const T*)a.residual + t * a.residual_stride;
+  const T* gate = (const T*)a.gate + t * a.gate_stride;
+  float h[C][8], r[C][8], g[C][8], w[C][8], pw[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = 8 * (tid + c * nt);
+    const int live = n - e;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[c][i] = r[c][i] = g[c][i] = w[c][i] = pw[c][i] = 0.0f;
+    if (live > 0) {
+      load8<VEC>(x + e, live, h[c]);
+      if (a.residual) load8<VEC>(res + e, live, r[c]);
+      if (a.gate) load8<VEC>(gate + e, live, g[c]);
+      if (a.post_weight) load8<VEC>(a.post_weight + e, live, pw[c]);
+      if (a.weight) load8<VEC>(a.weight + e, live, w[c]);
+    }
+  }
+  double post = 1.0;
+  if (a.post_weight) {
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = __builtin_fma((double)h[c][i], (double)h[c][i], s);
+    post = 1.0 / __builtin_sqrt(over_row(s, sh[0], plus_of) / (double)n + a.eps);
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      double b = h[c][i];
+      if (a.post_weight) b = b * post * (double)pw[c][i];
+      h[c][i] = sum_of<T>(b, a.gate != nullptr, g[c][i], a.residual != nullptr, r[c][i], a.residual_scale);
+      s = __builtin_fma((double)h[c][i], (double)h[c][i], s);
+    }
+  double rstd = 1.0;
+  if (a.weight) rstd = 1.0 / __builtin_sqrt(over_row(s, sh[1], plus_of) / (double)n + a.eps);
+  auto z_of = [&](int c, int i) {
+    const double z = h[c][i];
+    return a.weight ? z * rstd * (double)w[c][i] : z;
+  };
+  double top = 0.0;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = top_of(__builtin_fabs(z_of(c, i)), top);
+  const Scale sc = scale_of(over_row(top, sh[2], top_of));
+  if (tid == 0) a.scales[t] = sc.scale;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = 8 * (tid + c * nt);
+    const int live = n - e;
+    if (live <= 0) continue;
+    if (a.sum) store8<VEC>((T*)a.sum + t * a.n + e, live, h[c]);
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = sc.inv > 0.0 ? code_of(z_of(c, i), sc.top, sc.inv) : 0;
+    int8_t* dst = a.codes + t * a.n + e;
+    if constexpr (VEC) {
+      *reinterpret_cast<v2u*>(dst) = v2u{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < live) dst[i] = (int8_t)q[i];
+    }
+  }
+}
+
+// Rows of any length: the row is read again for each sum.  Every thread writes
+// only what it alone has read, last (the sum may stand in x's or the residual's place).
+template <class T>
+__global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a) {
+  __shared__ double sh[3][kMaxThreads / 64];
+  const int tid = threadIdx.x;
+  const int64_t t = blockIdx.x;
+  const T* x = (const T*)a.x + t * a.x_stride;
+  const T* res = (const T*)a.residual + t * a.residual_stride;
+  const T* gate = (const T*)a.gate + t * a.gate_stride;
+  double post = 1.0, rstd = 1.0;
+  auto h_of = [&](int64_t e) {
+    double b = to_float(x[e]);
+    if (a.post_weight) b = b * post * (double)a.post_weight[e];
+    return sum_of<T>(b, a.gate != nullptr, a.gate ? to_float(gate[e]) : 0.0f, a.residual != nullptr,
+                     a.residual ? to_float(res[e]) : 0.0f, a.residual_scale);
+  };
+  auto z_of = [&](int64_t e, float h) {
+    return a.weight ? (double)h * rstd * (double)a.weight[e] : (double)h;
+  };
+  if (a.post_weight) {
+    double s = 0.0;
+    for (int64_t e = tid; e < a.n; e += kMaxThreads) {
+      const double v = to_float(x[e]);
+      s = __builtin_fma(v, v, s);
+    }
+    post = 1.0 / __builtin_sqrt(over_row(s, sh[0], plus_of) / (double)a.n + a.eps);
+  }
+  if (a.weight) {
+    double s = 0.0;
+    for (int64_t e = tid; e < a.n; e += kMaxThreads) {
+      const double v = h_of(e);
+      s = __builtin_fma(v, v, s);
+    }
+    rstd = 1.0 / __builtin_sqrt(over_row(s, sh[1], plus_of) / (double)a.n + a.eps);
+  }
+  double top = 0.0;
+  for (int64_t e = tid; e < a.n; e += kMaxThreads) top = top_of(__builtin_fabs(z_of(e, h_of(e))), top);
+  const Scale sc = scale_of(over_row(top, sh[2], top_of));
+  if (tid == 0) a.scales[t] = sc.scale;
+  for (int64_t e = tid; e < a.n; e += kMaxThreads) {
+    const float h = h_of(e);
+    const int q = sc.inv > 0.0 ? code_of(z_of(e, h), sc.top, sc.inv) : 0;
+    if (a.sum) ((T*)a.sum)[t * a.n + e] = from_float<T>(h);
+    a.codes[t * a.n + e] = (int8_t)q;
+  }
+}
+
+template <class T, int C>
+void launch_regs(const NormArgs& a, bool vec, int threads, hipStream_t s) {
+  const dim3 g((unsigned)a.tokens), b((unsigned)threads);
+  if (vec) hipLaunchKernelGGL((k_norm<T, C, true>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((k_norm<T, C, false>), g, b, 0, s, a);
+}
+
+template <class T>
+hipError_t launch_type(const NormArgs& a, hipStream_t s) {
+  const int64_t strides = a.x_stride | (a.residual ? a.residual_stride : 0) | (a.gate ? a.gate_stride : 0);
+  const uintptr_t ptrs = (uintptr_t)a.x | (uintptr_t)a.residual | (uintptr_t)a.gate | (uintptr_t)a.sum |
+                         (uintptr_t)a.post_weight | (uintptr_t)a.weight;
+  const bool vec = a.n % 8 == 0 && strides % 8 == 0 && ptrs % 16 == 0 && (uintptr_t)a.codes % 8 == 0;
+  const int64_t groups = (a.n + 7) / 8;
+  auto threads = [&](int c) { return (int)((groups + 64 * c - 1) / (64 * c)) * 64; };
+  if (groups <= 512) launch_regs<T, 1>(a, vec, threads(1), s);
+  else if (groups <= 2048) launch_regs<T, 2>(a, vec, threads(2), s);
+  else hipLaunchKernelGGL((k_norm_long<T>), dim3((unsigned)a.tokens), dim3(kMaxThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_quantize(const NormArgs& a, hipStream_t s) {
+  // a launch has fewer than 2^32 threads: one for each 2^21 tokens
+  const int64_t es = a.dtype == Q8TA_F32 ? 4 : 2, most = (int64_t)1 << 21;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += most) {
+    NormArgs p = a;
+    p.tokens = a.tokens - t0 < most ? a.tokens - t0 : most;
+    p.x = (const char*)a.x + t0 * a.x_stride * es;
+    if (a.residual) p.residual = (const char*)a.residual + t0 * a.residual_stride * es;
+    if (a.gate) p.gate = (const char*)a.gate + t0 * a.gate_stride * es;
+    if (a.sum) p.sum = (char*)a.sum + t0 * a.n * es;
+    p.codes = a.codes + t0 * a.n;
+    p.scales = a.scales + t0;
+    hipError_t e;
+    switch (a.dtype) {
+      case Q8TA_F32: e = launch_type<float>(p, s); break;
+      case Q8TA_F16: e = launch_type<Half>(p, s); break;
+      default: e = launch_type<Bfloat>(p, s);
+    }
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace q8ta

@@ -38,6 +38,7 @@
 #include <cmath>
 
 #include "decode.h"
+#include "weights.h"
 
 namespace q8ta {
 namespace {
@@ -75,29 +76,6 @@ __device__ __forceinline__ Row make_row(float top, float temp, int shift) {
   return Row{(double)top, inv, inv * 1.4426950408889634, __builtin_ldexp(1.0, shift)};
 }
 
-// 2^y for y <= 0: 2^n times a polynomial in the rest f of [-1/2, 1/2], 1 + f * q(f)
-// with q of degree 8 through (2^f - 1) / f at nine Chebyshev points (off by
-// 4e-14 at most; exactly 1 for y = 0).
-__device__ __forceinline__ double poly(double f) {
-  double q = 0x1.b63880f16b7cap-24;
-  q = __builtin_fma(q, f, 0x1.63d1363459636p-20);
-  q = __builtin_fma(q, f, 0x1.ffcb95155d9ebp-17);
-  q = __builtin_fma(q, f, 0x1.4308ac85ac57dp-13);
-  q = __builtin_fma(q, f, 0x1.5d87fe86fe9e8p-10);
-  q = __builtin_fma(q, f, 0x1.3b2ab7181b748p-7);
-  q = __builtin_fma(q, f, 0x1.c6b08d7047e52p-5);
-  q = __builtin_fma(q, f, 0x1.ebfbdff823cedp-3);
-  q = __builtin_fma(q, f, 0x1.62e42fefa39efp-1);
-  return q;
-}
-__device__ __forceinline__ double exp2_of(double y) {
-  y = __builtin_fmax(y, -1100.0);
-  const double n = __builtin_rint(y);
-  const double f = y - n;
-  const double q = poly(f);
-  return __builtin_ldexp(__builtin_fma(q, f, 1.0), (int)n);
-}
-
 // exp((x - top) / T), 0 for -inf and 1 for the largest itself.
 __device__ __forceinline__ double weight(const Row& r, float x) {
   const double y = ((double)x - r.top) * r.scale;
@@ -123,7 +101,7 @@ struct UnitsOf {
     y = __builtin_fmax(y, -8.0);               // (also for the NaN of -inf * 0)
     const double t = y + magic;
     const double f = y - (t - magic);
-    const double q = __builtin_fma(poly(f), f, 1.0);
+    const double q = __builtin_fma(exp2_poly(f), f, 1.0);
     const uint32_t n = (uint32_t)__builtin_bit_cast(u64, t);
     const u64 w = __builtin_bit_cast(u64, q) + ((u64)(n << 20) << 32);
     const double big = 4503599627370496.0;     // 2^52 leaves the rounded value in the low bits

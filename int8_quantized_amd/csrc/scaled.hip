@@ -1,0 +1,202 @@
+// q8ta_linear_per_token and q8ta_gated_linear where there are few rows, and the
+// choice of their kernels.
+//
+//   y[m, n] = (sum_k x[m, k] w[n, k] * xs[m]) * ws[n] + bias[n]
+//   gated:  out[m, n] = act(y_gate[m, n]) * y_up[m, n]
+//
+// k_scaled_rows: 16 * MT rows by 16 * FN weight rows, for the row counts of decode
+// steps, where the weight stream is what has to be paid: the waves take every
+// WAVES-th 64-byte step of K, weight and activation fragments come straight
+// from memory into the operands of v_mfma_i32_16x16x64_i8 (16 bytes a lane, D
+// steps' loads in flight), and their integer sums meet in LDS.  The gated form
+// has a channel's gate and up rows in one workgroup, so that the block is one
+// launch and the two products never reach memory.
+#include <type_traits>
+
+#include "scaled_epilogue.h"
+
+namespace q8ta {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// FN: fragments of 16 weight rows, FN / MATS of each matrix.
+template <class YT, int MATS, int MT, int FN, int WAVES, int D>
+__global__ __launch_bounds__(64 * WAVES) void k_scaled_rows(ScaledArgs a) {
+  constexpr int BM = 16 * MT, BN = 16 * FN, C = BN / MATS, H = FN / MATS;
+  __shared__ int32_t part[WAVES][BM][BN + 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int64_t M = a.M, N = a.N, K = a.K;
+  const int64_t n0 = a.n0 + (int64_t)blockIdx.x * C, m0 = (int64_t)blockIdx.y * BM;
+  const int8_t* wp[FN];
+  const int8_t* xp[MT];
+#pragma unroll
+  for (int i = 0; i < FN; ++i) {
+    const int64_t c = n0 + 16 * (i % H) + n;
+    wp[i] = a.w[i / H] + (c < N ? c : N - 1) * K;
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int64_t m = m0 + 16 * j + n;
+    xp[j] = a.x + (m < M ? m : M - 1) * K;
+  }
+  v4i acc[FN][MT] = {};
+  v4i wf[D][FN], xf[D][MT];
+  // every load unconditional: chunks past K read the row's first bytes, and the
+  // rows' are replaced by zeros when they are used
+  auto load = [&](int64_t k, v4i (&w)[FN], v4i (&x)[MT]) {
+    const int64_t kk = k + 16 * g < K ? k + 16 * g : 0;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+      w[i] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wp[i] + kk));
+#pragma unroll
+    for (int j = 0; j < MT; ++j) x[j] = *reinterpret_cast<const v4i*>(xp[j] + kk);
+  };
+  constexpr int kStride = 64 * WAVES;
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(64 * wave + kStride * d, wf[d], xf[d]);
+  for (int64_t k0 = 64 * wave; k0 < K; k0 += kStride * D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const bool ok = k0 + kStride * d + 16 * g < K;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const v4i x = ok ? xf[d][j] : v4i{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[d][i], x, acc[i][j], 0, 0, 0);
+      }
+      if (k0 + kStride * D < K) load(k0 + kStride * (D + d), wf[d], xf[d]);
+    }
+  }
+  // register r of lane (n, g): weight row 4g + r, row n
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[wave][16 * j + n][16 * i + 4 * g + r] = acc[i][j][r];
+  // this thread's outputs; their constants are on their way while the sums meet
+  constexpr int E = (BM * C + 64 * WAVES - 1) / (64 * WAVES);
+  float xs[E], ws[E][MATS], bi[E][MATS];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int e = tid + i * 64 * WAVES;
+    const int64_t m = m0 + e / C, ch = n0 + e % C;
+    const bool in = e < BM * C && m < M && ch < N;
+    xs[i] = in ? a.xs[m] : 0.0f;
+#pragma unroll
+    for (int q = 0; q < MATS; ++q) {
+      ws[i][q] = in ? a.ws[q][ch] : 0.0f;
+      bi[i][q] = in && a.bias[q] ? a.bias[q][ch] : 0.0f;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int e = tid + i * 64 * WAVES;
+    const int row = e / C, c = e % C;
+    const int64_t m = m0 + row, ch = n0 + c;
+    if (e >= BM * C || m >= M || ch >= N) continue;
+    float y[MATS];
+#pragma unroll
+    for (int q = 0; q < MATS; ++q) {
+      int32_t s = 0;
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) s += part[v][row][q * C + c];
+      y[q] = scaled(s, xs[i], ws[i][q], bi[i][q]);
+    }
+    float out = activate(a.act, y[0]);
+    if constexpr (MATS == 2) out = out * y[1];
+    ((YT*)a.y)[m * N + ch] = from_float<YT>(out);
+  }
+}
+
+constexpr int64_t kMostThreads = (int64_t)1 << 31;   // of one launch
+
+template <class YT, int MATS, int MT, int FN, int WAVES, int D>
+hipError_t launch_shape(ScaledArgs a, hipStream_t s) {
+  constexpr int64_t C = 16 * FN / MATS, most = kMostThreads / (64 * WAVES);
+  const int64_t tiles = (a.N + C - 1) / C;
+  for (int64_t t0 = 0; t0 < tiles; t0 += most) {
+    a.n0 = t0 * C;
+    const dim3 g((unsigned)(tiles - t0 < most ? tiles - t0 : most),
+                 (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL((k_scaled_rows<YT, MATS, MT, FN, WAVES, D>), g, dim3(64 * WAVES), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <class YT>
+hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
+  if (a.mats == 2) {
+    if (a.M <= 16) return launch_shape<YT, 2, 1, 4, 8, 4>(a, s);
+    if (a.M <= 32) return launch_shape<YT, 2, 2, 4, 8, 2>(a, s);
+    return launch_shape<YT, 2, 4, 4, 8, 2>(a, s);
+  }
+  // channels of a workgroup: the fewest rounds of 256 workgroups times what one
+  // of them takes, which is about c + 1 (it reads its channels and all rows)
+  int c = 1;
+  int64_t least = INT64_MAX;
+  for (int i = 1; i <= 3; ++i) {
+    const int64_t groups = (a.N + 16 * i - 1) / (16 * i) * ((a.M + 63) / 64), cost = (groups + 255) / 256 * (i + 1);
+    if (cost <= least) {
+      least = cost;
+      c = i;
+    }
+  }
+  if (a.M <= 16) {
+    if (c == 1) return launch_shape<YT, 1, 1, 1, 16, 4>(a, s);
+    if (c == 2) return launch_shape<YT, 1, 1, 2, 8, 4>(a, s);
+    return launch_shape<YT, 1, 1, 3, 8, 4>(a, s);
+  }
+  if (a.M <= 32) {
+    if (c == 1) return launch_shape<YT, 1, 2, 1, 8, 4>(a, s);
+    if (c == 2) return launch_shape<YT, 1, 2, 2, 8, 4>(a, s);
+    return launch_shape<YT, 1, 2, 3, 16, 2>(a, s);
+  }
+  if (c == 1) return launch_shape<YT, 1, 4, 1, 16, 2>(a, s);
+  if (c == 2) return launch_shape<YT, 1, 4, 2, 8, 2>(a, s);
+  return launch_shape<YT, 1, 4, 3, 8, 2>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
+  const int64_t M = a.M, N = a.N, K = a.K, kp = (K + 15) / 16 * 16;
+  uintptr_t ptrs = (uintptr_t)a.x | (uintptr_t)a.w[0];
+  if (a.mats == 2) ptrs |= (uintptr_t)a.w[1];
+  const bool pad = K % 16 != 0 || ptrs % 16 != 0;
+  void* ws = nullptr;
+  hipError_t e = hipSuccess;
+  if (pad) {
+    e = workspace_acquire(&ws, (size_t)(M + a.mats * N) * kp, s);
+    if (e != hipSuccess) return e;
+    int8_t* to = (int8_t*)ws;
+    e = pad_rows(a.x, M, K, kp, to, s);
+    a.x = to;
+    to += M * kp;
+    for (int q = 0; q < a.mats && e == hipSuccess; ++q) {
+      e = pad_rows(a.w[q], N, K, kp, to, s);
+      a.w[q] = to;
+      to += N * kp;
+    }
+    a.K = kp;
+  }
+  if (e == hipSuccess) {
+    // (a tile's offsets are 32-bit)
+    if (M > 64 && kp <= (int64_t)1 << 23) e = launch_scaled_tiles(a, s);
+    else if (a.y_type == Q8TA_F32) e = launch_rows<float>(a, s);
+    else if (a.y_type == Q8TA_F16) e = launch_rows<Half>(a, s);
+    else e = launch_rows<Bfloat>(a, s);
+  }
+  if (!pad) return e;
+  const hipError_t f = workspace_release(ws, s);
+  return e != hipSuccess ? e : f;
+}
+
+}  // namespace q8ta

@@ -1,0 +1,42 @@
+// What the projections with scales per token and channel do with their integer
+// sums: the scales, the bias and the activation, in 32 bits, rounded once.
+#pragma once
+
+#include "decode.h"
+
+namespace q8ta {
+
+// 1 / (1 + e^-x).  e^-x = 2^y with y = -x log2(e) in two parts: rounded to one, y
+// is off by 2^-24 of itself, and 2^y by up to 40 times that.
+__device__ __forceinline__ float logistic(float x) {
+  x = __builtin_fminf(x, 128.0f);   // (infinities have no parts; a NaN comes back with v)
+  const float y = -x * 1.44269504f;
+  const float rest = __builtin_fmaf(-x, 1.44269504f, -y) - x * 1.92596299e-8f;
+  const float e = __builtin_amdgcn_exp2f(y);
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, rest * 0.693147181f, e));
+}
+
+__device__ __forceinline__ float activate(int act, float v) {
+  switch (act) {
+    case kActRelu: return v < 0.0f ? 0.0f : v;
+    // (e^-v passes the range of fp32: below -88 the value is under 2^-118)
+    case kActSilu: return v < -88.0f ? -0.0f : v * logistic(v);
+    // (the complement keeps the small outputs' bits)
+    case kActGelu: return 0.5f * v * erfcf(v * -0.707106781f);
+    case kActGeluTanh: {
+      // (1 + tanh(z / 2)) / 2 = logistic(z)
+      const float z = 1.59576912f * __builtin_fmaf(0.044715f * v * v, v, v);
+      return z < -88.0f ? -0.0f : v * logistic(z);
+    }
+    default: return v;
+  }
+}
+
+// (acc * token's scale) * channel's scale + bias, one rounding each.
+__device__ __forceinline__ float scaled(int32_t acc, float xs, float ws, float bias) {
+  float v = (float)acc * xs;
+  v = v * ws;
+  return v + bias;
+}
+
+}  // namespace q8ta
