@@ -1,363 +1,8 @@
-// Matrix-core GEMM of q8ta_linear_per_token and q8ta_gated_linear for more rows
-// than the row kernel of scaled.hip takes.
-//
-//   y[m, n] = (sum_k x[m, k] w[n, k] * xs[m]) * ws[n] + bias[n]
-//   gated:  out[m, n] = act(y_gate[m, n]) * y_up[m, n]
-//
-//  * The products run as in the eight-wave GEMM of q8ta_linear (gemm_w8.hip):
-//    64-byte K steps straight from memory into one of three LDS stages, each
-//    a shared object of its own, 32x32x32 products of waves that own 32 * FN weight
-//    rows by 64 rows of x, one barrier a step between its two slices, the loads two and
-//    a half steps ahead.  There is no zero point here, so no sums of the weights.
-//  * Weight rows are dealt out to the lanes so that the FN fragments of a lane
-//    are neighbouring channels (fragment i of lane l: channel FN * l + i of the
-//    wave's; gated: the first half gate, the second half up, of FN / 2 channels):
-//    LDS row 32 * i + l is fetched from that weight row.  A lane then stores up to 16
-//    bytes and half a wave a whole stretch of the row, straight from the
-//    accumulators, and the gated block's two factors meet in one lane.
-//  * K is a multiple of 16: chunks past it, in the last step only, come from 64
-//    bytes of zeros.
-//  * Rows past M or N read the last row; their products are not stored.
-#include <type_traits>
-
-#include "scaled_epilogue.h"
+// The matrix-core GEMM of q8ta_linear_per_token (gemm_scaled.h).
+#include "gemm_scaled.h"
 
 namespace q8ta {
-namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v16i __attribute__((ext_vector_type(16)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-#define Q8TA_LDS(p) ((__attribute__((address_space(3))) void*)(p))
-
-template <int B, int E>
-struct Static {
-  template <class F>
-  __device__ __forceinline__ static void each(F&& f) {
-    if constexpr (B < E) {
-      f(std::integral_constant<int, B>{});
-      Static<B + 1, E>::each(f);
-    }
-  }
-};
-
-// s_waitcnt immediate (gfx9 encoding): vmcnt <= vm, lgkmcnt 0, expcnt any.
-constexpr int wait_vm_lgkm0(int vm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4); }
-
-__device__ int8_t g_zeros[64] __attribute__((aligned(64)));   // never written
-
-// WAVES_N x WAVES_M waves of FN x 2 fragments of 32 x 32.
-template <int WAVES_N_, int WAVES_M_, int FN_>
-struct Tile {
-  static constexpr int WAVES_N = WAVES_N_, WAVES_M = WAVES_M_, FN = FN_, FM = 2;
-  static constexpr int WAVES = WAVES_N * WAVES_M, NT = 64 * WAVES;
-  static constexpr int TN = 32 * FN * WAVES_N, BM = 32 * FM * WAVES_M, BK = 64;
-  static constexpr int NBW = TN / 16, NBX = BM / 16;            // 16-row blocks of one step
-  static constexpr int NQ = (NBW + NBX + WAVES - 1) / WAVES;    // load instructions per wave and step
-  // bytes per stage: the blocks at 1 KiB each (W first, then X), then the landing
-  // place of the padding loads that even out the waves' counts
-  static constexpr int STAGE = WAVES * NQ * 1024;
-};
-
-__device__ __forceinline__ int swz4(int r, int c) { return c ^ ((r >> 2) & 3); }
-
-struct Smem {
-  int8_t *st0, *st1, *st2;
-  float* xs;   // the tile's rows' scales
-};
-
-// Weight row r of a tile: which matrix, and the channel within the tile.
-template <class T, int MATS>
-__device__ __forceinline__ void row_of(int r, int& mat, int& ch) {
-  constexpr int W = 32 * T::FN, H = T::FN / MATS;
-  const int wave = r / W, i = r % W / 32, l = r % 32;
-  mat = i / H;
-  ch = wave * (W / MATS) + H * l + i % H;
-}
-
-template <class YT, int H>
-__device__ __forceinline__ void put(YT* p, int live, bool vec, const float (&v)[H]) {
-  if (vec && live >= H) {
-    if constexpr (std::is_same<YT, float>::value) {
-      if constexpr (H == 4) *reinterpret_cast<v4f*>(p) = v4f{v[0], v[1], v[2], v[3]};
-      else if constexpr (H == 2) *reinterpret_cast<float2*>(p) = float2{v[0], v[1]};
-      else p[0] = v[0];
-    } else {
-      uint16_t b[H];
-#pragma unroll
-      for (int i = 0; i < H; ++i) b[i] = from_float<YT>(v[i]).bits;
-      if constexpr (H == 4)
-        *reinterpret_cast<uint2*>(p) = uint2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
-      else if constexpr (H == 2) *reinterpret_cast<uint32_t*>(p) = b[0] | (uint32_t)b[1] << 16;
-      else p[0].bits = b[0];
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < H; ++i)
-    if (i < live) p[i] = from_float<YT>(v[i]);
-}
-
-// One tile of shape T: weight rows of the tile's TN / MATS channels from c0 on,
-// rows bm0 .. of x.
-template <class T, int MATS, class YT>
-__device__ __forceinline__ void scaled_tile(const ScaledArgs& a, const Smem& sm, int64_t c0, int64_t bm0) {
-  constexpr int FN = T::FN, FM = T::FM, H = FN / MATS;
-  constexpr int NR = FN + FM;   // fragment reads per slice
-  constexpr int NP = FN * FM;   // products per slice
-  static_assert(NP >= NR, "a read behind each product");
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wave / T::WAVES_M, wm = wave % T::WAVES_M;
-  const int64_t M = a.M, N = a.N, K = a.K;
-  const int KT = (int)((K + T::BK - 1) / T::BK);
-  const int wr0 = 32 * FN * wn, xr0 = 32 * FM * wm;
-  const int lrow = lane & 31, kg = lane >> 5;
-
-  // Load instruction q of this wave moves 16-row block wave * NQ + q of a step (W
-  // blocks, X blocks, then padding: a repeat of the tile's first X rows).  Lane
-  // l takes row l / 4 of the block and the chunk that belongs at chunk
-  // position l % 4 of that LDS row.
-  const int8_t* gb[T::NQ];
-  uint32_t voff[T::NQ];
-  const int br = lane >> 2, chunk = swz4(br, lane & 3);
-  Static<0, T::NQ>::each([&](auto Q) {
-    constexpr int q = decltype(Q)::value;
-    const int blk = wave * T::NQ + q;
-    if (blk < T::NBW) {
-      int mat, ch, first;
-      row_of<T, MATS>(16 * blk, mat, first);   // (a block's rows are of one matrix)
-      row_of<T, MATS>(16 * blk + br, mat, ch);
-      const int64_t n = c0 + ch < N ? c0 + ch : N - 1;
-      gb[q] = (MATS == 2 && __builtin_amdgcn_readfirstlane(mat) ? a.w[MATS - 1] : a.w[0]) + c0 * K;
-      voff[q] = (uint32_t)((n - c0) * K + 16 * chunk);
-    } else {
-      const int xb = blk < T::NBW + T::NBX ? blk - T::NBW : 0;
-      const int64_t m = bm0 + 16 * xb + br;
-      gb[q] = a.x + bm0 * K;
-      voff[q] = (uint32_t)(((m < M ? m : M - 1) - bm0) * K + 16 * chunk);
-    }
-  });
-  if (tid < T::BM) sm.xs[tid] = a.xs[bm0 + tid < M ? bm0 + tid : M - 1];
-
-  auto stage = [&](auto SI) -> int8_t* {
-    constexpr int si = decltype(SI)::value;
-    if constexpr (si == 0) return sm.st0;
-    else if constexpr (si == 1) return sm.st1;
-    else return sm.st2;
-  };
-  const bool ragged = K % T::BK != 0;
-  const bool past = (int64_t)(KT - 1) * T::BK + 16 * chunk >= K;   // this lane's chunk of the last step
-  auto issue = [&](int k, auto SI) {
-    int8_t* d = stage(SI) + wave * T::NQ * 1024;
-    if (ragged && k == KT - 1) {
-      Static<0, T::NQ>::each([&](auto Q) {
-        constexpr int q = decltype(Q)::value;
-        const int8_t* p = gb[q] + (int64_t)k * T::BK + voff[q];
-        __builtin_amdgcn_global_load_lds((const void*)(past ? g_zeros : p), Q8TA_LDS(d + q * 1024), 16, 0, 0);
-      });
-    } else {
-      Static<0, T::NQ>::each([&](auto Q) {
-        constexpr int q = decltype(Q)::value;
-        __builtin_amdgcn_global_load_lds((const void*)(gb[q] + (int64_t)k * T::BK + voff[q]),
-                                         Q8TA_LDS(d + q * 1024), 16, 0, 0);
-      });
-    }
-  };
-
-  v16i acc[FN][FM];
-  Static<0, FN>::each([&](auto I) {
-    Static<0, FM>::each([&](auto J) { acc[decltype(I)::value][decltype(J)::value] = v16i{}; });
-  });
-  const int a_off = (wr0 + lrow) * T::BK;
-  const int b_off = T::TN * T::BK + (xr0 + lrow) * T::BK;
-  auto read_frag = [&](const int8_t* S, v4i (&af)[FN], v4i (&bf)[FM], auto KSI, auto R) {
-    constexpr int ks = decltype(KSI)::value, r = decltype(R)::value;
-    const int cpos = 16 * swz4(lrow, 2 * ks + kg);
-    if constexpr (r < FN) af[r] = *reinterpret_cast<const v4i*>(S + a_off + r * 32 * T::BK + cpos);
-    else bf[r - FN] = *reinterpret_cast<const v4i*>(S + b_off + (r - FN) * 32 * T::BK + cpos);
-  };
-  auto product = [&](const v4i (&af)[FN], const v4i (&bf)[FM], auto I, auto J) {
-    constexpr int i = decltype(I)::value, j = decltype(J)::value;
-    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
-  };
-  constexpr std::integral_constant<int, 0> K0{};
-  constexpr std::integral_constant<int, 1> K1{};
-
-  // Step k, its slab in stage k % 3 and slice 0's fragments in registers: the
-  // products of slice 0, each followed by a fragment read of slice 1; the wait
-  // for this wave's part of step k + 1 and the barrier; the load of step k + 3 into the
-  // stage that is free now; the products of slice 1, each followed by a
-  // fragment read of step k + 1.
-  v4i af[2][FN], bf[2][FM];
-  auto body = [&](int k, auto SI) {
-    constexpr int si = decltype(SI)::value;
-    using SNX = std::integral_constant<int, (si + 1) % 3>;
-    const int8_t* S = stage(SI);
-    const int8_t* SN = stage(SNX{});
-    Static<0, NP>::each([&](auto MI) {
-      constexpr int m = decltype(MI)::value;
-      product(af[0], bf[0], std::integral_constant<int, m / FM>{}, std::integral_constant<int, m % FM>{});
-      if constexpr (m < NR) read_frag(S, af[1], bf[1], K1, MI);
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(T::NQ));
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    issue(k + 3 < KT ? k + 3 : KT - 1, SI);
-    __builtin_amdgcn_sched_barrier(0);
-    Static<0, NP>::each([&](auto MI) {
-      constexpr int m = decltype(MI)::value;
-      product(af[1], bf[1], std::integral_constant<int, m / FM>{}, std::integral_constant<int, m % FM>{});
-      if constexpr (m < NR) read_frag(SN, af[0], bf[0], K0, MI);
-      __builtin_amdgcn_sched_barrier(0);
-    });
-  };
-  constexpr std::integral_constant<int, 0> S0{};
-  constexpr std::integral_constant<int, 1> S1{};
-  constexpr std::integral_constant<int, 2> S2{};
-  issue(0, S0);
-  issue(KT > 1 ? 1 : 0, S1);
-  issue(KT > 2 ? 2 : KT - 1, S2);
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(2 * T::NQ));   // this wave's part of step 0
-  __builtin_amdgcn_s_barrier();
-  Static<0, NR>::each([&](auto R) { read_frag(sm.st0, af[0], bf[0], K0, R); });
-  int k = 0;
-  for (; k + 3 <= KT; k += 3) {
-    body(k, S0);
-    body(k + 1, S1);
-    body(k + 2, S2);
-  }
-  if (k < KT) body(k, S0);
-  if (k + 1 < KT) body(k + 1, S1);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-
-  // lane l: channels ch .. ch + H - 1; register r of fragment (i, j): row xr0 +
-  // 32 j + 8 (r / 4) + 4 (l / 32) + r % 4
-  const int64_t ch = c0 + wn * (32 * FN / MATS) + H * lrow;
-  const int live = ch >= N ? 0 : (N - ch < H ? (int)(N - ch) : H);
-  const bool vec = N % H == 0 && ((uintptr_t)a.y & (H * sizeof(YT) - 1)) == 0;
-  float ws[MATS][H], bi[MATS][H];
-#pragma unroll
-  for (int q = 0; q < MATS; ++q)
-#pragma unroll
-    for (int i = 0; i < H; ++i) {
-      ws[q][i] = i < live ? a.ws[q][ch + i] : 0.0f;
-      bi[q][i] = i < live && a.bias[q] ? a.bias[q][ch + i] : 0.0f;
-    }
-  YT* out = (YT*)a.y;
-  Static<0, FM>::each([&](auto J) {
-    constexpr int j = decltype(J)::value;
-    Static<0, 4>::each([&](auto G) {
-      constexpr int g = decltype(G)::value;
-      const int row = xr0 + 32 * j + 8 * g + 4 * kg;
-      const v4f xs = *reinterpret_cast<const v4f*>(sm.xs + row);
-      Static<0, 4>::each([&](auto R) {
-        constexpr int r = decltype(R)::value;
-        float v[H];
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-          v[i] = activate(a.act, scaled(acc[i][j][4 * g + r], xs[r], ws[0][i], bi[0][i]));
-          if constexpr (MATS == 2)
-            v[i] = v[i] * scaled(acc[FN - H + i][j][4 * g + r], xs[r], ws[MATS - 1][i], bi[MATS - 1][i]);
-        }
-        const int64_t m = bm0 + row + r;
-        if (m < M) put<YT, H>(out + m * N + ch, live, vec, v);
-      });
-    });
-  });
-}
-
-// Workgroups below ta take tiles of shape TA (ma of them along M, M fastest), the
-// rest tiles of shape TB from channel cb on: the columns left after whole rounds
-// of TA tiles, in one launch.  Within each part the workgroups, which go
-// round the 8 XCDs, are renumbered so that an XCD walks a contiguous run of tiles, which
-// share slabs in its L2.
-template <class TA, class TB, int MATS, class YT>
-__global__ __launch_bounds__(TA::NT, 1) void k_gemm_scaled(ScaledArgs a, int ma, int ta, int mb, int tb,
-                                                            int64_t cb) {
-  static_assert(TA::NT == TB::NT, "one block size");
-  constexpr int STAGE = TA::STAGE > TB::STAGE ? TA::STAGE : TB::STAGE;
-  constexpr int BM = TA::BM > TB::BM ? TA::BM : TB::BM;
-  __shared__ __attribute__((aligned(16))) int8_t st0[STAGE];
-  __shared__ __attribute__((aligned(16))) int8_t st1[STAGE];
-  __shared__ __attribute__((aligned(16))) int8_t st2[STAGE];
-  __shared__ __attribute__((aligned(16))) float xs[BM];
-  const Smem sm{st0, st1, st2, xs};
-  auto remap = [](int b, int nt) {
-    const int per = nt / 8;
-    return b < per * 8 ? (b % 8) * per + (b / 8) : b;
-  };
-  const int b = blockIdx.x;
-  if (b < ta) {
-    const int t = remap(b, ta);
-    scaled_tile<TA, MATS, YT>(a, sm, (int64_t)(t / ma) * (TA::TN / MATS), (int64_t)(t % ma) * TA::BM);
-  } else {
-    const int t = remap(b - ta, tb);
-    scaled_tile<TB, MATS, YT>(a, sm, cb + (int64_t)(t / mb) * (TB::TN / MATS), (int64_t)(t % mb) * TB::BM);
-  }
-}
-
-using T256 = Tile<2, 4, 4>;   // 256 weight rows x 256 rows, waves of 128 x 64
-using T128 = Tile<4, 2, 2>;   // 256 x 128, waves of 64 x 64
-using T64 = Tile<2, 2, 2>;    // 128 x 128, four waves
-using T32 = Tile<1, 1, 2>;    // 64 x 64, one wave
-
-// A launch has fewer than 2^32 threads: columns go in as many as it takes.
-constexpr int64_t kMostTiles = (int64_t)1 << 21;
-
-template <class T, int MATS, class YT>
-hipError_t launch_one(const ScaledArgs& a, hipStream_t s) {
-  constexpr int64_t C = T::TN / MATS;
-  const int64_t m = (a.M + T::BM - 1) / T::BM, n = (a.N + C - 1) / C;
-  const int64_t most = kMostTiles / m > 0 ? kMostTiles / m : 1;
-  for (int64_t n0 = 0; n0 < n; n0 += most) {
-    const int64_t part = n - n0 < most ? n - n0 : most;
-    hipLaunchKernelGGL((k_gemm_scaled<T, T, MATS, YT>), dim3((unsigned)(m * part)), dim3(T::NT), 0, s, a, (int)m,
-                       0, (int)m, (int)(m * part), n0 * C);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
-template <int MATS, class YT>
-hipError_t launch_plan(const ScaledArgs& a, hipStream_t s) {
-  constexpr int64_t CN = T256::TN / MATS;
-  static_assert(T128::TN == T256::TN, "one width");
-  const int64_t n = (a.N + CN - 1) / CN;
-  const int64_t ma = (a.M + T256::BM - 1) / T256::BM, mb = (a.M + T128::BM - 1) / T128::BM;
-  const int64_t tiles = ma * n;
-  if (tiles < 192) {
-    const int64_t small = ((a.M + 127) / 128) * ((a.N + 128 / MATS - 1) / (128 / MATS));
-    return small >= 256 ? launch_one<T64, MATS, YT>(a, s) : launch_one<T32, MATS, YT>(a, s);
-  }
-  int64_t cols = n, rest = 0;
-  if (tiles % 256 != 0 && 256 % ma == 0 && tiles > 256) {
-    const int64_t c = tiles / 256 * 256 / ma;
-    if ((n - c) * mb <= 256) {
-      cols = c;
-      rest = n - c;
-    }
-  }
-  if (rest == 0 || tiles > kMostTiles) return launch_one<T256, MATS, YT>(a, s);
-  hipLaunchKernelGGL((k_gemm_scaled<T256, T128, MATS, YT>), dim3((unsigned)(ma * cols + mb * rest)),
-                     dim3(T256::NT), 0, s, a, (int)ma, (int)(ma * cols), (int)mb, (int)(mb * rest), cols * CN);
-  return hipGetLastError();
-}
-
-template <int MATS>
-hipError_t launch_type(const ScaledArgs& a, hipStream_t s) {
-  if (a.y_type == Q8TA_F32) return launch_plan<MATS, float>(a, s);
-  if (a.y_type == Q8TA_F16) return launch_plan<MATS, Half>(a, s);
-  return launch_plan<MATS, Bfloat>(a, s);
-}
-
-}  // namespace
-
-hipError_t launch_scaled_tiles(const ScaledArgs& a, hipStream_t s) {
-  return a.mats == 2 ? launch_type<2>(a, s) : launch_type<1>(a, s);
-}
+hipError_t launch_linear_tiles(const ScaledArgs& a, hipStream_t s) { return launch_type<1>(a, s); }
 
 }  // namespace q8ta

@@ -21,58 +21,58 @@
 namespace q8ta {
 namespace {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxThreads = 1024;
 
-// Eight elements from p on; `live` of them where not VEC.
-template <bool VEC>
-__device__ __forceinline__ void load8(const float* p, int live, float (&x)[8]) {
-  if constexpr (VEC) {
-    const v4f a = *reinterpret_cast<const v4f*>(p), b = *reinterpret_cast<const v4f*>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = a[i];
-      x[4 + i] = b[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < live ? p[i] : 0.0f;
-  }
-}
+// Eight elements as they lie in memory.
+template <class T>
+struct Raw {
+  v4u v[sizeof(T) / 2];
+};
+// From p on; `live` of them, zeros behind, where not VEC.
 template <bool VEC, class T>
-__device__ __forceinline__ void load8(const T* p, int live, float (&x)[8]) {
+__device__ __forceinline__ Raw<T> load8(const T* p, int live) {
+  Raw<T> r;
   if constexpr (VEC) {
-    const v4u v = *reinterpret_cast<const v4u*>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_float(T{(uint16_t)(v[i / 2] >> (16 * (i % 2)))});
+    for (int j = 0; j < (int)sizeof(T) / 2; ++j) r.v[j] = reinterpret_cast<const v4u*>(p)[j];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < live ? to_float(p[i]) : 0.0f;
+    for (int j = 0; j < (int)sizeof(T) / 2; ++j) r.v[j] = v4u{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= live) continue;
+      if constexpr (sizeof(T) == 4) r.v[i / 4][i % 4] = __builtin_bit_cast(uint32_t, p[i]);
+      else r.v[0][i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (16 * (i % 2));
+    }
   }
+  return r;
 }
-template <bool VEC>
-__device__ __forceinline__ void store8(float* p, int live, const float (&x)[8]) {
-  if constexpr (VEC) {
-    *reinterpret_cast<v4f*>(p) = v4f{x[0], x[1], x[2], x[3]};
-    *reinterpret_cast<v4f*>(p + 4) = v4f{x[4], x[5], x[6], x[7]};
+template <class T>
+__device__ __forceinline__ float element(const Raw<T>& r, int i) {
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t w = r.v[i / 4][i % 4];
+    return __builtin_bit_cast(float, w);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < live) p[i] = x[i];
+    return to_float(T{(uint16_t)(r.v[0][i / 2] >> (16 * (i % 2)))});
   }
 }
 // (x is of the type already: no rounding)
 template <bool VEC, class T>
 __device__ __forceinline__ void store8(T* p, int live, const float (&x)[8]) {
   if constexpr (VEC) {
-    v4u v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = (uint32_t)from_float<T>(x[2 * i]).bits | (uint32_t)from_float<T>(x[2 * i + 1]).bits << 16;
-    *reinterpret_cast<v4u*>(p) = v;
+    for (int j = 0; j < (int)sizeof(T) / 2; ++j) {
+      v4u v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) v[i] = __builtin_bit_cast(uint32_t, x[4 * j + i]);
+        else v[i] = (uint32_t)from_float<T>(x[2 * i]).bits | (uint32_t)from_float<T>(x[2 * i + 1]).bits << 16;
+      }
+      reinterpret_cast<v4u*>(p)[j] = v;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -127,23 +127,28 @@ __device__ __forceinline__ int code_of(double z, double top, double inv) {
   return (int)r;
 }
 
-// The row's scale and 127 / max; a row with a value that is not finite has the
-// scale NaN and codes 0, as has one of zeros with the scale 0.
-struct Scale {
-  double top, inv;
-  float scale;
-};
-__device__ __forceinline__ Scale scale_of(double top) {
-  Scale s{top, 0.0, 0.0f};
-  if (top > 0.0) {
-    s.inv = 127.0 / top;
-    s.scale = (float)(top / 127.0);
-  }
-  if (!(top < (double)__builtin_inff())) {
-    s.inv = 0.0;
-    s.scale = __builtin_nanf("");
-  }
-  return s;
+// 1 / x and 1 / sqrt(x) to the last bit or two, from the estimates by Newton steps.
+__device__ __forceinline__ double reciprocal(double x) {
+  double y = __builtin_amdgcn_rcp(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+  return y;
+}
+__device__ __forceinline__ double reciprocal_root(double x) {
+  double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = __builtin_fma(__builtin_fma(-x * y, y, 1.0), 0.5 * y, y);
+  return y;
+}
+
+// The row's scale; 127 / max goes to inv.  A row with a value that is not finite
+// has the scale NaN and codes 0 (inv 0), as has one of zeros with the scale 0.
+__device__ __forceinline__ float scale_of(double top) {
+  if (!(top < (double)__builtin_inff())) return __builtin_nanf("");
+  return (float)(top / 127.0);
+}
+__device__ __forceinline__ double inv_of(double top) {
+  return top > 0.0 && top < (double)__builtin_inff() ? 127.0 * reciprocal(top) : 0.0;
 }
 
 // h = residual_scale * residual + gate * b as it is stored.
@@ -157,77 +162,90 @@ __device__ __forceinline__ float sum_of(double b, bool has_gate, float gate, boo
 
 // C: groups of 8 elements a thread.
 template <class T, int C, bool VEC>
-__global__ __launch_bounds__(kMaxThreads) void k_norm(NormArgs a) {
+__global__ __launch_bounds__(kMaxThreads, C == 1 ? 8 : 4) void k_norm(NormArgs a, double inv_n) {
   __shared__ double sh[3][kMaxThreads / 64];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int64_t t = blockIdx.x;
   const int n = (int)a.n;
-  const T* x = (const T*)a.x + t * a.x_stride;
-  const T* res = (const T*)a.residual + t * a.residual_stride;
-  const T* gate = (const T*)a.gate + t * a.gate_stride;
-  float h[C][8], r[C][8], g[C][8], w[C][8], pw[C][8];
+  Raw<T> xr[C], rr[C], gr[C];
+  Raw<float> pw[C], w[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int e = 8 * (tid + c * nt);
-    const int live = n - e;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[c][i] = r[c][i] = g[c][i] = w[c][i] = pw[c][i] = 0.0f;
-    if (live > 0) {
-      load8<VEC>(x + e, live, h[c]);
-      if (a.residual) load8<VEC>(res + e, live, r[c]);
-      if (a.gate) load8<VEC>(gate + e, live, g[c]);
-      if (a.post_weight) load8<VEC>(a.post_weight + e, live, pw[c]);
-      if (a.weight) load8<VEC>(a.weight + e, live, w[c]);
-    }
+    const int live = n - e, at = live > 0 ? e : 0;   // (threads past the row read its first elements)
+    const int some = live > 0 ? live : 0;
+    xr[c] = load8<VEC>((const T*)a.x + t * a.x_stride + at, some);
+    if (a.residual) rr[c] = load8<VEC>((const T*)a.residual + t * a.residual_stride + at, some);
+    if (a.gate) gr[c] = load8<VEC>((const T*)a.gate + t * a.gate_stride + at, some);
+    if (a.post_weight) pw[c] = load8<VEC>(a.post_weight + at, some);
+    if (a.weight) w[c] = load8<VEC>(a.weight + at, some);
   }
   double post = 1.0;
   if (a.post_weight) {
     double s = 0.0;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      if (8 * (tid + c * nt) >= n) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = __builtin_fma((double)h[c][i], (double)h[c][i], s);
-    post = 1.0 / __builtin_sqrt(over_row(s, sh[0], plus_of) / (double)n + a.eps);
+      for (int i = 0; i < 8; ++i) {
+        const double v = element(xr[c], i);
+        s = __builtin_fma(v, v, s);
+      }
+    }
+    post = reciprocal_root(__builtin_fma(over_row(s, sh[0], plus_of), inv_n, a.eps));
   }
+  float h[C][8];
   double s = 0.0;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      double b = h[c][i];
-      if (a.post_weight) b = b * post * (double)pw[c][i];
-      h[c][i] = sum_of<T>(b, a.gate != nullptr, g[c][i], a.residual != nullptr, r[c][i], a.residual_scale);
-      s = __builtin_fma((double)h[c][i], (double)h[c][i], s);
+      double b = element(xr[c], i);
+      if (a.post_weight) b = b * post * (double)element(pw[c], i);
+      h[c][i] = sum_of<T>(b, a.gate != nullptr, element(gr[c], i), a.residual != nullptr, element(rr[c], i),
+                          a.residual_scale);
     }
+    const int e = 8 * (tid + c * nt);
+    if (e >= n) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __builtin_fma((double)h[c][i], (double)h[c][i], s);
+    if (a.sum) store8<VEC>((T*)a.sum + t * a.n + e, n - e, h[c]);
+  }
   double rstd = 1.0;
-  if (a.weight) rstd = 1.0 / __builtin_sqrt(over_row(s, sh[1], plus_of) / (double)n + a.eps);
+  if (a.weight) rstd = reciprocal_root(__builtin_fma(over_row(s, sh[1], plus_of), inv_n, a.eps));
   auto z_of = [&](int c, int i) {
     const double z = h[c][i];
-    return a.weight ? z * rstd * (double)w[c][i] : z;
+    return a.weight ? z * rstd * (double)element(w[c], i) : z;
   };
-  double top = 0.0;
+  // (a maximum would drop a NaN: z * 0 keeps it, and infinities)
+  double top = 0.0, odd = 0.0;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    if (8 * (tid + c * nt) >= n) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = top_of(__builtin_fabs(z_of(c, i)), top);
-  const Scale sc = scale_of(over_row(top, sh[2], top_of));
-  if (tid == 0) a.scales[t] = sc.scale;
+    for (int i = 0; i < 8; ++i) {
+      const double z = z_of(c, i);
+      top = __builtin_fmax(top, __builtin_fabs(z));
+      odd = __builtin_fma(z, 0.0, odd);
+    }
+  }
+  top = over_row(odd == 0.0 ? top : __builtin_nan(""), sh[2], top_of);
+  const double inv = inv_of(top);
+  if (tid == 0) a.scales[t] = scale_of(top);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int e = 8 * (tid + c * nt);
-    const int live = n - e;
-    if (live <= 0) continue;
-    if (a.sum) store8<VEC>((T*)a.sum + t * a.n + e, live, h[c]);
+    if (e >= n) continue;
     int q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = sc.inv > 0.0 ? code_of(z_of(c, i), sc.top, sc.inv) : 0;
+    for (int i = 0; i < 8; ++i) q[i] = inv > 0.0 ? code_of(z_of(c, i), top, inv) : 0;
     int8_t* dst = a.codes + t * a.n + e;
     if constexpr (VEC) {
       *reinterpret_cast<v2u*>(dst) = v2u{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < live) dst[i] = (int8_t)q[i];
+        if (i < n - e) dst[i] = (int8_t)q[i];
     }
   }
 }
@@ -235,7 +253,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_norm(NormArgs a) {
 // Rows of any length: the row is read again for each sum.  Every thread writes
 // only what it alone has read, last (the sum may stand in x's or the residual's place).
 template <class T>
-__global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a) {
+__global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a, double inv_n) {
   __shared__ double sh[3][kMaxThreads / 64];
   const int tid = threadIdx.x;
   const int64_t t = blockIdx.x;
@@ -258,7 +276,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a) {
       const double v = to_float(x[e]);
       s = __builtin_fma(v, v, s);
     }
-    post = 1.0 / __builtin_sqrt(over_row(s, sh[0], plus_of) / (double)a.n + a.eps);
+    post = reciprocal_root(__builtin_fma(over_row(s, sh[0], plus_of), inv_n, a.eps));
   }
   if (a.weight) {
     double s = 0.0;
@@ -266,15 +284,16 @@ __global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a) {
       const double v = h_of(e);
       s = __builtin_fma(v, v, s);
     }
-    rstd = 1.0 / __builtin_sqrt(over_row(s, sh[1], plus_of) / (double)a.n + a.eps);
+    rstd = reciprocal_root(__builtin_fma(over_row(s, sh[1], plus_of), inv_n, a.eps));
   }
   double top = 0.0;
   for (int64_t e = tid; e < a.n; e += kMaxThreads) top = top_of(__builtin_fabs(z_of(e, h_of(e))), top);
-  const Scale sc = scale_of(over_row(top, sh[2], top_of));
-  if (tid == 0) a.scales[t] = sc.scale;
+  top = over_row(top, sh[2], top_of);
+  const double inv = inv_of(top);
+  if (tid == 0) a.scales[t] = scale_of(top);
   for (int64_t e = tid; e < a.n; e += kMaxThreads) {
     const float h = h_of(e);
-    const int q = sc.inv > 0.0 ? code_of(z_of(e, h), sc.top, sc.inv) : 0;
+    const int q = inv > 0.0 ? code_of(z_of(e, h), top, inv) : 0;
     if (a.sum) ((T*)a.sum)[t * a.n + e] = from_float<T>(h);
     a.codes[t * a.n + e] = (int8_t)q;
   }
@@ -283,8 +302,8 @@ __global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a) {
 template <class T, int C>
 void launch_regs(const NormArgs& a, bool vec, int threads, hipStream_t s) {
   const dim3 g((unsigned)a.tokens), b((unsigned)threads);
-  if (vec) hipLaunchKernelGGL((k_norm<T, C, true>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((k_norm<T, C, false>), g, b, 0, s, a);
+  if (vec) hipLaunchKernelGGL((k_norm<T, C, true>), g, b, 0, s, a, 1.0 / (double)a.n);
+  else hipLaunchKernelGGL((k_norm<T, C, false>), g, b, 0, s, a, 1.0 / (double)a.n);
 }
 
 template <class T>
@@ -295,9 +314,10 @@ hipError_t launch_type(const NormArgs& a, hipStream_t s) {
   const bool vec = a.n % 8 == 0 && strides % 8 == 0 && ptrs % 16 == 0 && (uintptr_t)a.codes % 8 == 0;
   const int64_t groups = (a.n + 7) / 8;
   auto threads = [&](int c) { return (int)((groups + 64 * c - 1) / (64 * c)) * 64; };
-  if (groups <= 512) launch_regs<T, 1>(a, vec, threads(1), s);
+  if (groups <= 1024) launch_regs<T, 1>(a, vec, threads(1), s);
   else if (groups <= 2048) launch_regs<T, 2>(a, vec, threads(2), s);
-  else hipLaunchKernelGGL((k_norm_long<T>), dim3((unsigned)a.tokens), dim3(kMaxThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_norm_long<T>), dim3((unsigned)a.tokens), dim3(kMaxThreads), 0, s, a,
+                          1.0 / (double)a.n);
   return hipGetLastError();
 }
 

@@ -49,8 +49,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_scaled_rows(ScaledArgs a) {
   auto load = [&](int64_t k, v4i (&w)[FN], v4i (&x)[MT]) {
     const int64_t kk = k + 16 * g < K ? k + 16 * g : 0;
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
-      w[i] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(wp[i] + kk));
+    for (int i = 0; i < FN; ++i) w[i] = *reinterpret_cast<const v4i*>(wp[i] + kk);
 #pragma unroll
     for (int j = 0; j < MT; ++j) x[j] = *reinterpret_cast<const v4i*>(xp[j] + kk);
   };
@@ -94,6 +93,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_scaled_rows(ScaledArgs a) {
     }
   }
   __syncthreads();
+  with_activation<MATS>(a.act, [&](auto ACT) {
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const int e = tid + i * 64 * WAVES;
@@ -108,10 +108,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_scaled_rows(ScaledArgs a) {
       for (int v = 0; v < WAVES; ++v) s += part[v][row][q * C + c];
       y[q] = scaled(s, xs[i], ws[i][q], bi[i][q]);
     }
-    float out = activate(a.act, y[0]);
+    float out = activate<decltype(ACT)::value>(y[0]);
     if constexpr (MATS == 2) out = out * y[1];
     ((YT*)a.y)[m * N + ch] = from_float<YT>(out);
   }
+  });
 }
 
 constexpr int64_t kMostThreads = (int64_t)1 << 31;   // of one launch
@@ -131,37 +132,34 @@ hipError_t launch_shape(ScaledArgs a, hipStream_t s) {
   return hipSuccess;
 }
 
+// Of the matrices' 16-channel fragments a workgroup takes one each, and sixteen waves
+// share K (1 x 4096 x 4096 4.7 us, with eight waves 5.4, with three fragments 7.9).  For
+// up to 16 rows of the gated form three each, where that is fewer rounds of 256
+// workgroups times what one takes (1 x 11008: 16.9 us against 18.4, 1 x 2048: 8.0
+// and 4.3).  Plain loads: nontemporal ones took 10 to 20 % longer, also for weights that
+// no cache holds.
 template <class YT>
 hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
   if (a.mats == 2) {
-    if (a.M <= 16) return launch_shape<YT, 2, 1, 4, 8, 4>(a, s);
-    if (a.M <= 32) return launch_shape<YT, 2, 2, 4, 8, 2>(a, s);
-    return launch_shape<YT, 2, 4, 4, 8, 2>(a, s);
-  }
-  // channels of a workgroup: the fewest rounds of 256 workgroups times what one
-  // of them takes, which is about c + 1 (it reads its channels and all rows)
-  int c = 1;
-  int64_t least = INT64_MAX;
-  for (int i = 1; i <= 3; ++i) {
-    const int64_t groups = (a.N + 16 * i - 1) / (16 * i) * ((a.M + 63) / 64), cost = (groups + 255) / 256 * (i + 1);
-    if (cost <= least) {
-      least = cost;
-      c = i;
+    if (a.M <= 16) {
+      auto cost = [&](int64_t c) { return ((a.N + 16 * c - 1) / (16 * c) + 255) / 256 * (c + 1); };
+      return cost(3) < cost(1) ? launch_shape<YT, 2, 1, 6, 16, 2>(a, s) : launch_shape<YT, 2, 1, 2, 16, 2>(a, s);
     }
+    return a.M <= 32 ? launch_shape<YT, 2, 2, 2, 16, 2>(a, s) : launch_shape<YT, 2, 4, 2, 8, 2>(a, s);
   }
-  if (a.M <= 16) {
-    if (c == 1) return launch_shape<YT, 1, 1, 1, 16, 4>(a, s);
-    if (c == 2) return launch_shape<YT, 1, 1, 2, 8, 4>(a, s);
-    return launch_shape<YT, 1, 1, 3, 8, 4>(a, s);
-  }
-  if (a.M <= 32) {
-    if (c == 1) return launch_shape<YT, 1, 2, 1, 8, 4>(a, s);
-    if (c == 2) return launch_shape<YT, 1, 2, 2, 8, 4>(a, s);
-    return launch_shape<YT, 1, 2, 3, 16, 2>(a, s);
-  }
-  if (c == 1) return launch_shape<YT, 1, 4, 1, 16, 2>(a, s);
-  if (c == 2) return launch_shape<YT, 1, 4, 2, 8, 2>(a, s);
-  return launch_shape<YT, 1, 4, 3, 8, 2>(a, s);
+  // all of a wave's steps in flight at once, where there are up to four (4096 x 11008:
+  // 10.7 us with four at a time, 9.8 with two)
+  if (a.M <= 16)
+    return a.K <= 4096 ? launch_shape<YT, 1, 1, 1, 16, 4>(a, s) : launch_shape<YT, 1, 1, 1, 16, 2>(a, s);
+  return a.M <= 32 ? launch_shape<YT, 1, 2, 1, 16, 4>(a, s) : launch_shape<YT, 1, 4, 1, 16, 2>(a, s);
+}
+
+// The row kernel reads all rows of x for 16 channels: up to 16 rows it is the faster
+// everywhere, up to 64 where one round of 256 workgroups holds the channels (50 rows x
+// 4096 x 4096 10.2 us against 11.5 with the tiles, x 11008 27 and 12.8).  (A tile's
+// offsets are 32-bit.)
+bool by_rows(const ScaledArgs& a) {
+  return a.M <= 16 || (a.M <= 64 && a.N <= 16 * 256) || a.K > (int64_t)1 << 23;
 }
 
 }  // namespace
@@ -188,8 +186,7 @@ hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
     a.K = kp;
   }
   if (e == hipSuccess) {
-    // (a tile's offsets are 32-bit)
-    if (M > 64 && kp <= (int64_t)1 << 23) e = launch_scaled_tiles(a, s);
+    if (!by_rows(a)) e = a.mats == 2 ? launch_gated_tiles(a, s) : launch_linear_tiles(a, s);
     else if (a.y_type == Q8TA_F32) e = launch_rows<float>(a, s);
     else if (a.y_type == Q8TA_F16) e = launch_rows<Half>(a, s);
     else e = launch_rows<Bfloat>(a, s);

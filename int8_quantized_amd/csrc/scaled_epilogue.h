@@ -2,6 +2,8 @@
 // sums: the scales, the bias and the activation, in 32 bits, rounded once.
 #pragma once
 
+#include <type_traits>
+
 #include "decode.h"
 
 namespace q8ta {
@@ -16,19 +18,33 @@ __device__ __forceinline__ float logistic(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, rest * 0.693147181f, e));
 }
 
-__device__ __forceinline__ float activate(int act, float v) {
-  switch (act) {
-    case kActRelu: return v < 0.0f ? 0.0f : v;
-    // (e^-v passes the range of fp32: below -88 the value is under 2^-118)
-    case kActSilu: return v < -88.0f ? -0.0f : v * logistic(v);
-    // (the complement keeps the small outputs' bits)
-    case kActGelu: return 0.5f * v * erfcf(v * -0.707106781f);
-    case kActGeluTanh: {
-      // (1 + tanh(z / 2)) / 2 = logistic(z)
-      const float z = 1.59576912f * __builtin_fmaf(0.044715f * v * v, v, v);
-      return z < -88.0f ? -0.0f : v * logistic(z);
-    }
-    default: return v;
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (ACT == kActRelu) return v < 0.0f ? 0.0f : v;
+  // (e^-v passes the range of fp32: below -88 the value is under 2^-118)
+  if constexpr (ACT == kActSilu) return v < -88.0f ? -0.0f : v * logistic(v);
+  // (the complement keeps the small outputs' bits)
+  if constexpr (ACT == kActGelu) return 0.5f * v * erfcf(v * -0.707106781f);
+  if constexpr (ACT == kActGeluTanh) {
+    // (1 + tanh(z / 2)) / 2 = logistic(z)
+    const float z = 1.59576912f * __builtin_fmaf(0.044715f * v * v, v, v);
+    return z < -88.0f ? -0.0f : v * logistic(z);
+  }
+  return v;
+}
+
+// f(integral_constant) of the activation: one branch for all of a thread's outputs
+// (with a branch at each of them the code does not fit the instruction cache).
+template <int MATS, class F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  if constexpr (MATS == 1) {
+    if (act == kActRelu) f(std::integral_constant<int, kActRelu>{});
+    else f(std::integral_constant<int, kActNone>{});
+  } else {
+    if (act == kActSilu) f(std::integral_constant<int, kActSilu>{});
+    else if (act == kActGelu) f(std::integral_constant<int, kActGelu>{});
+    else if (act == kActGeluTanh) f(std::integral_constant<int, kActGeluTanh>{});
+    else f(std::integral_constant<int, kActRelu>{});
   }
 }
 
