@@ -825,7 +825,7 @@ q8ta_status q8ta_verify_drafts(const void* logits, int64_t batch_stride, int64_t
  * bytes move in 16-byte chunks).  lens outside [0, table_pages * page_size] are
  * taken into it.  Entries of 0 (requests, n, batch) are no-ops.  Requirements: requests, batch and
  * n <= 2^24 (copy and compact: n < 2^31), pages < 2^31, table_pages * page_size < 2^31,
- * requests * table_pages and batch * n <= 2^40, kv_heads <= 65535, dim <= 65536, the
+ * requests * table_pages and batch * n <= 2^40, kv_heads <= 32767, dim <= 65536, the
  * cache's elements <= 2^40.  Workspace of take and fork: 16 bytes an entry and 8
  * for each 4096 pages.
  */

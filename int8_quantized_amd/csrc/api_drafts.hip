@@ -24,8 +24,8 @@ q8ta_status table_ok(const char* op, const PagesArgs& a) {
 // The checks of the calls that move rows.
 q8ta_status cache_ok(const char* op, const CacheArgs& a, int64_t kv_heads, int64_t dim) {
   if (a.pages < 1 || a.pages >= ((int64_t)1 << 31) || a.page < 1 || a.page >= ((int64_t)1 << 31) ||
-      kv_heads < 1 || kv_heads > 65535 || dim < 1 || dim > 65536 || !fits({a.pages, a.page, kv_heads, dim, 2}))
-    return report(Q8TA_ERR_SHAPE, "%s: pages, page_size, kv_heads (<= 65535) and dim (<= 65536) must be >= 1 "
+      kv_heads < 1 || kv_heads > 32767 || dim < 1 || dim > 65536 || !fits({a.pages, a.page, kv_heads, dim, 2}))
+    return report(Q8TA_ERR_SHAPE, "%s: pages, page_size, kv_heads (<= 32767) and dim (<= 65536) must be >= 1 "
                   "and the cache at most 2^40 elements (got %lld, %lld, %lld, %lld)", op, (long long)a.pages,
                   (long long)a.page, (long long)kv_heads, (long long)dim);
   return Q8TA_OK;
