@@ -13,13 +13,18 @@
 //     4096: largest value, its first index, sum of weights relative to it.  All nodes,
 //     since which are reached is not known before.
 //  2. k_verify_walk: a workgroup for each chunk of the last node's row: the walk
-//     first, each for itself (a chain of short loads, one node after the
-//     other; a lane holds a node), then the chunk's sum of what is left.  Where
-//     nothing was rejected the first launch has that sum already.
+//     first, each for itself (a lane holds a node; all that it may need is loaded
+//     at once), then the chunk's sum of what is left.
 //  3. k_verify_pick: a workgroup a request finds the chunk, then the token in it.
 //
-// Weights are 64-bit (2^x by a polynomial, 4e-14 of the weight) and added in one
-// fixed order, so that a result does not depend on what else is in the batch.
+// What the next token is drawn from, and each drafted token's own weight, are 64-bit
+// (2^x by a polynomial, 4e-14 of the weight).  The sums that these are divided by, of
+// which every node has one, take the weights below a quarter of their chunk's largest in 32 bits (2^-22 of each,
+// both ways, sixteen of them added in 32), which leaves the sum off by some 1e-8 of itself at most: a random number
+// falls into that once in 1e8 tests (all in 64 bits took 41 us for 384 rows of
+// 131072: the vector instructions are what bounds it).
+// All is added in one fixed order, so that a result does not depend on what else is
+// in the batch.
 #include <cmath>
 
 #include "decode.h"
@@ -33,6 +38,7 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kNT = 256, kPer = 16, kChunk = kNT * kPer;
 constexpr int kWaves = kNT / 64;
+constexpr float kLarge = -2.0f;   // log2 of the weight from which one is formed in 64 bits
 
 struct Stat {
   float top;     // largest logit of the chunk, -inf where there is none
@@ -102,16 +108,40 @@ __device__ __forceinline__ float heat_of(const VerifyArgs& v, int b, bool draft)
   return draft && v.draft_temperature ? v.draft_temperature[b] : v.temperature[b];
 }
 
-template <class V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-  for (int m = 32; m > 0; m /= 2) v += __shfl_xor(v, m);
-  return v;
+// Over the 64 lanes of a wave (all active), the same in every lane.
+template <int CTRL>
+__device__ __forceinline__ float move(float v) {
+  return __builtin_bit_cast(float, row_move<CTRL>(__builtin_bit_cast(int32_t, v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double move(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)row_move<CTRL>((int32_t)(uint32_t)b);
+  const uint32_t hi = (uint32_t)row_move<CTRL>((int32_t)(uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, v), lane));
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int32_t)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int32_t)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <class V, class F>
+__device__ __forceinline__ V over_wave(V v, F&& f) {
+  v = f(v, move<kDppMirror16>(v));
+  v = f(v, move<kDppMirror8>(v));
+  v = f(v, move<kDppRev4>(v));
+  v = f(v, move<kDppSwap1>(v));
+  return f(f(lane_of(v, 0), lane_of(v, 16)), f(lane_of(v, 32), lane_of(v, 48)));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  return over_wave(v, [](double a, double b) { return a + b; });
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m /= 2) v = __builtin_fmaxf(v, __shfl_xor(v, m));
-  return v;
+  return over_wave(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
 }
 __device__ __forceinline__ int wave_min(int v) {
 #pragma unroll
@@ -156,10 +186,29 @@ __global__ __launch_bounds__(kNT) void k_verify_stats(Plan p) {
     for (int i = kPer - 1; i >= 0; --i) first = x[i] == top ? i0 + i : first;
     first = wave_min(first);
     if (tid % 64 == 0) firsts[wave] = first;
+  } else if (top == INFINITY) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += x[i] == top ? 1.0 : 0.0;
   } else if (top > -INFINITY) {
     const Heat h = make_heat(top, heat);
+    const Near near = make_near(h);
+    float four[4] = {};
+    bool large = false;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += weight(h, x[i]);
+    for (int i = 0; i < kPer; ++i) {
+      const float y = near_log2(near, x[i]);
+      const bool is = y > kLarge;
+      large |= is;
+      four[i % 4] += is ? 0.0f : __builtin_amdgcn_exp2f(y);
+    }
+    sum = ((double)four[0] + (double)four[1]) + ((double)four[2] + (double)four[3]);
+    if (__any(large)) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const bool is = near_log2(near, x[i]) > kLarge;
+        if (__any(is)) sum += is ? weight(h, x[i]) : 0.0;
+      }
+    }
   }
   sum = wave_sum(sum);
   if (tid % 64 == 0) sums[wave] = sum;
@@ -174,38 +223,55 @@ __global__ __launch_bounds__(kNT) void k_verify_stats(Plan p) {
   }
 }
 
-// A row's largest logit, its first index and its sum of weights, from its
-// chunks (every lane of a wave active).
+// A row's largest logit, its first index and its sum of weights.
 struct Row {
   float top;
   int at;
   double z;
 };
-__device__ __forceinline__ Row row_stat(const Plan& p, const Stat* st, int lane, float heat) {
+// Two disjoint parts of a row as one.
+__device__ __forceinline__ Row join(const Row& a, const Row& b, float heat) {
+  const bool a_top = a.top >= b.top;
+  Row r{a_top ? a.top : b.top, 0, 0.0};
+  r.at = a.top == b.top ? (a.at < b.at ? a.at : b.at) : (a_top ? a.at : b.at);
+  const double less = weight(make_heat(r.top, heat), a_top ? b.top : a.top);   // 1 where the tops are equal
+  r.z = a_top ? a.z + b.z * less : a.z * less + b.z;
+  return r;
+}
+// Every kWaves-th chunk of a row, from `first` on; kAhead of them loaded at once.
+__device__ __forceinline__ Row part_of(const Plan& p, const Stat* st, int first, float heat) {
+  constexpr int kAhead = 8;
   Row r{-INFINITY, INT32_MAX, 0.0};
-  for (int c = lane; c < p.chunks; c += 64) r.top = __builtin_fmaxf(r.top, st[c].top);
-  r.top = wave_max(r.top);
-  const Heat h = make_heat(r.top, heat);
-  for (int c = lane; c < p.chunks; c += 64) {
-    const Stat s = st[c];
-    if (s.top == r.top && s.at < r.at) r.at = s.at;
-    if (s.top > -INFINITY) r.z += s.sum * weight(h, s.top);
+  for (int c = first; c < p.chunks; c += kWaves * kAhead) {
+    Stat s[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) s[i] = st[c + kWaves * i < p.chunks ? c + kWaves * i : first];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (c + kWaves * i < p.chunks && s[i].top > -INFINITY) r = join(r, Row{s[i].top, s[i].at, s[i].sum}, heat);
   }
-  r.at = wave_min(r.at);
-  r.z = wave_sum(r.z);
   return r;
 }
 
+// Lane i of each wave holds token i; every value that the walk needs is
+// loaded beforehand, for all tokens at once.
 template <class T>
-__device__ __forceinline__ void walk(const Plan& p, int lb, bool writes, Last& out) {
+__device__ __forceinline__ void walk(const Plan& p, int lb, bool writes, Row (&rows)[2][kWaves][64], Last& out) {
   const VerifyArgs& v = p.v;
-  const int lane = threadIdx.x & 63, b = p.b0 + lb;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, b = p.b0 + lb;
   const int count = count_of(v, b);
   const float heat = heat_of(v, b, false), dheat = heat_of(v, b, true);
-  const bool greedy = !(heat > 0.0f);
+  const bool greedy = !(heat > 0.0f), dgreedy = !(dheat > 0.0f);
   const int64_t at = (int64_t)b * v.tokens + lane;
   const bool in = lane < count;
+  const bool drawn = v.draft && !greedy && in && lane > 0;   // from the drafter's row of the token before
+  const Stat* stats = p.stats + (int64_t)lb * p.rows * p.chunks;
+  if (in && wave < p.chunks) rows[0][wave][lane] = part_of(p, stats + (int64_t)lane * p.chunks, wave, greedy ? 1.0f : heat);
+  if (drawn && wave < p.chunks)
+    rows[1][wave][lane] =
+        part_of(p, stats + (int64_t)(v.tokens + lane - 1) * p.chunks, wave, dgreedy ? 1.0f : dheat);
   const int id = in ? v.ids[at] : -1;
+  const bool is_id = id >= 0 && id < v.vocab;
   float u = in ? v.u[at] : 0.0f;
   if (u < 0.0f) u = 0.0f;
   int parent = lane - 1;   // (-1: none)
@@ -213,82 +279,87 @@ __device__ __forceinline__ void walk(const Plan& p, int lb, bool writes, Last& o
     const uint64_t above = (uint64_t)v.mask[at] & ((1ull << lane) - 1);
     parent = above ? 63 - __builtin_clzll(above) : -1;
   }
-  const Stat* stats = p.stats + (int64_t)lb * p.rows * p.chunks;
-  int node = 0, kept = 0, path = -1;
-  int mode = kWhole, rejected = 0;
-  Row row{-INFINITY, 0, 0.0}, drow{-INFINITY, 0, 0.0};
+  const bool child = in && parent >= 0 && is_id;
+  const float x = child ? no_nan(to_float(row_of<T>(v, b, parent)[id])) : -INFINITY;
+  const float y = drawn && is_id ? no_nan(to_float(row_of<T>(v, b, v.tokens + lane - 1)[id])) : -INFINITY;
+  __syncthreads();
+  if (wave > 0) return;
+  Row row{-INFINITY, INT32_MAX, 0.0}, drow = row;
+  if (in) {
+    for (int w = 0; w < kWaves && w < p.chunks; ++w) row = join(row, rows[0][w][lane], greedy ? 1.0f : heat);
+  }
+  if (drawn) {
+    for (int w = 0; w < kWaves && w < p.chunks; ++w) drow = join(drow, rows[1][w][lane], dgreedy ? 1.0f : dheat);
+  }
+  const bool some = row.top > -INFINITY;
+  // this token's weight among its parent's, and its share of the drafter's
+  const float ptop = __shfl(row.top, parent & 63);
+  const double pz = __shfl(row.z, parent & 63);
+  const int pat = __shfl(row.at, parent & 63);
+  const double mine = greedy ? 0.0 : weight(make_heat(ptop, heat), x);
+  double q = 0.0;
+  if (drawn && drow.top > -INFINITY)
+    q = dgreedy ? (id == drow.at ? 1.0 : 0.0) : weight(make_heat(drow.top, dheat), y) / drow.z;
+  const uint64_t hits = __ballot(child && id == pat);                        // greedy
+  const uint64_t kept_by_q = __ballot(child && (double)u * q < mine / pz);   // chains
+  const uint64_t filled = __ballot(in && some);
+  int node = 0, kept = 0, path = -1, mode = kWhole, rejected = 0;
   while (count > 0) {
     if (lane == kept) path = node;
     ++kept;
     mode = kWhole;
     rejected = 0;
-    row = row_stat(p, stats + (int64_t)node * p.chunks, lane, greedy ? 1.0f : heat);
-    uint64_t children = __ballot(in && lane > 0 && parent == node && lane > node);
-    if (!(row.top > -INFINITY)) break;
+    if (!((filled >> node) & 1)) break;
+    uint64_t children = __ballot(in && parent == node && lane > node);
     int next = -1;
-    if (greedy) {
-      const uint64_t hit = __ballot(id == row.at) & children;
-      if (hit) next = __builtin_ctzll(hit);
-    } else if (children) {
-      const bool mine = (children >> lane) & 1 && id >= 0 && id < v.vocab;
-      const float x = mine ? no_nan(to_float(row_of<T>(v, b, node)[id])) : -INFINITY;
-      const double w = weight(make_heat(row.top, heat), x);
-      if (v.draft) {
-        // a chain: one child
-        double q = 0.0;
-        if (dheat > 0.0f) {
-          const float y = mine ? no_nan(to_float(row_of<T>(v, b, v.tokens + node)[id])) : -INFINITY;
-          drow = row_stat(p, stats + (int64_t)(v.tokens + node) * p.chunks, lane, dheat);
-          if (drow.top > -INFINITY) q = weight(make_heat(drow.top, dheat), y) / drow.z;
-        } else {   // a greedy drafter: all on its largest
-          drow = row_stat(p, stats + (int64_t)(v.tokens + node) * p.chunks, lane, 1.0f);
-          drow.z = 1.0;
-          if (!(drow.top > -INFINITY)) drow.at = -1;
-          q = id == drow.at ? 1.0 : 0.0;
-          out.ids[0] = drow.at;
+    if (greedy || v.draft) {
+      const uint64_t good = children & (greedy ? hits : kept_by_q);
+      if (good) next = __builtin_ctzll(good);
+      else if (!greedy && children) mode = kResidual;
+    } else {
+      double left = __shfl(row.z, node);
+      while (children) {
+        const int c = __builtin_ctzll(children);
+        children &= children - 1;
+        const double wc = __shfl(mine, c);
+        const int idc = __builtin_amdgcn_readlane(id, c);
+        bool again = false;   // rejected before: nothing left
+        for (int k = 0; k < rejected; ++k) again |= out.ids[k] == idc;
+        if (again || !(wc > 0.0)) continue;
+        if ((double)__shfl(u, c) * left < wc) {
+          next = c;
+          break;
         }
-        const uint64_t good = __ballot((double)u * q < w / row.z) & children;
-        if (good) next = __builtin_ctzll(good);
-        else mode = kResidual;
-      } else {
-        double left = row.z;
-        while (children) {
-          const int c = __builtin_ctzll(children);
-          children &= children - 1;
-          const double wc = __shfl(w, c);
-          const int idc = __builtin_amdgcn_readlane(id, c);
-          bool again = false;   // rejected before: nothing left
-          for (int k = 0; k < rejected; ++k) again |= out.ids[k] == idc;
-          if (!again && (double)__shfl(u, c) * left < wc) {
-            next = c;
-            break;
-          }
-          if (!again && wc > 0.0) {
-            left -= wc;
-            out.ids[rejected++] = idc;   // (every lane the same)
-            mode = kLess;
-          }
-        }
+        left -= wc;
+        out.ids[rejected++] = idc;   // (every lane the same)
+        mode = kLess;
       }
     }
     if (next < 0) break;
     node = next;
   }
-  const bool none = !(row.top > -INFINITY);   // nothing to take a token from
+  const float top = __shfl(row.top, node);
+  const int first = __shfl(row.at, node);
+  const bool none = count <= 0 || !(top > -INFINITY);   // nothing to take a token from
+  const int drafted = node + 1 < 64 ? node + 1 : 63;    // the drafter's row of this node is its child's
+  const int datum = __shfl(drow.top > -INFINITY ? drow.at : -1, drafted);
+  if (mode == kResidual) out.ids[0] = datum;
+  const double z = __shfl(row.z, node), draft_z = __shfl(drow.z, drafted);
+  const float draft_top = __shfl(drow.top, drafted);
   if (lane == 0) {
     out.node = node;
     out.mode = none || greedy ? kDone : mode;
     out.rejected = rejected;
-    out.top = row.top;
-    out.z = row.z;
-    out.draft_top = drow.top;
-    out.draft_z = drow.z;
+    out.top = top;
+    out.z = z;
+    out.draft_top = draft_top;
+    out.draft_z = draft_z;
   }
   if (writes) {
     if (lane < v.tokens) v.path[at] = path;
     if (lane == 0) {
       v.accepted[b] = kept;
-      v.next[b] = none || !greedy ? -1 : row.at;
+      v.next[b] = none || !greedy ? -1 : first;
     }
   }
 }
@@ -329,16 +400,17 @@ __device__ __forceinline__ void left16(const VerifyArgs& v, int b, const Last& l
 template <class T, bool VEC>
 __global__ __launch_bounds__(kNT) void k_verify_walk(Plan p) {
   __shared__ Last l;
+  __shared__ Row rows[2][kWaves][64];
   __shared__ double sums[kWaves];
   const int tid = threadIdx.x;
   const int lb = blockIdx.x / p.chunks, chunk = blockIdx.x - lb * p.chunks;
-  if (tid < 64) walk<T>(p, lb, chunk == 0, l);
+  walk<T>(p, lb, chunk == 0, rows, l);
   __syncthreads();
   if (chunk == 0) {   // for the last launch
     constexpr int kWords = sizeof(Last) / 4;
     if (tid < kWords) ((int32_t*)&p.last[lb])[tid] = ((const int32_t*)&l)[tid];
   }
-  if (l.mode == kDone || l.mode == kWhole) return;
+  if (l.mode == kDone) return;
   double r[kPer], sum = 0.0;
   left16<T, VEC>(p.v, p.b0 + lb, l, l.mode, chunk * kChunk + tid * kPer, r);
 #pragma unroll
@@ -385,37 +457,50 @@ __device__ __forceinline__ int find(Find& f, double mine, double before, double 
   return at;
 }
 
+// The running total of what is left in the chunks, each thread's own `each` neighbouring ones in
+// `mine`.
+__device__ __forceinline__ double total_of(const Plan& p, const double* sums, int each, double* sh, double& mine) {
+  const int tid = threadIdx.x;
+  mine = 0.0;
+  for (int c = tid * each; c < tid * each + each && c < p.chunks; ++c) mine += sums[c];
+  const double part = wave_sum(mine);
+  __syncthreads();
+  if (tid % 64 == 0) sh[tid / 64] = part;
+  __syncthreads();
+  return ((sh[0] + sh[1]) + sh[2]) + sh[3];
+}
+
 template <class T, bool VEC>
 __global__ __launch_bounds__(kNT) void k_verify_pick(Plan p) {
   __shared__ Find f;
-  __shared__ double totals[kWaves];
+  __shared__ double sh[kWaves];
   const VerifyArgs& v = p.v;
   const int tid = threadIdx.x, lb = blockIdx.x, b = p.b0 + lb;
   const Last& l = p.last[lb];
-  if (l.mode == kDone) return;
-  int mode = l.mode;
+  double* sums = p.sums + (int64_t)lb * p.chunks;
+  const int each = (p.chunks + kNT - 1) / kNT;
   const float given = v.u[(int64_t)b * v.tokens];
   const double u = given < 0.0f ? 0.0 : (double)given;
-  const Stat* st = p.stats + ((int64_t)lb * p.rows + l.node) * p.chunks;
-  const Heat h = make_heat(l.top, heat_of(v, b, false));
-  auto chunk_sum = [&](int c) {
-    if (c >= p.chunks) return 0.0;
-    if (mode != kWhole) return p.sums[(int64_t)lb * p.chunks + c];
-    return st[c].top > -INFINITY ? st[c].sum * weight(h, st[c].top) : 0.0;
-  };
-  // each thread a run of neighbouring chunks
-  const int each = (p.chunks + kNT - 1) / kNT;
-  double mine, total;
-  while (true) {
-    mine = 0.0;
-    for (int c = tid * each; c < tid * each + each; ++c) mine += chunk_sum(c);
-    total = wave_sum(mine);
+  int mode = l.mode;
+  if (mode == kDone) return;
+  double mine;
+  double total = total_of(p, sums, each, sh, mine);
+  if (!(total > 0.0) && mode != kWhole) {
+    // nothing left, as for a u of 1 (or but by rounding): the row itself
+    mode = kWhole;
+    for (int c = 0; c < p.chunks; ++c) {
+      double r[kPer], part = 0.0;
+      left16<T, VEC>(v, b, l, mode, c * kChunk + tid * kPer, r);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) part += r[i];
+      part = wave_sum(part);
+      __syncthreads();
+      if (tid % 64 == 0) sh[tid / 64] = part;
+      __syncthreads();
+      if (tid == 0) sums[c] = ((sh[0] + sh[1]) + sh[2]) + sh[3];
+    }
     __syncthreads();
-    if (tid % 64 == 0) totals[tid / 64] = total;
-    __syncthreads();
-    total = ((totals[0] + totals[1]) + totals[2]) + totals[3];
-    if (total > 0.0 || mode == kWhole) break;
-    mode = kWhole;   // nothing left but by rounding: the row itself
+    total = total_of(p, sums, each, sh, mine);
   }
   const double goal = u * total;
   double below;
@@ -424,8 +509,8 @@ __global__ __launch_bounds__(kNT) void k_verify_pick(Plan p) {
   // of the run's chunks the one that passes, else its last with a weight
   int chunk = -1;
   double sum = below, at_chunk = below;
-  for (int c = run * each; c < run * each + each; ++c) {
-    const double s = chunk_sum(c);
+  for (int c = run * each; c < run * each + each && c < p.chunks; ++c) {
+    const double s = sums[c];
     if (s > 0.0) {
       chunk = c;
       at_chunk = sum;

@@ -32,13 +32,36 @@ struct Heat {
   double top, scale;   // largest logit, log2(e) / temperature
 };
 __device__ __forceinline__ Heat make_heat(float top, float temperature) {
-  return Heat{(double)top, 1.4426950408889634 / (double)temperature};
+  // 1 / T to the last bit or two, from the estimate by Newton steps (which have none for infinity)
+  const double t = temperature;
+  double y = __builtin_amdgcn_rcp(t);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = __builtin_fma(__builtin_fma(-t, y, 1.0), y, y);
+  return Heat{(double)top, temperature < INFINITY ? 1.4426950408889634 * y : 0.0};
 }
 // exp((x - top) / T): 1 for the largest itself (an infinite one too), 0 for -inf.
 __device__ __forceinline__ double weight(const Heat& h, float x) {
   const double y = ((double)x - h.top) * h.scale;
   const double w = exp2_of(y);
   return (double)x == h.top ? 1.0 : (x == -INFINITY ? 0.0 : w);
+}
+
+// The same in 32 bits, for a finite top: off by 2^-23 of the weight and by up to 2^-24 of it for
+// each power of two below 1, both ways.
+struct Near {
+  float top, scale, rest;   // the scale in two parts of one sign, so that -inf stays
+};
+__device__ __forceinline__ Near make_near(const Heat& h) {
+  // (kept finite and above 0: 2^100 and 2^-100 are as good as infinity and 0 here)
+  const double s = __builtin_fmin(__builtin_fmax(h.scale, 0x1p-100), 0x1p100);
+  float hi = (float)s;
+  if ((double)hi > s) hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, hi) - 1);
+  return Near{(float)h.top, hi, (float)(s - (double)hi)};
+}
+// log2 of it; the weight is 2 to that.
+__device__ __forceinline__ float near_log2(const Near& h, float x) {
+  const float d = x - h.top;
+  return __builtin_fmaf(d, h.scale, d * h.rest);
 }
 
 }  // namespace q8ta
