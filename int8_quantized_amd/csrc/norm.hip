@@ -80,8 +80,8 @@ __device__ __forceinline__ void store8(T* p, int live, const float (&x)[8]) {
   }
 }
 
-// The larger magnitude; a NaN on either side stays (fmax would drop it).
-__device__ __forceinline__ double top_of(double a, double b) { return a > b || a != a ? a : b; }
+// (of magnitudes; a row that holds a NaN comes with an infinity in its place)
+__device__ __forceinline__ double top_of(double a, double b) { return __builtin_fmax(a, b); }
 __device__ __forceinline__ double plus_of(double a, double b) { return a + b; }
 
 template <int CTRL>
@@ -97,34 +97,45 @@ __device__ __forceinline__ double lane64(double v, int lane) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int32_t)(uint32_t)(b >> 32), lane);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-// v of all threads of the workgroup by `f`, in a fixed order, the same in every
-// thread.  `sh`: kMaxThreads / 64 doubles that no other call uses.
+// v of all lanes of a wave by `f`, the same in each.
 template <class F>
-__device__ __forceinline__ double over_row(double v, double* sh, F&& f) {
+__device__ __forceinline__ double over_wave(double v, F&& f) {
   v = f(v, row_move64<kDppMirror16>(v));
   v = f(v, row_move64<kDppMirror8>(v));
   v = f(v, row_move64<kDppRev4>(v));
   v = f(v, row_move64<kDppSwap1>(v));
-  v = f(f(lane64(v, 0), lane64(v, 16)), f(lane64(v, 32), lane64(v, 48)));
-  const int waves = blockDim.x / 64;
-  if (waves == 1) return v;
+  return f(f(lane64(v, 0), lane64(v, 16)), f(lane64(v, 32), lane64(v, 48)));
+}
+// The waves' values in `sh` by `f`, where 0 is none (every lane of the wave active).
+template <class F>
+__device__ __forceinline__ double over_waves(const double* sh, F&& f) {
+  const int lane = threadIdx.x & 15;
+  double v = lane < (int)blockDim.x / 64 ? sh[lane] : 0.0;
+  v = f(v, row_move64<kDppMirror16>(v));
+  v = f(v, row_move64<kDppMirror8>(v));
+  v = f(v, row_move64<kDppRev4>(v));
+  return f(v, row_move64<kDppSwap1>(v));
+}
+// v of all threads of the workgroup by `f`, in a fixed order.  `sh`: kMaxThreads / 64 doubles that
+// no other call uses.
+template <class F>
+__device__ __forceinline__ double over_row(double v, double* sh, F&& f) {
+  v = over_wave(v, f);
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x / 64] = v;
   __syncthreads();
-  v = sh[0];
-  for (int w = 1; w < waves; ++w) v = f(v, sh[w]);
-  return v;
+  return over_waves(sh, f);
 }
 
-// rint(z * 127 / top), inv = 127 / top: the quotient's rounding differs from
-// the product's by 2^-52 of it, which matters next to a tie.
-__device__ __forceinline__ int code_of(double z, double top, double inv) {
-  double q = z * inv;
-  double r = __builtin_rint(q);
-  if (__builtin_fabs(q - r) > 0.499999) {
-    q = z * 127.0 / top;
-    r = __builtin_rint(q);
-  }
-  return (int)r;
+// rint(p * 127 / top) in the low byte.  With inv = 127 / top the product's rounding differs from
+// the quotient's by 2^-52 of it, which matters next to a tie (near).
+constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: the sum's low word is the nearest whole number
+__device__ __forceinline__ uint32_t fast_code(double p, double inv, bool& near) {
+  const double q = p * inv, t = q + kMagic;
+  near |= __builtin_fabs(q - (t - kMagic)) > 0.499999;
+  return (uint32_t)__builtin_bit_cast(uint64_t, t);
+}
+__device__ __forceinline__ uint32_t exact_code(double p, double top) {
+  return (uint32_t)__builtin_bit_cast(uint64_t, p * 127.0 / top + kMagic);
 }
 
 // 1 / x and 1 / sqrt(x) to the last bit or two, from the estimates by Newton steps.
@@ -156,7 +167,7 @@ template <class T>
 __device__ __forceinline__ float sum_of(double b, bool has_gate, float gate, bool has_res, float res,
                                         double res_scale) {
   if (has_gate) b = b * (double)gate;
-  if (has_res) b = b + (double)res * res_scale;
+  if (has_res) b = __builtin_fma((double)res, res_scale, b);
   return to_float(from_float<T>((float)b));
 }
 
@@ -198,47 +209,77 @@ __global__ __launch_bounds__(kMaxThreads, C == 1 ? 8 : 4) void k_norm(NormArgs a
   double s = 0.0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
+    double y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      double b = element(xr[c], i);
-      if (a.post_weight) b = b * post * (double)element(pw[c], i);
-      h[c][i] = sum_of<T>(b, a.gate != nullptr, element(gr[c], i), a.residual != nullptr, element(rr[c], i),
-                          a.residual_scale);
+    for (int i = 0; i < 8; ++i) y[i] = element(xr[c], i);
+    if (a.post_weight) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * post * (double)element(pw[c], i);
     }
+    if (a.gate) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * (double)element(gr[c], i);
+    }
+    if (a.residual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __builtin_fma((double)element(rr[c], i), a.residual_scale, y[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[c][i] = to_float(from_float<T>((float)y[i]));
     const int e = 8 * (tid + c * nt);
     if (e >= n) continue;
+    if (a.weight) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = __builtin_fma((double)h[c][i], (double)h[c][i], s);
+      for (int i = 0; i < 8; ++i) s = __builtin_fma((double)h[c][i], (double)h[c][i], s);
+    }
     if (a.sum) store8<VEC>((T*)a.sum + t * a.n + e, n - e, h[c]);
   }
-  double rstd = 1.0;
-  if (a.weight) rstd = reciprocal_root(__builtin_fma(over_row(s, sh[1], plus_of), inv_n, a.eps));
-  auto z_of = [&](int c, int i) {
-    const double z = h[c][i];
-    return a.weight ? z * rstd * (double)element(w[c], i) : z;
-  };
-  // (a maximum would drop a NaN: z * 0 keeps it, and infinities)
-  double top = 0.0, odd = 0.0;
+  // the codes need p = h * weight and the largest of them alone: rms(h) is a factor of both
+  double p[C][8], top = 0.0, odd = 0.0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[c][i] = h[c][i];
+    if (a.weight) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[c][i] = p[c][i] * (double)element(w[c], i);
+    }
     if (8 * (tid + c * nt) >= n) continue;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const double z = z_of(c, i);
-      top = __builtin_fmax(top, __builtin_fabs(z));
-      odd = __builtin_fma(z, 0.0, odd);
+      top = __builtin_fmax(top, __builtin_fabs(p[c][i]));
+      odd = __builtin_fma(p[c][i], 0.0, odd);   // (a maximum would drop a NaN)
     }
   }
-  top = over_row(odd == 0.0 ? top : __builtin_nan(""), sh[2], top_of);
+  top = over_wave(odd == 0.0 ? top : (double)__builtin_inff(), top_of);
+  s = over_wave(s, plus_of);
+  if ((tid & 63) == 0) {
+    sh[1][tid / 64] = s;
+    sh[2][tid / 64] = top;
+  }
+  __syncthreads();
+  top = over_waves(sh[2], top_of);
   const double inv = inv_of(top);
-  if (tid == 0) a.scales[t] = scale_of(top);
+  if (tid < 64) {   // (a whole wave: its lanes hold the parts)
+    const double rstd = a.weight ? reciprocal_root(__builtin_fma(over_waves(sh[1], plus_of), inv_n, a.eps)) : 1.0;
+    if (tid == 0) a.scales[t] = scale_of(top * rstd);
+  }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int e = 8 * (tid + c * nt);
     if (e >= n) continue;
-    int q[8];
+    uint32_t q[8];
+    bool near = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = inv > 0.0 ? code_of(z_of(c, i), top, inv) : 0;
+    for (int i = 0; i < 8; ++i) q[i] = fast_code(p[c][i], inv, near);
+    if (near) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = exact_code(p[c][i], top);
+    }
+    if (!(inv > 0.0)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = 0;
+    }
     int8_t* dst = a.codes + t * a.n + e;
     if constexpr (VEC) {
       *reinterpret_cast<v2u*>(dst) = v2u{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
@@ -267,9 +308,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a, double in
     return sum_of<T>(b, a.gate != nullptr, a.gate ? to_float(gate[e]) : 0.0f, a.residual != nullptr,
                      a.residual ? to_float(res[e]) : 0.0f, a.residual_scale);
   };
-  auto z_of = [&](int64_t e, float h) {
-    return a.weight ? (double)h * rstd * (double)a.weight[e] : (double)h;
-  };
+  auto p_of = [&](int64_t e, float h) { return a.weight ? (double)h * (double)a.weight[e] : (double)h; };
   if (a.post_weight) {
     double s = 0.0;
     for (int64_t e = tid; e < a.n; e += kMaxThreads) {
@@ -286,14 +325,19 @@ __global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a, double in
     }
     rstd = reciprocal_root(__builtin_fma(over_row(s, sh[1], plus_of), inv_n, a.eps));
   }
-  double top = 0.0;
-  for (int64_t e = tid; e < a.n; e += kMaxThreads) top = top_of(__builtin_fabs(z_of(e, h_of(e))), top);
+  double top = 0.0, odd = 0.0;
+  for (int64_t e = tid; e < a.n; e += kMaxThreads) {
+    const double p = p_of(e, h_of(e));
+    top = top_of(__builtin_fabs(p), top);
+    odd = __builtin_fma(p, 0.0, odd);
+  }
+  if (!(odd == 0.0)) top = (double)__builtin_inff();
   top = over_row(top, sh[2], top_of);
   const double inv = inv_of(top);
-  if (tid == 0) a.scales[t] = scale_of(top);
+  if (tid == 0) a.scales[t] = scale_of(top * rstd);
   for (int64_t e = tid; e < a.n; e += kMaxThreads) {
     const float h = h_of(e);
-    const int q = inv > 0.0 ? code_of(z_of(e, h), top, inv) : 0;
+    const uint32_t q = inv > 0.0 ? exact_code(p_of(e, h), top) : 0;
     if (a.sum) ((T*)a.sum)[t * a.n + e] = from_float<T>(h);
     a.codes[t * a.n + e] = (int8_t)q;
   }
@@ -314,7 +358,9 @@ hipError_t launch_type(const NormArgs& a, hipStream_t s) {
   const bool vec = a.n % 8 == 0 && strides % 8 == 0 && ptrs % 16 == 0 && (uintptr_t)a.codes % 8 == 0;
   const int64_t groups = (a.n + 7) / 8;
   auto threads = [&](int c) { return (int)((groups + 64 * c - 1) / (64 * c)) * 64; };
-  if (groups <= 1024) launch_regs<T, 1>(a, vec, threads(1), s);
+  // 16 elements a thread where there are many rows (8191 x 5120: 93 us against 99 with 8), 8 where
+  // a row is a chain of latencies
+  if (groups <= 1024 && a.tokens < 512) launch_regs<T, 1>(a, vec, threads(1), s);
   else if (groups <= 2048) launch_regs<T, 2>(a, vec, threads(2), s);
   else hipLaunchKernelGGL((k_norm_long<T>), dim3((unsigned)a.tokens), dim3(kMaxThreads), 0, s, a,
                           1.0 / (double)a.n);
