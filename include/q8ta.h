@@ -769,8 +769,8 @@ q8ta_status q8ta_gated_linear(const int8_t* x, int64_t M, int64_t K, const float
  * Sums and weights are 64-bit and added in an order that depends on vocab alone.
  * A NaN logit counts as -inf; +inf logits share the weight alone; where all
  * logits are -inf the walk ends, with next -1.  An id outside [0, vocab) has p and q 0.
- * u: in [0, 1); below 0 as 0; a NaN or one of 1 and beyond keeps no drawn child with p <=
- * q and takes the last index with anything left.  A request with counts[b] <= 0 gets
+ * u: in [0, 1); below 0 as 0; one of 1 and beyond keeps no drawn child with p <= q and
+ * takes the last index with anything left, a NaN keeps none and takes that too. A request with counts[b] <= 0 gets
  * accepted 0 and next -1.
  * logits [batch, tokens, vocab], draft_logits [batch, tokens - 1, vocab], both of
  * `dtype`, inner stride 1, any other strides; ids int32 [batch, tokens]; counts int32

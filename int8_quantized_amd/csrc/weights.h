@@ -56,7 +56,8 @@ __device__ __forceinline__ Near make_near(const Heat& h) {
   const double s = __builtin_fmin(__builtin_fmax(h.scale, 0x1p-100), 0x1p100);
   float hi = (float)s;
   if ((double)hi > s) hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, hi) - 1);
-  return Near{(float)h.top, hi, (float)(s - (double)hi)};
+  // (a rest of 0 would make a NaN of -inf)
+  return Near{(float)h.top, hi, __builtin_fmaxf((float)(s - (double)hi), 0x1p-126f)};
 }
 // log2 of it; the weight is 2 to that.
 __device__ __forceinline__ float near_log2(const Near& h, float x) {
