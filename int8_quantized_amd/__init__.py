@@ -781,9 +781,8 @@ def q8ta_norm_quantize(x, residual, post_weight, gate, residual_scale, weight, e
             raise ValueError(f"gate must be {dtype} [{T} or 1, {N}] (got {gate.dtype} {tuple(gs)})")
         if gs[0] == 1:
             gt = (0, 1)
-    for name, t in (("post_weight", post_weight), ("weight", weight)):
-        if t is not None and t.shape != (N,):
-            raise ValueError(f"{name} must be [{N}] (got {tuple(t.shape)})")
+    if (post_weight is not None and post_weight.shape != (N,)) or (weight is not None and weight.shape != (N,)):
+        raise ValueError(f"post_weight and weight must be [{N}]")
     if codes.shape != xs or scales.shape != (T,) or (residual_out is not None and residual_out.shape != xs):
         raise ValueError(f"codes and residual_out must be {tuple(xs)} and scales [{T}]")
     f32 = torch.float32
@@ -846,10 +845,10 @@ def q8ta_gated_linear(x, x_scales, gate_weight, gate_scales, gate_bias, up_weigh
     (M, K), N = xs, wsh[0]
     if x_scales.shape != (M,):
         raise ValueError(f"x_scales must be [{M}] (got {tuple(x_scales.shape)})")
-    for name, t in (("gate_scales", gate_scales), ("gate_bias", gate_bias), ("up_scales", up_scales),
-                    ("up_bias", up_bias)):
-        if t is not None and t.shape != (N,):
-            raise ValueError(f"{name} must be [{N}] (got {tuple(t.shape)})")
+    if (gate_scales.shape != (N,) or up_scales.shape != (N,) or
+            (gate_bias is not None and gate_bias.shape != (N,)) or
+            (up_bias is not None and up_bias.shape != (N,))):
+        raise ValueError(f"gate_scales, gate_bias, up_scales and up_bias must be [{N}]")
     f32, i8 = torch.float32, torch.int8
     _check(lib().q8ta_gated_linear(
         _ptr(x, i8, "x"), M, K, _ptr(x_scales, f32, "x_scales"), _ptr(gate_weight, i8, "gate_weight"),
@@ -880,12 +879,13 @@ def q8ta_verify_drafts(logits, draft_logits, ids, counts, mask, temperature, dra
             raise ValueError(f"draft_logits must be {logits.dtype} [{B}, {T - 1}, {V}] (got "
                              f"{draft_logits.dtype} {tuple(ds)})")
         dp = dp or lp   # (no rows of a single token's chain: a pointer that is not read)
-    for name, t, shape in (("ids", ids, (B, T)), ("u", u, (B, T)), ("path", path, (B, T)),
-                           ("mask", mask, (B, T)), ("counts", counts, (B,)),
-                           ("temperature", temperature, (B,)), ("accepted", accepted, (B,)),
-                           ("draft_temperature", draft_temperature, (B,)), ("next_ids", next_ids, (B,))):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)} (got {tuple(t.shape)})")
+    each, one = (B, T), (B,)
+    if (ids.shape != each or u.shape != each or path.shape != each or temperature.shape != one or
+            accepted.shape != one or next_ids.shape != one or (counts is not None and counts.shape != one) or
+            (mask is not None and mask.shape != each) or
+            (draft_temperature is not None and draft_temperature.shape != one)):
+        raise ValueError(f"ids, mask, u and path must be {list(each)}, counts, both temperatures, accepted and "
+                         f"next_ids {list(one)}")
     f32, i32 = torch.float32, torch.int32
     _check(lib().q8ta_verify_drafts(
         lp, lt[0], lt[1], dp, dt[0], dt[1], _code(logits, "logits"), B, T, V, _ptr(ids, i32, "ids"),

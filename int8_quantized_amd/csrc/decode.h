@@ -212,9 +212,10 @@ struct ScaledArgs {
   int64_t n0 = 0;             // first channel of a launch of the row kernel
 };
 hipError_t launch_scaled(ScaledArgs a, hipStream_t s);
-// K a multiple of 16 up to 2^23 and 16-byte aligned x and w; mats 1, mats 2.
-hipError_t launch_linear_tiles(const ScaledArgs& a, hipStream_t s);
-hipError_t launch_gated_tiles(const ScaledArgs& a, hipStream_t s);
+// The GEMM for K a multiple of 16 up to 2^23 and 16-byte aligned x and w, by the type of y.
+hipError_t launch_tiles_f32(const ScaledArgs& a, hipStream_t s);
+hipError_t launch_tiles_f16(const ScaledArgs& a, hipStream_t s);
+hipError_t launch_tiles_bf16(const ScaledArgs& a, hipStream_t s);
 
 struct VerifyArgs {
   const void* logits;         // [batch, tokens, vocab], unit inner stride

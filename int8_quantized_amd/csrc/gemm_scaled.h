@@ -26,7 +26,7 @@
 #include "scaled_epilogue.h"
 
 namespace q8ta {
-namespace {   // (each of the two sources that include this has kernels of its own)
+namespace {   // (each source that includes this has kernels of its own)
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
@@ -484,11 +484,9 @@ hipError_t launch_plan(const ScaledArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MATS>
-hipError_t launch_type(const ScaledArgs& a, hipStream_t s) {
-  if (a.y_type == Q8TA_F32) return launch_plan<MATS, float>(a, s);
-  if (a.y_type == Q8TA_F16) return launch_plan<MATS, Half>(a, s);
-  return launch_plan<MATS, Bfloat>(a, s);
+template <class YT>
+hipError_t launch_mats(const ScaledArgs& a, hipStream_t s) {
+  return a.mats == 2 ? launch_plan<2, YT>(a, s) : launch_plan<1, YT>(a, s);
 }
 
 }  // namespace

@@ -186,10 +186,10 @@ hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
     a.K = kp;
   }
   if (e == hipSuccess) {
-    if (!by_rows(a)) e = a.mats == 2 ? launch_gated_tiles(a, s) : launch_linear_tiles(a, s);
-    else if (a.y_type == Q8TA_F32) e = launch_rows<float>(a, s);
-    else if (a.y_type == Q8TA_F16) e = launch_rows<Half>(a, s);
-    else e = launch_rows<Bfloat>(a, s);
+    const bool rows = by_rows(a);
+    if (a.y_type == Q8TA_F32) e = rows ? launch_rows<float>(a, s) : launch_tiles_f32(a, s);
+    else if (a.y_type == Q8TA_F16) e = rows ? launch_rows<Half>(a, s) : launch_tiles_f16(a, s);
+    else e = rows ? launch_rows<Bfloat>(a, s) : launch_tiles_bf16(a, s);
   }
   if (!pad) return e;
   const hipError_t f = workspace_release(ws, s);
