@@ -36,8 +36,13 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-constexpr int kNT = 256, kPer = 16, kChunk = kNT * kPer;
-constexpr int kWaves = kNT / 64;
+constexpr int kChunk = 4096;
+// of a chunk, in the statistics: 16 a thread, for the loads; in the sums of what is left 8,
+// for the time that 64-bit weights take (the last two launches: a chain of 5 with drafter's
+// rows of 32000 16.8 us, 16 a thread 19.3, 4 a thread 18.5; 16 trees of 24 16.7, 17.2, 23)
+constexpr int kPer = 16, kNT = kChunk / kPer, kWaves = kNT / 64;
+constexpr int kFew = 8, kMany = kChunk / kFew, kManyWaves = kMany / 64;
+constexpr int kParts = 4;   // waves that share a node's chunks in the walk
 constexpr float kLarge = -2.0f;   // log2 of the weight from which one is formed in 64 bits
 
 struct Stat {
@@ -70,33 +75,35 @@ __device__ __forceinline__ const T* row_of(const VerifyArgs& v, int b, int row) 
 }
 __device__ __forceinline__ float no_nan(float x) { return x != x ? -INFINITY : x; }
 
-// This thread's 16 neighbouring logits of a chunk, -inf past the vocabulary.
-template <bool VEC>
-__device__ __forceinline__ void load16(const float* row, int i0, int vocab, float (&x)[kPer]) {
-  if (VEC && i0 + kPer <= vocab) {
+// This thread's P neighbouring logits of a chunk, -inf past the vocabulary.
+template <bool VEC, int P>
+__device__ __forceinline__ void load(const float* row, int i0, int vocab, float (&x)[P]) {
+  if (VEC && i0 + P <= vocab) {
 #pragma unroll
-    for (int j = 0; j < kPer / 4; ++j) {
+    for (int j = 0; j < P / 4; ++j) {
       const v4f v = *reinterpret_cast<const v4f*>(row + i0 + 4 * j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[4 * j + i] = no_nan(v[i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = i0 + i < vocab ? no_nan(row[i0 + i]) : -INFINITY;
+    for (int i = 0; i < P; ++i) x[i] = i0 + i < vocab ? no_nan(row[i0 + i]) : -INFINITY;
   }
 }
-template <bool VEC, class T>
-__device__ __forceinline__ void load16(const T* row, int i0, int vocab, float (&x)[kPer]) {
-  if (VEC && i0 + kPer <= vocab) {
+template <bool VEC, int P, class T>
+__device__ __forceinline__ void load(const T* row, int i0, int vocab, float (&x)[P]) {
+  typedef uint32_t V __attribute__((ext_vector_type(P < 8 ? P / 2 : 4)));
+  constexpr int E = P < 8 ? P : 8;
+  if (VEC && i0 + P <= vocab) {
 #pragma unroll
-    for (int j = 0; j < kPer / 8; ++j) {
-      const v4u v = *reinterpret_cast<const v4u*>(row + i0 + 8 * j);
+    for (int j = 0; j < P / E; ++j) {
+      const V v = *reinterpret_cast<const V*>(row + i0 + E * j);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[8 * j + i] = no_nan(to_float(T{(uint16_t)(v[i / 2] >> (16 * (i % 2)))}));
+      for (int i = 0; i < E; ++i) x[E * j + i] = no_nan(to_float(T{(uint16_t)(v[i / 2] >> (16 * (i % 2)))}));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = i0 + i < vocab ? no_nan(to_float(row[i0 + i])) : -INFINITY;
+    for (int i = 0; i < P; ++i) x[i] = i0 + i < vocab ? no_nan(to_float(row[i0 + i])) : -INFINITY;
   }
 }
 
@@ -171,7 +178,7 @@ __global__ __launch_bounds__(kNT) void k_verify_stats(Plan p) {
   if (node + draft >= count_of(v, b) || (greedy && draft)) return;
   const int i0 = chunk * kChunk + tid * kPer;
   float x[kPer];
-  load16<VEC>(row_of<T>(v, b, row), i0, v.vocab, x);
+  load<VEC, kPer>(row_of<T>(v, b, row), i0, v.vocab, x);
   float top = x[0];
 #pragma unroll
   for (int i = 1; i < kPer; ++i) top = __builtin_fmaxf(top, x[i]);
@@ -229,26 +236,35 @@ struct Row {
   int at;
   double z;
 };
-// Two disjoint parts of a row as one.
-__device__ __forceinline__ Row join(const Row& a, const Row& b, float heat) {
-  const bool a_top = a.top >= b.top;
-  Row r{a_top ? a.top : b.top, 0, 0.0};
-  r.at = a.top == b.top ? (a.at < b.at ? a.at : b.at) : (a_top ? a.at : b.at);
-  const double less = weight(make_heat(r.top, heat), a_top ? b.top : a.top);   // 1 where the tops are equal
-  r.z = a_top ? a.z + b.z * less : a.z * less + b.z;
+// Disjoint parts of a row as one; `scale` is that of its weights.
+template <int N>
+__device__ __forceinline__ Row join(const Row (&part)[N], double scale) {
+  Row r = part[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    const bool over = part[i].top > r.top || (part[i].top == r.top && part[i].at < r.at);
+    r.top = over ? part[i].top : r.top;
+    r.at = over ? part[i].at : r.at;
+  }
+  r.z = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r.z += part[i].z * weight(Heat{(double)r.top, scale}, part[i].top);
   return r;
 }
-// Every kWaves-th chunk of a row, from `first` on; kAhead of them loaded at once.
-__device__ __forceinline__ Row part_of(const Plan& p, const Stat* st, int first, float heat) {
-  constexpr int kAhead = 8;
+// Every kParts-th chunk of a row, from `first` on, four of them loaded at once.
+__device__ __forceinline__ Row part_of(const Plan& p, const Stat* st, int first, double scale) {
   Row r{-INFINITY, INT32_MAX, 0.0};
-  for (int c = first; c < p.chunks; c += kWaves * kAhead) {
-    Stat s[kAhead];
+  for (int c = first; c < p.chunks; c += kParts * 4) {
+    Row part[5];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) s[i] = st[c + kWaves * i < p.chunks ? c + kWaves * i : first];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (c + kWaves * i < p.chunks && s[i].top > -INFINITY) r = join(r, Row{s[i].top, s[i].at, s[i].sum}, heat);
+    for (int i = 0; i < 4; ++i) {
+      const int at = c + kParts * i;
+      const Stat x = st[at < p.chunks ? at : first];
+      const bool some = at < p.chunks && x.top > -INFINITY;
+      part[i] = Row{some ? x.top : -INFINITY, some ? x.at : INT32_MAX, some ? x.sum : 0.0};
+    }
+    part[4] = r;
+    r = join(part, scale);
   }
   return r;
 }
@@ -256,7 +272,7 @@ __device__ __forceinline__ Row part_of(const Plan& p, const Stat* st, int first,
 // Lane i of each wave holds token i; every value that the walk needs is
 // loaded beforehand, for all tokens at once.
 template <class T>
-__device__ __forceinline__ void walk(const Plan& p, int lb, bool writes, Row (&rows)[2][kWaves][64], Last& out) {
+__device__ __forceinline__ void walk(const Plan& p, int lb, bool writes, Row (&rows)[2][kParts][64], Last& out) {
   const VerifyArgs& v = p.v;
   const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, b = p.b0 + lb;
   const int count = count_of(v, b);
@@ -265,41 +281,41 @@ __device__ __forceinline__ void walk(const Plan& p, int lb, bool writes, Row (&r
   const int64_t at = (int64_t)b * v.tokens + lane;
   const bool in = lane < count;
   const bool drawn = v.draft && !greedy && in && lane > 0;   // from the drafter's row of the token before
-  const Stat* stats = p.stats + (int64_t)lb * p.rows * p.chunks;
-  if (in && wave < p.chunks) rows[0][wave][lane] = part_of(p, stats + (int64_t)lane * p.chunks, wave, greedy ? 1.0f : heat);
-  if (drawn && wave < p.chunks)
-    rows[1][wave][lane] =
-        part_of(p, stats + (int64_t)(v.tokens + lane - 1) * p.chunks, wave, dgreedy ? 1.0f : dheat);
-  const int id = in ? v.ids[at] : -1;
+  const double scale = make_heat(0.0f, greedy ? 1.0f : heat).scale;
+  const double dscale = make_heat(0.0f, dgreedy ? 1.0f : dheat).scale;
+  // (what depends on loads in two steps comes first)
+  const bool walks = in && wave == 0;
+  const int id = walks ? v.ids[at] : -1;
   const bool is_id = id >= 0 && id < v.vocab;
-  float u = in ? v.u[at] : 0.0f;
+  float u = walks ? v.u[at] : 0.0f;
   if (u < 0.0f) u = 0.0f;
   int parent = lane - 1;   // (-1: none)
-  if (v.mask && in) {
+  if (v.mask && walks) {
     const uint64_t above = (uint64_t)v.mask[at] & ((1ull << lane) - 1);
     parent = above ? 63 - __builtin_clzll(above) : -1;
   }
-  const bool child = in && parent >= 0 && is_id;
+  const bool child = walks && parent >= 0 && is_id;
   const float x = child ? no_nan(to_float(row_of<T>(v, b, parent)[id])) : -INFINITY;
   const float y = drawn && is_id ? no_nan(to_float(row_of<T>(v, b, v.tokens + lane - 1)[id])) : -INFINITY;
+  const Stat* stats = p.stats + (int64_t)lb * p.rows * p.chunks;
+  const int part = wave % kParts, which = wave / kParts;   // (which 1: the drafter's rows)
+  if (which == 0 ? in : which == 1 && drawn)
+    rows[which][part][lane] = part_of(
+        p, stats + (int64_t)(which ? v.tokens + lane - 1 : lane) * p.chunks, part, which ? dscale : scale);
   __syncthreads();
   if (wave > 0) return;
   Row row{-INFINITY, INT32_MAX, 0.0}, drow = row;
-  if (in) {
-    for (int w = 0; w < kWaves && w < p.chunks; ++w) row = join(row, rows[0][w][lane], greedy ? 1.0f : heat);
-  }
-  if (drawn) {
-    for (int w = 0; w < kWaves && w < p.chunks; ++w) drow = join(drow, rows[1][w][lane], dgreedy ? 1.0f : dheat);
-  }
+  if (in) row = join<kParts>({rows[0][0][lane], rows[0][1][lane], rows[0][2][lane], rows[0][3][lane]}, scale);
+  if (drawn) drow = join<kParts>({rows[1][0][lane], rows[1][1][lane], rows[1][2][lane], rows[1][3][lane]}, dscale);
   const bool some = row.top > -INFINITY;
   // this token's weight among its parent's, and its share of the drafter's
   const float ptop = __shfl(row.top, parent & 63);
   const double pz = __shfl(row.z, parent & 63);
   const int pat = __shfl(row.at, parent & 63);
-  const double mine = greedy ? 0.0 : weight(make_heat(ptop, heat), x);
+  const double mine = greedy ? 0.0 : weight(Heat{(double)ptop, scale}, x);
   double q = 0.0;
   if (drawn && drow.top > -INFINITY)
-    q = dgreedy ? (id == drow.at ? 1.0 : 0.0) : weight(make_heat(drow.top, dheat), y) / drow.z;
+    q = dgreedy ? (id == drow.at ? 1.0 : 0.0) : weight(Heat{(double)drow.top, dscale}, y) / drow.z;
   const uint64_t hits = __ballot(child && id == pat);                        // greedy
   const uint64_t kept_by_q = __ballot(child && (double)u * q < mine / pz);   // chains
   const uint64_t filled = __ballot(in && some);
@@ -364,25 +380,32 @@ __device__ __forceinline__ void walk(const Plan& p, int lb, bool writes, Row (&r
   }
 }
 
-// What is left of a thread's 16 tokens.
+__device__ __forceinline__ double of_waves(const double* sums) {
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kManyWaves; ++w) s += sums[w];
+  return s;
+}
+
+// What is left of a thread's tokens.
 template <class T, bool VEC>
-__device__ __forceinline__ void left16(const VerifyArgs& v, int b, const Last& l, int mode, int i0,
-                                       double (&r)[kPer]) {
-  float x[kPer];
-  load16<VEC>(row_of<T>(v, b, l.node), i0, v.vocab, x);
+__device__ __forceinline__ void left_of(const VerifyArgs& v, int b, const Last& l, int mode, int i0,
+                                       double (&r)[kFew]) {
+  float x[kFew];
+  load<VEC, kFew>(row_of<T>(v, b, l.node), i0, v.vocab, x);
   const Heat h = make_heat(l.top, heat_of(v, b, false));
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) r[i] = weight(h, x[i]);
+  for (int i = 0; i < kFew; ++i) r[i] = weight(h, x[i]);
   if (mode == kResidual) {
-    float y[kPer];
-    load16<VEC>(row_of<T>(v, b, v.tokens + l.node), i0, v.vocab, y);
+    float y[kFew];
+    load<VEC, kFew>(row_of<T>(v, b, v.tokens + l.node), i0, v.vocab, y);
     const float dheat = heat_of(v, b, true);
     const Heat d = make_heat(l.draft_top, dheat);
     const double pz = 1.0 / l.z, qz = l.draft_top > -INFINITY ? 1.0 / l.draft_z : 0.0;
     int first = INT32_MAX;
     if (!(dheat > 0.0f)) first = l.ids[0];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < kFew; ++i) {
       double q;
       if (dheat > 0.0f) q = weight(d, y[i]) * qz;
       else q = i0 + i == first ? 1.0 : 0.0;
@@ -392,16 +415,16 @@ __device__ __forceinline__ void left16(const VerifyArgs& v, int b, const Last& l
     for (int k = 0; k < l.rejected; ++k) {
       const int e = l.ids[k] - i0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) r[i] = i == e ? 0.0 : r[i];
+      for (int i = 0; i < kFew; ++i) r[i] = i == e ? 0.0 : r[i];
     }
   }
 }
 
 template <class T, bool VEC>
-__global__ __launch_bounds__(kNT) void k_verify_walk(Plan p) {
+__global__ __launch_bounds__(kMany) void k_verify_walk(Plan p) {
   __shared__ Last l;
-  __shared__ Row rows[2][kWaves][64];
-  __shared__ double sums[kWaves];
+  __shared__ Row rows[2][kParts][64];
+  __shared__ double sums[kManyWaves];
   const int tid = threadIdx.x;
   const int lb = blockIdx.x / p.chunks, chunk = blockIdx.x - lb * p.chunks;
   walk<T>(p, lb, chunk == 0, rows, l);
@@ -411,23 +434,23 @@ __global__ __launch_bounds__(kNT) void k_verify_walk(Plan p) {
     if (tid < kWords) ((int32_t*)&p.last[lb])[tid] = ((const int32_t*)&l)[tid];
   }
   if (l.mode == kDone) return;
-  double r[kPer], sum = 0.0;
-  left16<T, VEC>(p.v, p.b0 + lb, l, l.mode, chunk * kChunk + tid * kPer, r);
+  double r[kFew], sum = 0.0;
+  left_of<T, VEC>(p.v, p.b0 + lb, l, l.mode, chunk * kChunk + tid * kFew, r);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) sum += r[i];
+  for (int i = 0; i < kFew; ++i) sum += r[i];
   sum = wave_sum(sum);
   if (tid % 64 == 0) sums[tid / 64] = sum;
   __syncthreads();
-  if (tid == 0) p.sums[(int64_t)lb * p.chunks + chunk] = ((sums[0] + sums[1]) + sums[2]) + sums[3];
+  if (tid == 0) p.sums[(int64_t)lb * p.chunks + chunk] = of_waves(sums);
 }
 
 // Of `mine`, one value a thread: the first thread at which the running sum from
 // `before` on passes `goal`, else the last one with a value above 0; -1 where there
 // is none.  `below`: the running sum before it.  The same in every thread.
 struct Find {
-  double sums[kWaves];
-  int hit[kWaves], any[kWaves];
-  double below[kNT];
+  double sums[kManyWaves];
+  int hit[kManyWaves], any[kManyWaves];
+  double below[kMany];
 };
 __device__ __forceinline__ int find(Find& f, double mine, double before, double goal, double& below) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
@@ -450,9 +473,9 @@ __device__ __forceinline__ int find(Find& f, double mine, double before, double 
   }
   __syncthreads();
   int at = -1;
-  for (int w = kWaves - 1; w >= 0; --w) at = f.hit[w] >= 0 ? f.hit[w] : at;
+  for (int w = kManyWaves - 1; w >= 0; --w) at = f.hit[w] >= 0 ? f.hit[w] : at;
   if (at < 0)
-    for (int w = 0; w < kWaves; ++w) at = f.any[w] >= 0 ? f.any[w] : at;
+    for (int w = 0; w < kManyWaves; ++w) at = f.any[w] >= 0 ? f.any[w] : at;
   below = at >= 0 ? f.below[at] : before;
   return at;
 }
@@ -467,18 +490,18 @@ __device__ __forceinline__ double total_of(const Plan& p, const double* sums, in
   __syncthreads();
   if (tid % 64 == 0) sh[tid / 64] = part;
   __syncthreads();
-  return ((sh[0] + sh[1]) + sh[2]) + sh[3];
+  return of_waves(sh);
 }
 
 template <class T, bool VEC>
-__global__ __launch_bounds__(kNT) void k_verify_pick(Plan p) {
+__global__ __launch_bounds__(kMany) void k_verify_pick(Plan p) {
   __shared__ Find f;
-  __shared__ double sh[kWaves];
+  __shared__ double sh[kManyWaves];
   const VerifyArgs& v = p.v;
   const int tid = threadIdx.x, lb = blockIdx.x, b = p.b0 + lb;
   const Last& l = p.last[lb];
   double* sums = p.sums + (int64_t)lb * p.chunks;
-  const int each = (p.chunks + kNT - 1) / kNT;
+  const int each = (p.chunks + kMany - 1) / kMany;
   const float given = v.u[(int64_t)b * v.tokens];
   const double u = given < 0.0f ? 0.0 : (double)given;
   int mode = l.mode;
@@ -489,15 +512,15 @@ __global__ __launch_bounds__(kNT) void k_verify_pick(Plan p) {
     // nothing left, as for a u of 1 (or but by rounding): the row itself
     mode = kWhole;
     for (int c = 0; c < p.chunks; ++c) {
-      double r[kPer], part = 0.0;
-      left16<T, VEC>(v, b, l, mode, c * kChunk + tid * kPer, r);
+      double r[kFew], part = 0.0;
+      left_of<T, VEC>(v, b, l, mode, c * kChunk + tid * kFew, r);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) part += r[i];
+      for (int i = 0; i < kFew; ++i) part += r[i];
       part = wave_sum(part);
       __syncthreads();
       if (tid % 64 == 0) sh[tid / 64] = part;
       __syncthreads();
-      if (tid == 0) sums[c] = ((sh[0] + sh[1]) + sh[2]) + sh[3];
+      if (tid == 0) sums[c] = of_waves(sh);
     }
     __syncthreads();
     total = total_of(p, sums, each, sh, mine);
@@ -518,15 +541,15 @@ __global__ __launch_bounds__(kNT) void k_verify_pick(Plan p) {
     }
     sum += s;
   }
-  double r[kPer], part = 0.0;
-  const int i0 = chunk * kChunk + tid * kPer;
-  left16<T, VEC>(v, b, l, mode, i0, r);
+  double r[kFew], part = 0.0;
+  const int i0 = chunk * kChunk + tid * kFew;
+  left_of<T, VEC>(v, b, l, mode, i0, r);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) part += r[i];
+  for (int i = 0; i < kFew; ++i) part += r[i];
   const int who = find(f, part, at_chunk, goal, below);
   if (tid != who) return;
   int token = -1;
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < kFew; ++i) {
     if (!(r[i] > 0.0)) continue;
     token = i0 + i;
     below += r[i];
@@ -557,8 +580,8 @@ hipError_t launch_parts(const VerifyArgs& v, hipStream_t s) {
     const int64_t n = v.batch - b0 < part ? v.batch - b0 : part;
     p.b0 = (int)b0;
     hipLaunchKernelGGL((k_verify_stats<T, VEC>), dim3((unsigned)(n * blocks)), dim3(kNT), 0, s, p);
-    hipLaunchKernelGGL((k_verify_walk<T, VEC>), dim3((unsigned)(n * p.chunks)), dim3(kNT), 0, s, p);
-    hipLaunchKernelGGL((k_verify_pick<T, VEC>), dim3((unsigned)n), dim3(kNT), 0, s, p);
+    hipLaunchKernelGGL((k_verify_walk<T, VEC>), dim3((unsigned)(n * p.chunks)), dim3(kMany), 0, s, p);
+    hipLaunchKernelGGL((k_verify_pick<T, VEC>), dim3((unsigned)n), dim3(kMany), 0, s, p);
     e = hipGetLastError();
   }
   const hipError_t f = workspace_release(ws, s);
