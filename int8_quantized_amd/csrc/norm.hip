@@ -126,16 +126,23 @@ __device__ __forceinline__ double over_row(double v, double* sh, F&& f) {
   return over_waves(sh, f);
 }
 
-// rint(p * 127 / top) in the low byte.  With inv = 127 / top the product's rounding differs from
-// the quotient's by 2^-52 of it, which matters next to a tie (near).
+// rint(p * 127 / top).  fast_code: in the high byte, of q = p * 127 / top with 24 bits behind the
+// point and a half added, as the sum's low word; the lower bytes are the distance from the tie
+// below, in 2^-24.  With inv = 127 / top the product's rounding differs from the
+// quotient's by 2^-52 of it, which matters next to a tie: kNear says how near.
 constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: the sum's low word is the nearest whole number
-__device__ __forceinline__ uint32_t fast_code(double p, double inv, bool& near) {
-  const double q = p * inv, t = q + kMagic;
-  near |= __builtin_fabs(q - (t - kMagic)) > 0.499999;
-  return (uint32_t)__builtin_bit_cast(uint64_t, t);
+constexpr uint32_t kNear = 4;
+__device__ __forceinline__ uint32_t fast_code(double p, double inv) {
+  constexpr double kHalf = 0x1.8p28 + 0.5 + kNear / 2 * 0x1p-24;   // 1.5 * 2^(52 - 24)
+  return (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(p, inv, kHalf));
 }
 __device__ __forceinline__ uint32_t exact_code(double p, double top) {
   return (uint32_t)__builtin_bit_cast(uint64_t, p * 127.0 / top + kMagic);
+}
+// The high bytes of four words.
+__device__ __forceinline__ uint32_t pack_high(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0703), hi = __builtin_amdgcn_perm(d, c, 0x07030c0c);
+  return lo | hi;
 }
 
 // 1 / x and 1 / sqrt(x) to the last bit or two, from the estimates by Newton steps.
@@ -268,13 +275,17 @@ __global__ __launch_bounds__(kMaxThreads, C == 1 ? 8 : 4) void k_norm(NormArgs a
   for (int c = 0; c < C; ++c) {
     const int e = 8 * (tid + c * nt);
     if (e >= n) continue;
-    uint32_t q[8];
-    bool near = false;
+    uint32_t q[8], least = kNear;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = fast_code(p[c][i], inv, near);
-    if (near) {
+    for (int i = 0; i < 8; ++i) q[i] = fast_code(p[c][i], inv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = exact_code(p[c][i], top);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t r = q[i] & 0xffffff;
+      least = r < least ? r : least;
+    }
+    if (least < kNear) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = exact_code(p[c][i], top) << 24;
     }
     if (!(inv > 0.0)) {
 #pragma unroll
@@ -282,11 +293,11 @@ __global__ __launch_bounds__(kMaxThreads, C == 1 ? 8 : 4) void k_norm(NormArgs a
     }
     int8_t* dst = a.codes + t * a.n + e;
     if constexpr (VEC) {
-      *reinterpret_cast<v2u*>(dst) = v2u{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
+      *reinterpret_cast<v2u*>(dst) = v2u{pack_high(q[0], q[1], q[2], q[3]), pack_high(q[4], q[5], q[6], q[7])};
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < n - e) dst[i] = (int8_t)q[i];
+        if (i < n - e) dst[i] = (int8_t)(q[i] >> 24);
     }
   }
 }
