@@ -16,6 +16,13 @@
 // thread): x, residual and gate are read once, the sum and the codes written
 // once, and the two or three sums over the row meet in LDS.  Rows too long for
 // that are read again for each sum (k_norm_long).
+//
+// Measured: 8191 x 5120 bf16 with both norms, residual and gate 87 us, 294 MB at
+// 3.4 TB/s (a copy of the same bytes 57): the vector instructions, 47 for an element, are
+// busy six tenths of the time and the rows' barriers keep them and the loads from
+// overlapping whole.  One row of 4096: 2.8 us, a chain of latencies.  Workgroups that
+// take row after row and load the next one early, and 32-bit estimates of the codes,
+// both took 108 when this form took 108 too.
 #include "decode.h"
 
 namespace q8ta {
@@ -369,7 +376,7 @@ hipError_t launch_type(const NormArgs& a, hipStream_t s) {
   const bool vec = a.n % 8 == 0 && strides % 8 == 0 && ptrs % 16 == 0 && (uintptr_t)a.codes % 8 == 0;
   const int64_t groups = (a.n + 7) / 8;
   auto threads = [&](int c) { return (int)((groups + 64 * c - 1) / (64 * c)) * 64; };
-  // 16 elements a thread where there are many rows (8191 x 5120: 93 us against 99 with 8), 8 where
+  // 16 elements a thread where there are many rows (8191 x 5120: 87 us, with 8 6 % more), 8 where
   // a row is a chain of latencies
   if (groups <= 1024 && a.tokens < 512) launch_regs<T, 1>(a, vec, threads(1), s);
   else if (groups <= 2048) launch_regs<T, 2>(a, vec, threads(2), s);
