@@ -718,7 +718,7 @@ q8ta_status q8ta_quantize_per_token(const void* x, int64_t x_stride, q8ta_dtype 
 /* ---------------------------------------------------------------------------
  * q8ta_linear_per_token: the int8 product with a scale for each token and
  * channel, symmetric codes and a floating-point output:
- *   acc[m, n] = sum_k x[m, k] * weight[n, k]                          (int32)
+ *   acc[m, n] = sum_k x[m, k] * weight[n, k]   (int32: any codes up to K = 131071)
  *   y = ((float)acc * x_scales[m]) * weight_scales[n] + bias[n]
  *   out[m, n] = y, or max(y, 0) for "relu", rounded once to out_dtype.
  * x: int8 [M, K], weight: int8 [N, K], x_scales fp32 [M], weight_scales fp32 [N],
@@ -766,7 +766,10 @@ q8ta_status q8ta_gated_linear(const int8_t* x, int64_t M, int64_t K, const float
  * other.  T <= 0 (or NaN) is greedy: a child is kept if it is the target's
  * largest (the first of equal ones), and next is that.  T' = draft_temperature[b], or T
  * where draft_temperature is NULL; T' <= 0 puts all of q on its largest.
- * Sums and weights are 64-bit and added in an order that depends on vocab alone.
+ * What a token is drawn from is 64-bit; the sums that shares are divided by take
+ * small weights in 32 bits and are off by some 1e-8 of themselves (there, logits
+ * further apart than fp32 holds count as infinitely far).  All is added in an order that depends on
+ * vocab alone.
  * A NaN logit counts as -inf; +inf logits share the weight alone; where all
  * logits are -inf the walk ends, with next -1.  An id outside [0, vocab) has p and q 0.
  * u: in [0, 1); below 0 as 0; one of 1 and beyond keeps no drawn child with p <= q and

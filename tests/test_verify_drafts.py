@@ -284,6 +284,28 @@ def test_verify_does_not_depend_on_the_batch():
         assert all((a[b:b + 1] == o).all() for a, o in zip(whole, run(one)))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,V,draft", [(40000, 64, 5, False), (65535, 33, 9, True)])
+def test_verify_of_more_requests_than_one_launch(B, T, V, draft):
+    g = torch.Generator(device="cuda").manual_seed(B)
+    x = torch.randn(B, T, V, generator=g, device="cuda")
+    y = torch.randn(B, T - 1, V, generator=g, device="cuda") if draft else None
+    ids = torch.randint(0, V, (B, T), generator=g, dtype=torch.int32, device="cuda")
+    u = torch.rand(B, T, generator=g, device="cuda") * 0.3
+    heat = torch.rand(B, generator=g, device="cuda") + 0.5
+
+    def run_rows(a, b):
+        outs = [torch.full(s, -7, dtype=torch.int32, device="cuda") for s in ((b - a, T), (b - a,), (b - a,))]
+        q8.q8ta_verify_drafts(x[a:b], None if y is None else y[a:b], ids[a:b], None, None, heat[a:b], None, u[a:b],
+                              *outs)
+        return outs
+
+    whole, parts = run_rows(0, B), [run_rows(a, min(a + 9999, B)) for a in range(0, B, 9999)]
+    for i, o in enumerate(whole):
+        assert torch.equal(o, torch.cat([p[i] for p in parts]))
+    assert (whole[1] > 1).any() and ((whole[2] >= 0) & (whole[2] < V)).all()
+
+
 def frequencies_near(counts, p, n):
     # five standard deviations of a count
     assert (np.abs(counts - n * p) <= 5 * np.sqrt(n * p * (1 - p)) + 1).all(), (counts / n, p)
