@@ -210,7 +210,9 @@ struct ScaledArgs {
   void* y;                    // [M, N]
   int y_type;
   int64_t n0 = 0;             // first channel of a launch of the row kernel
+  int tile = -1;              // of the GEMM: one of kTile*
 };
+enum { kTile64Split, kTile64, kTile128, kTile256x128, kTile256 };
 hipError_t launch_scaled(ScaledArgs a, hipStream_t s);
 // The GEMM for K a multiple of 16 up to 2^23 and 16-byte aligned x and w, by the type of y.
 hipError_t launch_tiles_f32(const ScaledArgs& a, hipStream_t s);

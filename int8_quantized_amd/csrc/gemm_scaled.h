@@ -20,7 +20,6 @@
 //  * Rows past M or N read the last row; their products are not stored.
 #pragma once
 
-#include <cmath>
 #include <type_traits>
 
 #include "scaled_epilogue.h"
@@ -419,48 +418,13 @@ hipError_t launch_one(const ScaledArgs& a, hipStream_t s) {
   return hipSuccess;
 }
 
-// Which tile, by an estimate of the time in us: a start, and for each 64-byte step the
-// larger of its latency times the rounds of workgroups and of all tiles' loads at the 13
-// TB/s at which they come from the L2s; the large tiles' steps take up to 40 % longer where
-// they fill the card.  Measured (K 4096, us; four waves that share K, one, T64, T128,
-// T256): 65 x 4096 10.7, 18, 21, 28, 41; 128 x 11008 22, 20, 21, 29, 42; 400 x 4096 20,
-// 20, 21, 27, 42; 1024 x 4096 -, 31, 26, 29, 42; 400 x 11008 49, 51, 36, 33, 42; 768 x
-// 11008 -, 85, 56, 59, 45.
-struct Guess {
-  double start, step;
-  int at_once, tn, bm;   // workgroups of a CU
-  bool large;
-};
-constexpr Guess kGuess[] = {{3.0, 0.13, 1, 64, 64, false},
-                            {2.0, 0.25, 6, 64, 64, false},
-                            {2.5, 0.28, 3, 128, 128, false},
-                            {3.0, 0.40, 1, 256, 128, true},
-                            {4.0, 0.59, 1, 256, 256, true}};
-int best_tile(int64_t m, int64_t rows, int64_t steps) {
-  int best = 0;
-  double least = 0.0;
-  for (int i = 0; i < 5; ++i) {
-    const Guess& g = kGuess[i];
-    const double tiles = (double)((m + g.bm - 1) / g.bm) * (double)((rows + g.tn - 1) / g.tn);
-    const double rounds = std::ceil(tiles / (256.0 * g.at_once)), fill = tiles < 256.0 ? tiles / 256.0 : 1.0;
-    const double latency = g.step * rounds * (g.large ? 1.0 + 0.4 * fill * fill : 1.0);
-    const double loads = tiles * (g.tn + g.bm) * 64 / 13e6;
-    const double t = g.start + (double)steps * (latency > loads ? latency : loads);
-    if (i == 0 || t < least) {
-      best = i;
-      least = t;
-    }
-  }
-  return best;
-}
-
 template <int MATS, class YT>
 hipError_t launch_plan(const ScaledArgs& a, hipStream_t s) {
-  switch (best_tile(a.M, (a.N + 31) / 32 * 32 * MATS, (a.K + 63) / 64)) {
-    case 0: return launch_one<T32, MATS, YT, 4>(a, s);
-    case 1: return launch_one<T32, MATS, YT>(a, s);
-    case 2: return launch_one<T64, MATS, YT>(a, s);
-    case 3: return launch_one<T128, MATS, YT>(a, s);
+  switch (a.tile) {
+    case kTile64Split: return launch_one<T32, MATS, YT, 4>(a, s);
+    case kTile64: return launch_one<T32, MATS, YT>(a, s);
+    case kTile128: return launch_one<T64, MATS, YT>(a, s);
+    case kTile256x128: return launch_one<T128, MATS, YT>(a, s);
   }
   // Whole rounds of 256 x 256 tiles, then the columns that are left as 256 x 128 tiles where
   // those fit one round, in the same launch: they start on the CUs that the first

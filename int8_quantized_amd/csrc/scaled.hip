@@ -11,6 +11,7 @@
 // steps' loads in flight), and their integer sums meet in LDS.  The gated form
 // has a channel's gate and up rows in one workgroup, so that the block is one
 // launch and the two products never reach memory.
+#include <cmath>
 #include <type_traits>
 
 #include "scaled_epilogue.h"
@@ -154,12 +155,48 @@ hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
   return a.M <= 32 ? launch_shape<YT, 1, 2, 1, 16, 4>(a, s) : launch_shape<YT, 1, 4, 1, 16, 2>(a, s);
 }
 
-// The row kernel reads all rows of x for 16 channels: up to 16 rows it is the faster
-// everywhere, up to 64 where one round of 256 workgroups holds the channels (50 rows x
-// 4096 x 4096 10.2 us against 11.5 with the tiles, x 11008 27 and 12.8).  (A tile's
-// offsets are 32-bit.)
-bool by_rows(const ScaledArgs& a) {
-  return a.M <= 16 || (a.M <= 64 && a.N <= 16 * 256) || a.K > (int64_t)1 << 23;
+// Which kernel, by an estimate of the time in us.  The tiles: a start, and for each 64-byte
+// step the larger of its latency (which grows as the tiles fill the card) times the
+// rounds of workgroups, and of all tiles' loads at the 10.7 TB/s at which they come from the
+// L2s.  The row kernel, which reads all rows of x for each 16 channels: a start and, for each
+// round of 256 workgroups, the rows of x and the weights' at 28 KB a us.  The numbers are fitted to the
+// measured times of all six kernels at 540 sizes (17 to 2048 rows, K 512 to 11008, N 256 to 28000, one
+// and two matrices): what it takes is 1 % slower than the fastest on average, 23 % at most.  Some
+// of them, K 4096 and one matrix (us; rows, four waves that share K, one, 128 x 128, 256 x 128, 256 x 256):
+// 17 x 4096 6.5, 7.5, 18, 17, 26, 38; 64 x 4096 11.8, 8.2, 18, 19, 28, 41; 128 x 11008 -, 23, 20,
+// 22, 29, 42; 512 x 4096 -, 23, 20, 20, 27, 40; 512 x 11008 -, 61, 49, 37, 33, 42; 1000 x 11008 -,
+// 119, 104, 65, 62, 52.
+struct Guess {
+  double start, step, fill;
+  int at_once, tn, bm;   // workgroups of a CU, the tile
+};
+constexpr Guess kGuess[] = {{2.4, 0.094, 1.31, 1, 64, 64},     // in the order of kTile*
+                            {1.6, 0.201, 0.66, 6, 64, 64},
+                            {3.0, 0.390, 0.0, 3, 128, 128},
+                            {3.0, 0.387, 0.08, 1, 256, 128},
+                            {4.1, 0.560, 0.37, 1, 256, 256}};
+// The tile, or -1 for the row kernel.
+int best_kernel(const ScaledArgs& a) {
+  // (a tile's offsets are 32-bit; up to 16 rows the row kernel is the faster everywhere)
+  if (a.M <= 16 || a.K > (int64_t)1 << 23) return -1;
+  const double m = (double)a.M, k = (double)a.K, steps = std::ceil(k / 64);
+  const double rows = std::ceil((double)a.N / 32) * 32 * a.mats;
+  int best = -1;
+  double least = 1.8 + std::ceil((double)a.N / 16 / 256) * (m + 16 * a.mats) * k / 28100.0;
+  if (a.M > 64) least = INFINITY;
+  for (int i = 0; i < 5; ++i) {
+    const Guess& g = kGuess[i];
+    const double tiles = std::ceil(m / g.bm) * std::ceil(rows / g.tn);
+    const double rounds = std::ceil(tiles / (256.0 * g.at_once)), fill = tiles < 256.0 ? tiles / 256.0 : 1.0;
+    const double latency = g.step * rounds * (1.0 + g.fill * fill * fill);
+    const double loads = tiles * (g.tn + g.bm) * 64 / 10.7e6;
+    const double t = g.start + steps * (latency > loads ? latency : loads);
+    if (t < least) {
+      best = i;
+      least = t;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -186,7 +223,8 @@ hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
     a.K = kp;
   }
   if (e == hipSuccess) {
-    const bool rows = by_rows(a);
+    a.tile = best_kernel(a);
+    const bool rows = a.tile < 0;
     if (a.y_type == Q8TA_F32) e = rows ? launch_rows<float>(a, s) : launch_tiles_f32(a, s);
     else if (a.y_type == Q8TA_F16) e = rows ? launch_rows<Half>(a, s) : launch_tiles_f16(a, s);
     else e = rows ? launch_rows<Bfloat>(a, s) : launch_tiles_bf16(a, s);
