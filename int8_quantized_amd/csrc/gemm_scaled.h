@@ -426,23 +426,13 @@ hipError_t launch_plan(const ScaledArgs& a, hipStream_t s) {
     case kTile128: return launch_one<T64, MATS, YT>(a, s);
     case kTile256x128: return launch_one<T128, MATS, YT>(a, s);
   }
-  // Whole rounds of 256 x 256 tiles, then the columns that are left as 256 x 128 tiles where
-  // those fit one round, in the same launch: they start on the CUs that the first
-  // whole tiles free.
+  // Columns of whole tiles, then the others as 256 x 128 tiles, in the same launch: they start on
+  // the CUs that the first whole tiles free.
   constexpr int64_t CN = T256::TN / MATS;
   static_assert(T128::TN == T256::TN, "one width");
-  const int64_t n = (a.N + CN - 1) / CN;
   const int64_t ma = (a.M + T256::BM - 1) / T256::BM, mb = (a.M + T128::BM - 1) / T128::BM;
-  const int64_t tiles = ma * n;
-  int64_t cols = n, rest = 0;
-  if (tiles % 256 != 0 && 256 % ma == 0 && tiles > 256) {
-    const int64_t c = tiles / 256 * 256 / ma;
-    if ((n - c) * mb <= 256) {
-      cols = c;
-      rest = n - c;
-    }
-  }
-  if (rest == 0 || tiles > kMostTiles) return launch_one<T256, MATS, YT>(a, s);
+  const int64_t cols = a.columns, rest = (a.N + CN - 1) / CN - cols;
+  if (rest == 0) return launch_one<T256, MATS, YT>(a, s);
   hipLaunchKernelGGL((k_gemm_scaled<T256, T128, MATS, YT>), dim3((unsigned)(ma * cols + mb * rest)),
                      dim3(T256::NT), 0, s, a, (int)ma, (int)(ma * cols), (int)mb, (int)(mb * rest), cols * CN);
   return hipGetLastError();

@@ -175,13 +175,13 @@ constexpr Guess kGuess[] = {{2.4, 0.094, 1.31, 1, 64, 64},     // in the order o
                             {3.0, 0.390, 0.0, 3, 128, 128},
                             {3.0, 0.387, 0.08, 1, 256, 128},
                             {4.1, 0.560, 0.37, 1, 256, 256}};
-// The tile, or -1 for the row kernel.
-int best_kernel(const ScaledArgs& a) {
+// Sets the tile, -1 for the row kernel.
+void choose(ScaledArgs& a) {
   // (a tile's offsets are 32-bit; up to 16 rows the row kernel is the faster everywhere)
-  if (a.M <= 16 || a.K > (int64_t)1 << 23) return -1;
+  a.tile = -1;
+  if (a.M <= 16 || a.K > (int64_t)1 << 23) return;
   const double m = (double)a.M, k = (double)a.K, steps = std::ceil(k / 64);
   const double rows = std::ceil((double)a.N / 32) * 32 * a.mats;
-  int best = -1;
   double least = 1.8 + std::ceil((double)a.N / 16 / 256) * (m + 16 * a.mats) * k / 28100.0;
   if (a.M > 64) least = INFINITY;
   for (int i = 0; i < 5; ++i) {
@@ -192,11 +192,22 @@ int best_kernel(const ScaledArgs& a) {
     const double loads = tiles * (g.tn + g.bm) * 64 / 10.7e6;
     const double t = g.start + steps * (latency > loads ? latency : loads);
     if (t < least) {
-      best = i;
+      a.tile = i;
       least = t;
     }
   }
-  return best;
+  // Whole rounds of 256 x 256 tiles, and the columns that are left as 256 x 128 tiles where those
+  // fit one round, which takes that tile's time.
+  const int64_t c = 256 / a.mats, n = (a.N + c - 1) / c, ma = (a.M + 255) / 256, mb = (a.M + 127) / 128;
+  a.columns = n;
+  const int64_t whole = ma * n / 256, cols = whole * 256 / ma;
+  if (whole == 0 || cols == n || (n - cols) * mb > 256 || ma * cols > 1 << 20) return;
+  const Guess &g = kGuess[kTile256], &h = kGuess[kTile256x128];
+  const double t = g.start + steps * (g.step * (1.0 + g.fill) * (double)whole + h.step * (1.0 + h.fill));
+  if (t < least) {
+    a.tile = kTile256;
+    a.columns = cols;
+  }
 }
 
 }  // namespace
@@ -223,7 +234,7 @@ hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
     a.K = kp;
   }
   if (e == hipSuccess) {
-    a.tile = best_kernel(a);
+    choose(a);
     const bool rows = a.tile < 0;
     if (a.y_type == Q8TA_F32) e = rows ? launch_rows<float>(a, s) : launch_tiles_f32(a, s);
     else if (a.y_type == Q8TA_F16) e = rows ? launch_rows<Half>(a, s) : launch_tiles_f16(a, s);
