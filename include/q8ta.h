@@ -724,8 +724,9 @@ q8ta_status q8ta_quantize_per_token(const void* x, int64_t x_stride, q8ta_dtype 
  * x: int8 [M, K], weight: int8 [N, K], x_scales fp32 [M], weight_scales fp32 [N],
  * bias fp32 [N] or NULL; out: dense [M, N].  Requirements: M <= 2^21, N and K <=
  * 2^30, the elements of each tensor <= 2^40.  Any K and alignment: where K is no
- * multiple of 16 or x or a weight is not 16-byte aligned, they are first copied into
- * rows that are (workspace: (M + N) * K bytes, K rounded up to 16); none otherwise.
+ * multiple of 16 or x or a weight is not 16-byte aligned, for more than some rows, or K
+ * below 16, they are first copied into rows that are (workspace: (M + N) * K bytes, K
+ * rounded up to 16); none otherwise.
  *
  * q8ta_gated_linear: two such products and the gate between them in one launch:
  *   out[m, n] = act(y_gate[m, n]) * y_up[m, n], rounded once to out_dtype,

@@ -211,6 +211,7 @@ struct ScaledArgs {
   int y_type;
   int64_t n0 = 0;             // first channel of a launch of the row kernel
   int tile = -1;              // of the GEMM: one of kTile*
+  bool odd = false;           // K is no multiple of 16, or x or a weight not 16-byte aligned
   int64_t columns = 0;        // kTile256: of whole tiles; what is left takes 256 x 128 ones
 };
 enum { kTile64Split, kTile64, kTile128, kTile256x128, kTile256 };

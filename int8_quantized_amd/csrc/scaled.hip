@@ -21,8 +21,11 @@ namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 
-// FN: fragments of 16 weight rows, FN / MATS of each matrix.
-template <class YT, int MATS, int MT, int FN, int WAVES, int D>
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(1)));
+
+// FN: fragments of 16 weight rows, FN / MATS of each matrix.  ODD: any alignment and any K >= 16;
+// a row's last chunk is then its last 16 bytes, those that the chunk before had as zeros in x.
+template <class YT, int MATS, int MT, int FN, int WAVES, int D, bool ODD>
 __global__ __launch_bounds__(64 * WAVES) void k_scaled_rows(ScaledArgs a) {
   constexpr int BM = 16 * MT, BN = 16 * FN, C = BN / MATS, H = FN / MATS;
   __shared__ int32_t part[WAVES][BM][BN + 1];
@@ -47,12 +50,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_scaled_rows(ScaledArgs a) {
   v4i wf[D][FN], xf[D][MT];
   // every load unconditional: chunks past K read the row's first bytes, and the
   // rows' are replaced by zeros when they are used
+  using Chunk = std::conditional_t<ODD, v4i_any, v4i>;
   auto load = [&](int64_t k, v4i (&w)[FN], v4i (&x)[MT]) {
-    const int64_t kk = k + 16 * g < K ? k + 16 * g : 0;
+    int64_t kk = k + 16 * g < K ? k + 16 * g : 0;
+    if (ODD && kk > K - 16) kk = K - 16;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) w[i] = *reinterpret_cast<const v4i*>(wp[i] + kk);
+    for (int i = 0; i < FN; ++i) w[i] = *reinterpret_cast<const Chunk*>(wp[i] + kk);
 #pragma unroll
-    for (int j = 0; j < MT; ++j) x[j] = *reinterpret_cast<const v4i*>(xp[j] + kk);
+    for (int j = 0; j < MT; ++j) x[j] = *reinterpret_cast<const Chunk*>(xp[j] + kk);
   };
   constexpr int kStride = 64 * WAVES;
 #pragma unroll
@@ -60,10 +65,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_scaled_rows(ScaledArgs a) {
   for (int64_t k0 = 64 * wave; k0 < K; k0 += kStride * D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const bool ok = k0 + kStride * d + 16 * g < K;
+      const int64_t kk = k0 + kStride * d + 16 * g;
+      v4i keep = kk < K ? v4i{-1, -1, -1, -1} : v4i{0, 0, 0, 0};
+      if (ODD && kk < K && kk > K - 16) {
+        const int twice = (int)(kk - (K - 16));   // bytes of the chunk before, 1 to 15
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          keep[i] = twice >= 4 * i + 4 ? 0 : (twice <= 4 * i ? -1 : (int)(0xffffffffu << (8 * (twice - 4 * i))));
+      }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        const v4i x = ok ? xf[d][j] : v4i{0, 0, 0, 0};
+        const v4i x = xf[d][j] & keep;
 #pragma unroll
         for (int i = 0; i < FN; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[d][i], x, acc[i][j], 0, 0, 0);
@@ -118,7 +130,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_scaled_rows(ScaledArgs a) {
 
 constexpr int64_t kMostThreads = (int64_t)1 << 31;   // of one launch
 
-template <class YT, int MATS, int MT, int FN, int WAVES, int D>
+template <class YT, int MATS, int MT, int FN, int WAVES, int D, bool ODD>
 hipError_t launch_shape(ScaledArgs a, hipStream_t s) {
   constexpr int64_t C = 16 * FN / MATS, most = kMostThreads / (64 * WAVES);
   const int64_t tiles = (a.N + C - 1) / C;
@@ -126,7 +138,7 @@ hipError_t launch_shape(ScaledArgs a, hipStream_t s) {
     a.n0 = t0 * C;
     const dim3 g((unsigned)(tiles - t0 < most ? tiles - t0 : most),
                  (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
-    hipLaunchKernelGGL((k_scaled_rows<YT, MATS, MT, FN, WAVES, D>), g, dim3(64 * WAVES), 0, s, a);
+    hipLaunchKernelGGL((k_scaled_rows<YT, MATS, MT, FN, WAVES, D, ODD>), g, dim3(64 * WAVES), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -139,30 +151,54 @@ hipError_t launch_shape(ScaledArgs a, hipStream_t s) {
 // workgroups times what one takes (1 x 11008: 16.9 us against 18.4, 1 x 2048: 8.0
 // and 4.3).  Plain loads: nontemporal ones took 10 to 20 % longer, also for weights that
 // no cache holds.
-template <class YT>
-hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
+// Channels of a workgroup:
+int64_t channels_of(const ScaledArgs& a) {
+  auto cost = [&](int64_t c) { return ((a.N + 16 * c - 1) / (16 * c) + 255) / 256 * (c + 1); };
+  return a.mats == 2 && a.M <= 16 && cost(3) < cost(1) ? 48 : 16;
+}
+
+// (D: a wave's steps, up to what measured best: a load that is not needed is no smaller than one that is,
+// 16 x 1024 x 11008 12.6 us with four at a time.  All of them at once where there are up to four; where there
+// are more, two: 1 x 11008 x 4096 10.7 with four, 9.8 with two.)
+template <class YT, bool ODD>
+hipError_t launch_rows_of(const ScaledArgs& a, hipStream_t s) {
+  const int64_t k16 = (a.K + 1023) / 1024;   // steps of one of sixteen waves
   if (a.mats == 2) {
     if (a.M <= 16) {
-      auto cost = [&](int64_t c) { return ((a.N + 16 * c - 1) / (16 * c) + 255) / 256 * (c + 1); };
-      return cost(3) < cost(1) ? launch_shape<YT, 2, 1, 6, 16, 2>(a, s) : launch_shape<YT, 2, 1, 2, 16, 2>(a, s);
+      if (channels_of(a) == 48)
+        return k16 == 1 ? launch_shape<YT, 2, 1, 6, 16, 1, ODD>(a, s) : launch_shape<YT, 2, 1, 6, 16, 2, ODD>(a, s);
+      return k16 == 1 ? launch_shape<YT, 2, 1, 2, 16, 1, ODD>(a, s) : launch_shape<YT, 2, 1, 2, 16, 2, ODD>(a, s);
     }
-    return a.M <= 32 ? launch_shape<YT, 2, 2, 2, 16, 2>(a, s) : launch_shape<YT, 2, 4, 2, 8, 2>(a, s);
+    if (a.M > 32) return launch_shape<YT, 2, 4, 2, 8, 2, ODD>(a, s);
+    return k16 == 1 ? launch_shape<YT, 2, 2, 2, 16, 1, ODD>(a, s) : launch_shape<YT, 2, 2, 2, 16, 2, ODD>(a, s);
   }
-  // all of a wave's steps in flight at once, where there are up to four (4096 x 11008:
-  // 10.7 us with four at a time, 9.8 with two)
-  if (a.M <= 16)
-    return a.K <= 4096 ? launch_shape<YT, 1, 1, 1, 16, 4>(a, s) : launch_shape<YT, 1, 1, 1, 16, 2>(a, s);
-  return a.M <= 32 ? launch_shape<YT, 1, 2, 1, 16, 4>(a, s) : launch_shape<YT, 1, 4, 1, 16, 2>(a, s);
+  if (a.M <= 16) {
+    if (k16 == 1) return launch_shape<YT, 1, 1, 1, 16, 1, ODD>(a, s);
+    if (k16 == 2 || k16 > 4) return launch_shape<YT, 1, 1, 1, 16, 2, ODD>(a, s);
+    return launch_shape<YT, 1, 1, 1, 16, 4, ODD>(a, s);
+  }
+  if (a.M <= 32) {
+    if (k16 == 1) return launch_shape<YT, 1, 2, 1, 16, 1, ODD>(a, s);
+    return k16 == 2 ? launch_shape<YT, 1, 2, 1, 16, 2, ODD>(a, s) : launch_shape<YT, 1, 2, 1, 16, 4, ODD>(a, s);
+  }
+  return k16 == 1 ? launch_shape<YT, 1, 4, 1, 16, 1, ODD>(a, s) : launch_shape<YT, 1, 4, 1, 16, 2, ODD>(a, s);
+}
+
+template <class YT>
+hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
+  return a.odd ? launch_rows_of<YT, true>(a, s) : launch_rows_of<YT, false>(a, s);
 }
 
 // Which kernel, by an estimate of the time in us.  The tiles: a start, and for each 64-byte
 // step the larger of its latency (which grows as the tiles fill the card) times the
 // rounds of workgroups, and of all tiles' loads at the 10.7 TB/s at which they come from the
 // L2s.  The row kernel, which reads all rows of x for each 16 channels: a start and, for each
-// round of 256 workgroups, the rows of x and the weights' at 28 KB a us.  The numbers are fitted to the
-// measured times of all six kernels at 540 sizes (17 to 2048 rows, K 512 to 11008, N 256 to 28000, one
-// and two matrices): what it takes is 1 % slower than the fastest on average, 23 % at most.  Some
-// of them, K 4096 and one matrix (us; rows, four waves that share K, one, 128 x 128, 256 x 128, 256 x 256):
+// round of 256 workgroups, the rows of x and the weights' at 26 KB a us.  Where rows have no 16-byte
+// alignment it reads them as they are, at odd addresses at about a third of the rate (1 x
+// 4089 x 4096 7.9 us, 1 x 4096 x 4096 4.5), and the tiles pay for the copies of x and the weights.  The
+// numbers are fitted to the measured times of all six kernels at 1500 sizes (1 to 2048 rows, K 256 to 11008,
+// N 256 to 28000, one and two matrices): what it takes is 1 % slower than the fastest on average and
+// 36 % at most, 81 % where copies are counted.  Some of them, K 4096 and one matrix (us; rows, four waves that share K, one, 128 x 128, 256 x 128, 256 x 256):
 // 17 x 4096 6.5, 7.5, 18, 17, 26, 38; 64 x 4096 11.8, 8.2, 18, 19, 28, 41; 128 x 11008 -, 23, 20,
 // 22, 29, 42; 512 x 4096 -, 23, 20, 20, 27, 40; 512 x 11008 -, 61, 49, 37, 33, 42; 1000 x 11008 -,
 // 119, 104, 65, 62, 52.
@@ -177,20 +213,24 @@ constexpr Guess kGuess[] = {{2.4, 0.094, 1.31, 1, 64, 64},     // in the order o
                             {4.1, 0.560, 0.37, 1, 256, 256}};
 // Sets the tile, -1 for the row kernel.
 void choose(ScaledArgs& a) {
-  // (a tile's offsets are 32-bit; up to 16 rows the row kernel is the faster everywhere)
+  // (a tile's offsets are 32-bit)
   a.tile = -1;
-  if (a.M <= 16 || a.K > (int64_t)1 << 23) return;
+  if (a.K > (int64_t)1 << 23) return;
   const double m = (double)a.M, k = (double)a.K, steps = std::ceil(k / 64);
   const double rows = std::ceil((double)a.N / 32) * 32 * a.mats;
-  double least = 1.8 + std::ceil((double)a.N / 16 / 256) * (m + 16 * a.mats) * k / 28100.0;
+  const int64_t own = channels_of(a);
+  const bool bytes = a.odd && (a.K % 2 != 0 || ((uintptr_t)a.x | (uintptr_t)a.w[0] | (uintptr_t)a.w[a.mats - 1]) % 2 != 0);
+  const double slab = (m + (double)(own * a.mats)) * k / 25900.0;
+  double least = 1.2 + (double)((a.N + 256 * own - 1) / (256 * own)) * (0.1 + (bytes ? 1.5 + 2.8 * slab : slab));
   if (a.M > 64) least = INFINITY;
+  const double copies = a.odd ? 11.7 + 0.93 * k / 1000 + 2.0 * a.mats * (double)a.N * k / 4.2e6 : 0.0;
   for (int i = 0; i < 5; ++i) {
     const Guess& g = kGuess[i];
     const double tiles = std::ceil(m / g.bm) * std::ceil(rows / g.tn);
     const double rounds = std::ceil(tiles / (256.0 * g.at_once)), fill = tiles < 256.0 ? tiles / 256.0 : 1.0;
     const double latency = g.step * rounds * (1.0 + g.fill * fill * fill);
     const double loads = tiles * (g.tn + g.bm) * 64 / 10.7e6;
-    const double t = g.start + steps * (latency > loads ? latency : loads);
+    const double t = copies + g.start + steps * (latency > loads ? latency : loads);
     if (t < least) {
       a.tile = i;
       least = t;
@@ -203,7 +243,7 @@ void choose(ScaledArgs& a) {
   const int64_t whole = ma * n / 256, cols = whole * 256 / ma;
   if (whole == 0 || cols == n || (n - cols) * mb > 256 || ma * cols > 1 << 20) return;
   const Guess &g = kGuess[kTile256], &h = kGuess[kTile256x128];
-  const double t = g.start + steps * (g.step * (1.0 + g.fill) * (double)whole + h.step * (1.0 + h.fill));
+  const double t = copies + g.start + steps * (g.step * (1.0 + g.fill) * (double)whole + h.step * (1.0 + h.fill));
   if (t < least) {
     a.tile = kTile256;
     a.columns = cols;
@@ -216,7 +256,9 @@ hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
   const int64_t M = a.M, N = a.N, K = a.K, kp = (K + 15) / 16 * 16;
   uintptr_t ptrs = (uintptr_t)a.x | (uintptr_t)a.w[0];
   if (a.mats == 2) ptrs |= (uintptr_t)a.w[1];
-  const bool pad = K % 16 != 0 || ptrs % 16 != 0;
+  a.odd = K % 16 != 0 || ptrs % 16 != 0;
+  choose(a);
+  const bool rows = a.tile < 0, pad = a.odd && (!rows || K < 16);
   void* ws = nullptr;
   hipError_t e = hipSuccess;
   if (pad) {
@@ -232,10 +274,9 @@ hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
       to += N * kp;
     }
     a.K = kp;
+    a.odd = false;
   }
   if (e == hipSuccess) {
-    choose(a);
-    const bool rows = a.tile < 0;
     if (a.y_type == Q8TA_F32) e = rows ? launch_rows<float>(a, s) : launch_tiles_f32(a, s);
     else if (a.y_type == Q8TA_F16) e = rows ? launch_rows<Half>(a, s) : launch_tiles_f16(a, s);
     else e = rows ? launch_rows<Bfloat>(a, s) : launch_tiles_bf16(a, s);

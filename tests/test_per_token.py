@@ -279,6 +279,16 @@ def test_products_odd_sizes_and_alignment(M, K, N, offset):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("offset", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("M,K,N", [(1, 15, 17), (1, 16, 40), (2, 17, 33), (5, 31, 20), (16, 63, 50), (1, 65, 800), (3, 1023, 17),
+                                   (16, 1025, 40), (30, 1040, 33), (31, 2047, 18), (60, 2049, 20), (64, 95, 300), (4, 4095, 30),
+                                   (2, 4097, 65), (9, 7001, 12400), (17, 5003, 16)])
+def test_products_of_rows_as_they_lie(M, K, N, offset):
+    check_linear(product_case(M, K, N, seed=K, offset=offset), "fp32")
+    check_gated(product_case(M, K, N, seed=K + 1, offset=offset, mats=2), "fp16", "silu")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N", [(3, 40), (100, 200), (600, 4500)])
 def test_products_outputs_at_odd_addresses(M, N):
     c = product_case(M, 128, N, seed=5)
