@@ -214,7 +214,7 @@ struct ScaledArgs {
   bool odd = false;           // K is no multiple of 16, or x or a weight not 16-byte aligned
   int64_t columns = 0;        // kTile256: of whole tiles; what is left takes 256 x 128 ones
 };
-enum { kTile64Split, kTile64, kTile128, kTile256x128, kTile256 };
+enum { kTile64Split, kTile64, kTile128, kTile256x128, kTile256, kTile32Split };
 hipError_t launch_scaled(ScaledArgs a, hipStream_t s);
 // The GEMM for K a multiple of 16 up to 2^23 and 16-byte aligned x and w, by the type of y.
 hipError_t launch_tiles_f32(const ScaledArgs& a, hipStream_t s);

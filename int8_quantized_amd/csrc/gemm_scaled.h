@@ -55,17 +55,17 @@ constexpr int wait_vm_lgkm0(int vm) { return (vm & 15) | ((vm >> 4) << 14) | (7 
 
 __device__ int8_t g_zeros[64] __attribute__((aligned(64)));   // never written
 
-// WAVES_N x WAVES_M waves of FN x 2 fragments of 32 x 32.
-template <int WAVES_N_, int WAVES_M_, int FN_>
+// WAVES_N x WAVES_M waves of FN x FM fragments of 32 x 32.
+template <int WAVES_N_, int WAVES_M_, int FN_, int FM_ = 2>
 struct Tile {
-  static constexpr int WAVES_N = WAVES_N_, WAVES_M = WAVES_M_, FN = FN_, FM = 2;
+  static constexpr int WAVES_N = WAVES_N_, WAVES_M = WAVES_M_, FN = FN_, FM = FM_;
   static constexpr int WAVES = WAVES_N * WAVES_M, NT = 64 * WAVES;
   static constexpr int TN = 32 * FN * WAVES_N, BM = 32 * FM * WAVES_M, BK = 64;
   static constexpr int NBW = TN / 16, NBX = BM / 16;            // 16-row blocks of one step
   static constexpr int NQ = (NBW + NBX + WAVES - 1) / WAVES;    // load instructions per wave and step
   // bytes per stage: the blocks at 1 KiB each (W first, then X), then the landing
-  // place of the padding loads that even out the waves' counts
-  static constexpr int STAGE = WAVES * NQ * 1024;
+  // place of the padding loads that even out the waves' counts; a fragment row's sums fit too
+  static constexpr int STAGE = WAVES * NQ * 1024 > 128 * TN || WAVES > 1 ? WAVES * NQ * 1024 : 128 * TN;
 };
 
 __device__ __forceinline__ int swz4(int r, int c) { return c ^ ((r >> 2) & 3); }
@@ -143,7 +143,7 @@ __device__ __forceinline__ void scaled_tile(const ScaledArgs& a, const Smem& sm,
   constexpr int FN = T::FN, FM = T::FM, H = FN / MATS;
   constexpr int NR = FN + FM;   // fragment reads per slice
   constexpr int NP = FN * FM;   // products per slice
-  static_assert(NP >= NR, "a read behind each product");
+  constexpr int kReads = (NR + NP - 1) / NP;   // behind each product
   static_assert(SPLIT == 1 || T::WAVES == 1, "a split tile is one wave's");
   const int tid = threadIdx.x, lane = tid & 63;
   const int split = SPLIT > 1 ? __builtin_amdgcn_readfirstlane(tid >> 6) : 0;
@@ -241,7 +241,8 @@ __device__ __forceinline__ void scaled_tile(const ScaledArgs& a, const Smem& sm,
     Static<0, NP>::each([&](auto MI) {
       constexpr int m = decltype(MI)::value;
       product(af[0], bf[0], std::integral_constant<int, m / FM>{}, std::integral_constant<int, m % FM>{});
-      if constexpr (m < NR) read_frag(S, af[1], bf[1], K1, MI);
+      Static<m * kReads, (m * kReads + kReads < NR ? m * kReads + kReads : NR)>::each(
+          [&](auto R) { read_frag(S, af[1], bf[1], K1, R); });
       __builtin_amdgcn_sched_barrier(0);
     });
     __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(T::NQ));
@@ -252,7 +253,8 @@ __device__ __forceinline__ void scaled_tile(const ScaledArgs& a, const Smem& sm,
     Static<0, NP>::each([&](auto MI) {
       constexpr int m = decltype(MI)::value;
       product(af[1], bf[1], std::integral_constant<int, m / FM>{}, std::integral_constant<int, m % FM>{});
-      if constexpr (m < NR) read_frag(SN, af[0], bf[0], K0, MI);
+      Static<m * kReads, (m * kReads + kReads < NR ? m * kReads + kReads : NR)>::each(
+          [&](auto R) { read_frag(SN, af[0], bf[0], K0, R); });
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -406,6 +408,8 @@ using T256 = Tile<2, 4, 4>;   // 256 weight rows x 256 rows, waves of 128 x 64
 using T128 = Tile<4, 2, 2>;   // 256 x 128, waves of 64 x 64
 using T64 = Tile<2, 2, 2>;    // 128 x 128, four waves
 using T32 = Tile<1, 1, 2>;    // 64 x 64, one wave, or four that share K
+template <int MATS>
+using T16 = Tile<1, 1, MATS, 1>;   // 32 channels x 32, eight waves (two matrices: six) that share K
 
 // A launch has fewer than 2^32 threads: columns go in as many as it takes.
 constexpr int64_t kMostTiles = (int64_t)1 << 21;
@@ -429,6 +433,7 @@ template <int MATS, class YT>
 hipError_t launch_plan(const ScaledArgs& a, hipStream_t s) {
   switch (a.tile) {
     case kTile64Split: return launch_one<T32, MATS, YT, 4>(a, s);
+    case kTile32Split: return launch_one<T16<MATS>, MATS, YT, MATS == 2 ? 6 : 8>(a, s);
     case kTile64: return launch_one<T32, MATS, YT>(a, s);
     case kTile128: return launch_one<T64, MATS, YT>(a, s);
     case kTile256x128: return launch_one<T128, MATS, YT>(a, s);

@@ -201,21 +201,27 @@ hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
 // round of 256 workgroups, the rows of x and the weights' at 26 KB a us.  Where rows have no 16-byte
 // alignment it reads them as they are, at odd addresses at about a third of the rate (1 x
 // 4089 x 4096 7.9 us, 1 x 4096 x 4096 4.5), and the tiles pay for the copies of x and the weights.  The
-// numbers are fitted to the measured times of all six kernels at 1500 sizes (1 to 2048 rows, K 256 to 11008,
+// numbers are fitted to the measured times of all seven kernels at 1700 sizes (1 to 2048 rows, K 64 to 11008,
 // N 256 to 28000, one and two matrices): what it takes is 1 % slower than the fastest on average and
-// 36 % at most, 81 % where copies are counted.  Some of them, K 4096 and one matrix (us; rows, four waves that share K, one, 128 x 128, 256 x 128, 256 x 256):
-// 17 x 4096 6.5, 7.5, 18, 17, 26, 38; 64 x 4096 11.8, 8.2, 18, 19, 28, 41; 128 x 11008 -, 23, 20,
-// 22, 29, 42; 512 x 4096 -, 23, 20, 20, 27, 40; 512 x 11008 -, 61, 49, 37, 33, 42; 1000 x 11008 -,
-// 119, 104, 65, 62, 52.
+// 34 % at most.  Some of them, one matrix (us; the row kernel, 32 x 32 by eight waves, 64 x 64 by four, by
+// one, 128 x 128, 256 x 128, 256 x 256; rows x K x N):
+//   16 x 4096 x 4096     5.8  5.1  7.3  18   17   26   38
+//   64 x 4096 x 4096    11.8  7.1  8.2  18   19   28   41
+//   64 x 11008 x 4096   28    17   27   40   47   66   96
+//   128 x 4096 x 11008    -    -   23   20   22   29   42
+//   512 x 4096 x 4096     -   44   23   20   20   27   40
+//   512 x 4096 x 11008    -    -   61   49   37   33   42
+//   1000 x 4096 x 11008   -    -  119  104   65   62   52
 struct Guess {
   double start, step, fill;
   int at_once, tn, bm;   // workgroups of a CU, the tile
 };
-constexpr Guess kGuess[] = {{2.4, 0.094, 1.31, 1, 64, 64},     // in the order of kTile*
-                            {1.6, 0.201, 0.66, 6, 64, 64},
-                            {3.0, 0.390, 0.0, 3, 128, 128},
-                            {3.0, 0.387, 0.08, 1, 256, 128},
-                            {4.1, 0.560, 0.37, 1, 256, 256}};
+constexpr Guess kGuess[] = {{2.4, 0.0964, 1.1, 1, 64, 64},     // in the order of kTile*
+                            {1.9, 0.205, 0.86, 6, 64, 64},
+                            {3.0, 0.386, 0.0, 3, 128, 128},
+                            {3.0, 0.387, 0.06, 1, 256, 128},
+                            {4.1, 0.569, 0.35, 1, 256, 256},
+                            {2.4, 0.0323, 1.76, 1, 32, 32}};   // (for each matrix)
 // Sets the tile, -1 for the row kernel.
 void choose(ScaledArgs& a) {
   // (a tile's offsets are 32-bit)
@@ -225,12 +231,16 @@ void choose(ScaledArgs& a) {
   const double rows = std::ceil((double)a.N / 32) * 32 * a.mats;
   const int64_t own = channels_of(a);
   const bool bytes = a.odd && (a.K % 2 != 0 || ((uintptr_t)a.x | (uintptr_t)a.w[0] | (uintptr_t)a.w[a.mats - 1]) % 2 != 0);
-  const double slab = (m + (double)(own * a.mats)) * k / 25900.0;
-  double least = 1.2 + (double)((a.N + 256 * own - 1) / (256 * own)) * (0.1 + (bytes ? 1.5 + 2.8 * slab : slab));
+  const double slab = (m + (double)(own * a.mats)) * k / 26500.0;
+  double least = 1.5 + (double)((a.N + 256 * own - 1) / (256 * own)) * (bytes ? 1.5 + 2.8 * slab : slab);
   if (a.M > 64) least = INFINITY;
   const double copies = a.odd ? 11.7 + 0.93 * k / 1000 + 2.0 * a.mats * (double)a.N * k / 4.2e6 : 0.0;
-  for (int i = 0; i < 5; ++i) {
-    const Guess& g = kGuess[i];
+  for (int i = 0; i < 6; ++i) {
+    Guess g = kGuess[i];
+    if (i == kTile32Split) {
+      g.step *= a.mats;
+      g.tn *= a.mats;
+    }
     const double tiles = std::ceil(m / g.bm) * std::ceil(rows / g.tn);
     const double rounds = std::ceil(tiles / (256.0 * g.at_once)), fill = tiles < 256.0 ? tiles / 256.0 : 1.0;
     const double latency = g.step * rounds * (1.0 + g.fill * fill * fill);
