@@ -174,11 +174,6 @@ hipError_t launch_linear_lora(LoraArgs a, hipStream_t s);
 hipError_t launch_gemm_w8_lora(const LoraArgs& a, hipStream_t s);
 hipError_t launch_gemm_mx_lora(const LoraArgs& a, hipStream_t s);
 
-// Rows of `bytes` bytes at any address into rows of `padded` bytes (a multiple of
-// 16), zero past the row (lora.hip).
-hipError_t pad_rows(const void* src, int64_t rows, int64_t bytes, int64_t padded, int8_t* dst,
-                    hipStream_t s);
-
 struct NormArgs {
   const void* x;              // [tokens, n], row stride in elements
   const void* residual;       // or NULL

@@ -359,8 +359,6 @@ __global__ __launch_bounds__(256) void k_pad_rows(const int8_t* __restrict__ src
 // error); what takes more goes in launches of up to this many.
 constexpr int64_t kMostThreads = (int64_t)1 << 31;
 
-}  // namespace
-
 hipError_t pad_rows(const void* src, int64_t rows, int64_t bytes, int64_t padded, int8_t* dst,
                     hipStream_t s) {
   const int64_t most = kMostThreads / (padded / 16);   // (a row of 2^31 bytes is 2^27 chunks)
@@ -373,8 +371,6 @@ hipError_t pad_rows(const void* src, int64_t rows, int64_t bytes, int64_t padded
   }
   return hipSuccess;
 }
-
-namespace {
 
 template <class AT, class YT, int MT, int FN, int WAVES, int D>
 hipError_t launch_shape(LoraArgs a, hipStream_t s) {

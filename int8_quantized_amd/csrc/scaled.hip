@@ -198,13 +198,14 @@ hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
 // step the larger of its latency (which grows as the tiles fill the card) times the
 // rounds of workgroups, and of all tiles' loads at the 10.7 TB/s at which they come from the
 // L2s.  The row kernel, which reads all rows of x for each 16 channels: a start and, for each
-// round of 256 workgroups, the rows of x and the weights' at 26 KB a us.  Where rows have no 16-byte
-// alignment it reads them as they are, at odd addresses at about a third of the rate (1 x
-// 4089 x 4096 7.9 us, 1 x 4096 x 4096 4.5), and the tiles pay for the copies of x and the weights.  The
-// numbers are fitted to the measured times of all seven kernels at 1700 sizes (1 to 2048 rows, K 64 to 11008,
-// N 256 to 28000, one and two matrices): what it takes is 1 % slower than the fastest on average and
-// 34 % at most.  Some of them, one matrix (us; the row kernel, 32 x 32 by eight waves, 64 x 64 by four, by
-// one, 128 x 128, 256 x 128, 256 x 256; rows x K x N):
+// round of 256 workgroups, the rows of x and the weights' at 26 KB a us.  Where rows have no
+// 16-byte alignment it reads them as they are, at odd addresses at about a third of the
+// rate (1 x 4089 x 4096 7.9 us, 1 x 4096 x 4096 4.5), and the tiles pay for the copies of x and
+// the weights.  The numbers are fitted to the measured times of all seven kernels at 1700
+// sizes (1 to 2048 rows, K 64 to 11008, N 256 to 28000, one and two matrices): what it takes is
+// 1 % slower than the fastest on average and 34 % at most (with copies 2 and 62 %).  Some of
+// them, one matrix (us; the row kernel, 32 x 32 by eight waves, 64 x 64 by four, by one,
+// 128 x 128, 256 x 128, 256 x 256; rows x K x N):
 //   16 x 4096 x 4096     5.8  5.1  7.3  18   17   26   38
 //   64 x 4096 x 4096    11.8  7.1  8.2  18   19   28   41
 //   64 x 11008 x 4096   28    17   27   40   47   66   96
@@ -234,7 +235,7 @@ void choose(ScaledArgs& a) {
   const double slab = (m + (double)(own * a.mats)) * k / 26500.0;
   double least = 1.5 + (double)((a.N + 256 * own - 1) / (256 * own)) * (bytes ? 1.5 + 2.8 * slab : slab);
   if (a.M > 64) least = INFINITY;
-  const double copies = a.odd ? 11.7 + 0.93 * k / 1000 + 2.0 * a.mats * (double)a.N * k / 4.2e6 : 0.0;
+  const double copies = a.odd ? 7.0 + 0.7 * k / 1000 + 2.0 * a.mats * (double)a.N * k / 3.5e6 : 0.0;
   for (int i = 0; i < 6; ++i) {
     Guess g = kGuess[i];
     if (i == kTile32Split) {
@@ -265,6 +266,40 @@ void choose(ScaledArgs& a) {
   }
 }
 
+// The rows of x and of the weights, K bytes each, one after the other in rows of kp, which end
+// in zeros: a wave a row.
+__global__ __launch_bounds__(256) void k_copy_rows(ScaledArgs a, int64_t kp, int8_t* to) {
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = a.M + a.mats * a.N, K = a.K;
+  for (int64_t r = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); r < rows;
+       r += (int64_t)gridDim.x * 4) {
+    const int8_t* src = r < a.M ? a.x + r * K : (r < a.M + a.N ? a.w[0] + (r - a.M) * K : a.w[1] + (r - a.M - a.N) * K);
+    int8_t* dst = to + r * kp;
+    int64_t k = 16 * lane;
+    for (; k + 1024 * (kAhead - 1) + 16 <= K; k += 1024 * kAhead) {
+      v4i v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) v[u] = *reinterpret_cast<const v4i_any*>(src + k + 1024 * u);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) *reinterpret_cast<v4i*>(dst + k + 1024 * u) = v[u];
+    }
+    for (; k + 16 <= K; k += 1024) *reinterpret_cast<v4i*>(dst + k) = *reinterpret_cast<const v4i_any*>(src + k);
+    if (k < K) {
+      uint32_t v[4] = {};
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (k + i < K) v[i / 4] |= (uint32_t)(uint8_t)src[k + i] << (8 * (i % 4));
+      *reinterpret_cast<v4i*>(dst + k) = v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+    }
+  }
+}
+hipError_t launch_copies(const ScaledArgs& a, int64_t kp, int8_t* to, hipStream_t s) {
+  const int64_t blocks = (a.M + a.mats * a.N + 3) / 4, most = (int64_t)1 << 20;
+  hipLaunchKernelGGL(k_copy_rows, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s, a, kp, to);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
@@ -280,14 +315,10 @@ hipError_t launch_scaled(ScaledArgs a, hipStream_t s) {
     e = workspace_acquire(&ws, (size_t)(M + a.mats * N) * kp, s);
     if (e != hipSuccess) return e;
     int8_t* to = (int8_t*)ws;
-    e = pad_rows(a.x, M, K, kp, to, s);
+    e = launch_copies(a, kp, to, s);
     a.x = to;
     to += M * kp;
-    for (int q = 0; q < a.mats && e == hipSuccess; ++q) {
-      e = pad_rows(a.w[q], N, K, kp, to, s);
-      a.w[q] = to;
-      to += N * kp;
-    }
+    for (int q = 0; q < a.mats; ++q, to += N * kp) a.w[q] = to;
     a.K = kp;
     a.odd = false;
   }
