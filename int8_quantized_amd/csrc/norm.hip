@@ -17,12 +17,13 @@
 // once, and the two or three sums over the row meet in LDS.  Rows too long for
 // that are read again for each sum (k_norm_long).
 //
-// Measured: 8191 x 5120 bf16 with both norms, residual and gate 87 us, 294 MB at
-// 3.4 TB/s (a copy of the same bytes 57): the vector instructions, 47 for an element, are
-// busy six tenths of the time and the rows' barriers keep them and the loads from
+// Measured: 8191 x 5120 bf16 with both norms, residual and gate 81 us, 294 MB at
+// 3.6 TB/s (a copy of the same bytes 57); 4096 x 6144 36 us, 4.9; 4096 x 4096 28 us, 4.1;
+// without the norm of x 4.6, 5.9 and 5.3.  The vector instructions, 47 for an element, are
+// busy over half of the time and the rows' barriers keep them and the loads from
 // overlapping whole.  One row of 4096: 2.8 us, a chain of latencies.  Workgroups that
-// take row after row and load the next one early, and 32-bit estimates of the codes,
-// both took 108 when this form took 108 too.
+// take row after row and load the next one early (their registers spill, 188 us), and
+// 32-bit estimates of the codes, were no faster.
 #include "decode.h"
 
 namespace q8ta {
@@ -187,7 +188,7 @@ __device__ __forceinline__ float sum_of(double b, bool has_gate, float gate, boo
 
 // C: groups of 8 elements a thread.
 template <class T, int C, bool VEC>
-__global__ __launch_bounds__(kMaxThreads, C == 1 ? 8 : 4) void k_norm(NormArgs a, double inv_n) {
+__global__ __launch_bounds__(C > 2 ? 256 : kMaxThreads, C == 1 ? 8 : (C == 4 ? 3 : 4)) void k_norm(NormArgs a, double inv_n) {
   __shared__ double sh[3][kMaxThreads / 64];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int64_t t = blockIdx.x;
@@ -376,10 +377,21 @@ hipError_t launch_type(const NormArgs& a, hipStream_t s) {
   const bool vec = a.n % 8 == 0 && strides % 8 == 0 && ptrs % 16 == 0 && (uintptr_t)a.codes % 8 == 0;
   const int64_t groups = (a.n + 7) / 8;
   auto threads = [&](int c) { return (int)((groups + 64 * c - 1) / (64 * c)) * 64; };
-  // 16 elements a thread where there are many rows (8191 x 5120: 87 us, with 8 6 % more), 8 where
-  // a row is a chain of latencies
-  if (groups <= 1024 && a.tokens < 512) launch_regs<T, 1>(a, vec, threads(1), s);
-  else if (groups <= 2048) launch_regs<T, 2>(a, vec, threads(2), s);
+  // 8 elements a thread where a row is a chain of latencies; where there are many, 16 (8 took 6 % more),
+  // and 24 or 32 of 16 bits where four waves hold a row then, one a SIMD (8191 x 5120: 89 us with 16,
+  // 82 with 24; 4096 x 6144 44 and 36; 4096 x 7168 48, with 32 42; 8192 x 8192 117 with 16 as with 32)
+  if (groups <= 1024 && a.tokens < 512) {
+    launch_regs<T, 1>(a, vec, threads(1), s);
+    return hipGetLastError();
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (groups > 512 && groups < 1024) {
+      if (groups <= 768) launch_regs<T, 3>(a, vec, threads(3), s);
+      else launch_regs<T, 4>(a, vec, threads(4), s);
+      return hipGetLastError();
+    }
+  }
+  if (groups <= 2048) launch_regs<T, 2>(a, vec, threads(2), s);
   else hipLaunchKernelGGL((k_norm_long<T>), dim3((unsigned)a.tokens), dim3(kMaxThreads), 0, s, a,
                           1.0 / (double)a.n);
   return hipGetLastError();

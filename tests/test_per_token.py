@@ -178,6 +178,15 @@ def test_quantize_per_token_zeros_and_values_that_are_not_finite(N, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("T,N", [(512, 4104), (513, 5120), (600, 5001), (515, 6144), (512, 6145), (514, 7168), (516, 8184),
+                                 (513, 8192)])
+def test_norm_quantize_of_many_long_rows(T, N, dtype):
+    check_norm(norm_case(T, N, dtype, seed=N))
+    check_norm(norm_case(T, N, dtype, post=False, gate=None, weight=False, out=False, seed=N + 1))
+
+
+@pytest.mark.gpu
 def test_norm_quantize_of_more_tokens_than_one_launch():
     check_norm(norm_case((1 << 21) + 77, 8, "fp16", seed=4))
 
