@@ -694,7 +694,8 @@ q8ta_status q8ta_sample(const void* logits, int64_t row_stride, q8ta_dtype dtype
  *   z = h * rms(h) * weight          (weight NULL: h)
  *   residual_out = h;  scales[t] = max |z| / 127, rounded to fp32;
  *   codes = rint(z * 127 / max |z|)  (all 0, with scale 0, for a row of zeros)
- * A row whose z holds a value that is not finite gets the scale NaN and codes 0.
+ * A row whose z holds a value that is not finite gets the scale NaN and codes 0.  Where x
+ * holds an infinite one, rms(x) is 0: with post_weight, b is NaN there and 0 elsewhere.
  * x, residual, gate: [tokens, N] of `dtype`, inner stride 1, any row stride
  * (gate_stride 0: one row of N for all tokens); post_weight, weight: fp32 [N];
  * residual_out: dense, of `dtype`, may be NULL, or x or residual itself where that is

@@ -164,7 +164,7 @@ __device__ __forceinline__ double reciprocal_root(double x) {
   double y = __builtin_amdgcn_rsq(x);
 #pragma unroll
   for (int i = 0; i < 2; ++i) y = __builtin_fma(__builtin_fma(-x * y, y, 1.0), 0.5 * y, y);
-  return y;
+  return x == (double)__builtin_inff() ? 0.0 : y;   // (the steps would make a NaN of it)
 }
 
 // The row's scale; 127 / max goes to inv.  A row with a value that is not finite
