@@ -217,7 +217,10 @@ __global__ __launch_bounds__(kNT) void k_verify_stats(Plan p) {
     const Heat h = make_heat(top, heat);
     const Near near = make_near(h);
     float four[4] = {};
-    if (near_log2(near, wave_top) > kLarge) {
+    if (!near_scale(h)) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum += weight(h, x[i]);
+    } else if (near_log2(near, wave_top) > kLarge) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const float y = near_log2(near, x[i]);

@@ -46,18 +46,20 @@ __device__ __forceinline__ double weight(const Heat& h, float x) {
   return (double)x == h.top ? 1.0 : (x == -INFINITY ? 0.0 : w);
 }
 
-// The same in 32 bits, for a finite top: off by 2^-23 of the weight and by up to 2^-24 of it for
-// each power of two below 1, both ways.
+// The same in 32 bits, for a finite top and a scale of near_scale: y = log2 of the weight is off by
+// 2^-23 of itself (the difference's rounding and the multiply-add's), so the weight by 0.7 * 2^-23 of
+// itself for each power of two below 1, and by 2^-23 for the exponential; the same way for equal logits.
 struct Near {
   float top, scale, rest;   // the scale in two parts of one sign, so that -inf stays
 };
+// Temperatures from 2^-99 to 2^100: both parts are normal numbers above 0, and a difference that
+// passes fp32's range is a weight of 0 (2^-2^28).
+__device__ __forceinline__ bool near_scale(const Heat& h) { return h.scale >= 0x1p-100 && h.scale <= 0x1p100; }
 __device__ __forceinline__ Near make_near(const Heat& h) {
-  // (kept finite and above 0: 2^100 and 2^-100 are as good as infinity and 0 here)
-  const double s = __builtin_fmin(__builtin_fmax(h.scale, 0x1p-100), 0x1p100);
-  float hi = (float)s;
-  if ((double)hi > s) hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, hi) - 1);
+  float hi = (float)h.scale;
+  if ((double)hi > h.scale) hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, hi) - 1);
   // (a rest of 0 would make a NaN of -inf)
-  return Near{(float)h.top, hi, __builtin_fmaxf((float)(s - (double)hi), 0x1p-126f)};
+  return Near{(float)h.top, hi, __builtin_fmaxf((float)(h.scale - (double)hi), 0x1p-126f)};
 }
 // log2 of it; the weight is 2 to that.
 __device__ __forceinline__ float near_log2(const Near& h, float x) {
