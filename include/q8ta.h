@@ -768,9 +768,11 @@ q8ta_status q8ta_gated_linear(const int8_t* x, int64_t M, int64_t K, const float
  * other.  T <= 0 (or NaN) is greedy: a child is kept if it is the target's
  * largest (the first of equal ones), and next is that.  T' = draft_temperature[b], or T
  * where draft_temperature is NULL; T' <= 0 puts all of q on its largest.
- * What a token is drawn from is 64-bit; the sums that shares are divided by take
- * small weights in 32 bits and are off by some 1e-8 of themselves.  All is added in an
- * order that depends on vocab alone.
+ * Weights that a token is drawn from are 64-bit; the sums that p and q are divided by,
+ * and that left starts from, take small weights in 32 bits: they are off by up to 2^-19 of
+ * themselves where many equal small logits make them up, by some 1e-8 where logits are
+ * spread, and left keeps that much of the whole.  All is added in an order that depends on
+ * vocab alone.
  * A NaN logit counts as -inf; +inf logits share the weight alone; where all
  * logits are -inf the walk ends, with next -1.  An id outside [0, vocab) has p and q 0.
  * u: in [0, 1); below 0 as 0; one of 1 and beyond keeps no drawn child with p <= q and

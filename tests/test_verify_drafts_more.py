@@ -1,8 +1,15 @@
-"""q8ta_verify_drafts at temperatures and logits at the ends of fp32."""
+"""q8ta_verify_drafts at temperatures and logits at the ends of fp32, how far off the sums are that shares are divided
+by, and the longest vocabulary with a drafter's logits.
+
+Tolerance of the sums.  A weight 2^-y of its chunk's largest that is formed in 32 bits has y off by 2^-23 of itself
+(a difference and a multiply-add) and its exponential by 2^-23: 2^-23 (1 + 0.7 y) in all; four are added at a time, with
+three roundings of 2^-24.  A chunk's sum takes these by the shares of its 4096 weights, of which the mean of y
+is at most log2 4096 = 12: 2^-23 (1 + 8.4 + 1.5) < 2^-19 of the sum.
+"""
 import numpy as np
 import pytest
 
-from test_verify_drafts import check, make
+from test_verify_drafts import check, definition, make, run
 
 torch = pytest.importorskip("torch")
 
@@ -36,3 +43,40 @@ def test_masks_of_the_types_lowest_value(temperature, dtype):
                 c["ids"] &= ~1
             c["temperature"][:] = temperature
             check(c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V,low,temperature", [(4096, -9.5, 1.0), (40960, -4.5, 0.8), (40960, -5.75, 1.0), (131072, -2.25, 0.8),
+                                               (131072, -7.0, 0.9), (8192, -1.5, 1.0)])
+def test_sums_of_few_distinct_logits(V, low, temperature, dtype):
+    """Equal logits' errors do not cancel: one child, whose random number goes through its share in steps of 2^-22."""
+    j = np.arange(-40, 41)
+    B = len(j)
+    c = make(B, 2, V, dtype, False, seed=1)
+    c["logits"][:] = low
+    c["logits"][:, :, ::4096] = 0.0
+    c["ids"][:, 1] = 0
+    c["temperature"][:] = temperature
+    tops = -(-V // 4096)
+    low = float(c["logits"][0, 0, 1])
+    share = 1.0 / (tops + (V - tops) * np.exp(low / float(np.float32(temperature))))
+    c["u"][:, 1] = share * (1 + j * 2.0 ** -22)
+    off = c["u"][:, 1].astype(np.float64) / share - 1
+    _, accepted, _ = run(c)
+    assert (accepted[off < -2.0 ** -19] == 2).all() and (accepted[off > 2.0 ** -19] == 1).all(), (off, accepted)
+    assert (np.diff(accepted[np.argsort(off)]) <= 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", [3, 5])
+def test_longest_vocabulary_with_a_drafter(seed):
+    """A residual over 4096 chunks, and a kept token with the one after it."""
+    c = make(1, 2, 1 << 24, "bf16", True, seed=seed, temperature=0.3)
+    want = definition(c)
+    assert want[3][0] > 1e-2 and want[1][0] == 1     # far from every border, nothing kept
+    assert all((a == b).all() for a, b in zip(run(c), want))
+    c["u"][0, 1] = 0.0
+    want = definition(c)
+    assert want[3][0] > 1e-9 and want[1][0] == 2
+    assert all((a == b).all() for a, b in zip(run(c), want))
