@@ -784,8 +784,8 @@ q8ta_status q8ta_gated_linear(const int8_t* x, int64_t M, int64_t K, const float
  * draft_temperature fp32 [batch]; u fp32 [batch, tokens]; path int32 [batch, tokens];
  * accepted, next int32 [batch].  batch == 0 is a no-op.  Requirements: batch <=
  * 65535, 1 <= tokens <= 64, 1 <= vocab <= 2^24; draft_logits and mask not both
- * (Q8TA_ERR_UNSUPPORTED).  Workspace: 16 bytes for each 4096 logits and some hundred
- * for each request, 33 MB at most.
+ * (Q8TA_ERR_UNSUPPORTED).  Workspace: 16 bytes for each 4096 logits, 8 more for each 4096 of
+ * a request's vocabulary and some hundred for each request, 33 MB at most.
  */
 q8ta_status q8ta_verify_drafts(const void* logits, int64_t batch_stride, int64_t token_stride,
                                const void* draft_logits, int64_t draft_batch_stride,

@@ -588,14 +588,16 @@ hipError_t launch_parts(const VerifyArgs& v, hipStream_t s) {
   p.v = v;
   p.chunks = (v.vocab + kChunk - 1) / kChunk;
   p.rows = v.tokens + (v.draft ? v.tokens - 1 : 0);
-  // requests of a launch: up to 2^20 workgroups and as many chunks' sums
+  // requests of a launch: up to 2^20 workgroups and 33 MB (one takes 8.4 MB at most)
   const int64_t blocks = (int64_t)p.rows * p.chunks;
+  const int64_t each = blocks * (int64_t)sizeof(Stat) + p.chunks * (int64_t)sizeof(double) + (int64_t)sizeof(Last);
   int64_t part = ((int64_t)1 << 20) / blocks;
+  part = part < 33000000 / each ? part : 33000000 / each;
   part = part < 1 ? 1 : (part < v.batch ? part : v.batch);
   const size_t stats = (size_t)part * blocks * sizeof(Stat);
   const size_t sums = (size_t)part * p.chunks * sizeof(double);
   void* ws = nullptr;
-  hipError_t e = workspace_acquire(&ws, stats + sums + (size_t)part * sizeof(Last), s);
+  hipError_t e = workspace_acquire(&ws, (size_t)(part * each), s);
   if (e != hipSuccess) return e;
   p.stats = (Stat*)ws;
   p.sums = (double*)((char*)ws + stats);

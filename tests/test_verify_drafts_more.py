@@ -9,6 +9,7 @@ is at most log2 4096 = 12: 2^-23 (1 + 8.4 + 1.5) < 2^-19 of the sum.
 import numpy as np
 import pytest
 
+import int8_quantized_amd as q8
 from test_verify_drafts import check, definition, make, run
 
 torch = pytest.importorskip("torch")
@@ -80,3 +81,22 @@ def test_longest_vocabulary_with_a_drafter(seed):
     want = definition(c)
     assert want[3][0] > 1e-9 and want[1][0] == 2
     assert all((a == b).all() for a, b in zip(run(c), want))
+
+
+@pytest.mark.gpu
+def test_more_requests_than_a_launchs_workspace_holds():
+    """One row of logits, read by every request with numbers of its own."""
+    B, V = 65535, 65536
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = (torch.randn(1, 1, V, generator=g, device="cuda") * 2).bfloat16().expand(B, 1, V)
+    ids, heat = torch.zeros(B, 1, dtype=torch.int32, device="cuda"), torch.rand(B, generator=g, device="cuda") + 0.5
+    u = torch.rand(B, 1, generator=g, device="cuda")
+
+    def run_rows(a, b):
+        outs = [torch.full(s, -7, dtype=torch.int32, device="cuda") for s in ((b - a, 1), (b - a,), (b - a,))]
+        q8.q8ta_verify_drafts(x[a:b], None, ids[a:b], None, None, heat[a:b], None, u[a:b], *outs)
+        return outs
+    whole, parts = run_rows(0, B), [run_rows(a, min(a + 9999, B)) for a in range(0, B, 9999)]
+    for i, o in enumerate(whole):
+        assert torch.equal(o, torch.cat([p[i] for p in parts]))
+    assert (whole[1] == 1).all() and ((whole[2] >= 0) & (whole[2] < V)).all() and whole[2].unique().numel() > 1000
