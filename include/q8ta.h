@@ -731,7 +731,8 @@ q8ta_status q8ta_quantize_per_token(const void* x, int64_t x_stride, q8ta_dtype 
  *
  * q8ta_gated_linear: two such products and the gate between them in one launch:
  *   out[m, n] = act(y_gate[m, n]) * y_up[m, n], rounded once to out_dtype,
- * both in 32 bits; activation "silu", "gelu" (by erf), "gelu_tanh" or "relu".
+ * both in 32 bits; activation "silu", "gelu" (by erf), "gelu_tanh" or "relu" (act of
+ * "silu" and "gelu_tanh" below 2^-118 in magnitude may be 0).
  * gate_weight and up_weight: int8 [N, K] each, with scales [N] and biases [N] (or NULL)
  * of their own; the rest as above (workspace, where needed: (M + 2 * N) * K).
  */

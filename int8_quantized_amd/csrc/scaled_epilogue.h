@@ -21,7 +21,9 @@ __device__ __forceinline__ float logistic(float x) {
 template <int ACT>
 __device__ __forceinline__ float activate(float v) {
   if constexpr (ACT == kActRelu) return v < 0.0f ? 0.0f : v;
-  // (e^-v passes the range of fp32: below -88 the value is under 2^-118)
+  // (e^-v passes the range of fp32: below -88 the value is under 2^-118 and taken as -0, here and in the tanh
+  // form; both sides of the fraction times 2^-64 there, for fp32's range: five more instructions, 2048 x 4096 x
+  // 11008 183 -> 189 us)
   if constexpr (ACT == kActSilu) return v < -88.0f ? -0.0f : v * logistic(v);
   // (the complement keeps the small outputs' bits)
   if constexpr (ACT == kActGelu) return 0.5f * v * erfcf(v * -0.707106781f);

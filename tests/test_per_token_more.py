@@ -1,12 +1,17 @@
-"""q8ta_norm_quantize of rows whose mean square is infinite, or next to it.
+"""q8ta_norm_quantize of rows whose mean square is infinite, or next to it, and the gated block's activations down to
+the smallest that are promised.
 
-Tolerance.  What is left of a row with an infinite mean square is residual_scale * residual: half a step of the type
-after one rounding to fp32.
+Tolerances.  What is left of a row with an infinite mean square is residual_scale * residual: half a step of the type
+after one rounding to fp32.  A gate's activation is off by 2^-21 of itself (as in test_per_token.py), or is 0 where
+it is below 2^-118; the argument z of the tanh form's logistic has up to six roundings, each of 2^-24 of z,
+and e^z changes by that much of itself.
 """
 import math
 
+import numpy as np
 import pytest
 
+import int8_quantized_amd as q8
 from test_per_token import EPS, TYPES, U32, half_step, norm_case, run_norm, smallest
 
 torch = pytest.importorskip("torch")
@@ -52,3 +57,25 @@ def test_large_values_are_not_infinite(N):
         out, codes, scales = run_norm(c)
         assert ((out.double() - b).abs() <= b.abs() * (half_step(TYPES[dtype]) + U32) * 1.001 + smallest(TYPES[dtype])).all()
         assert torch.isfinite(scales).all() and (codes.abs().amax(1) == 127).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [2, 100, 900])
+@pytest.mark.parametrize("up", [1.0, 2.0 ** 100])
+def test_gates_whose_activation_is_small(act, M, up):
+    """A gate's bias alone: activations down to 2^-118, and that or less from there on."""
+    N, K = 4096, 64
+    g = torch.linspace(-140.0, -60.0, N) if act == "silu" else torch.linspace(-12.5, -8.0, N)
+    x, w = torch.zeros(M, K, dtype=torch.int8, device="cuda"), torch.zeros(N, K, dtype=torch.int8, device="cuda")
+    one, out = torch.ones(max(M, N), device="cuda"), torch.full((M, N), 9.0, device="cuda")
+    q8.q8ta_gated_linear(x, one[:M], w, one[:N], g.cuda(), w, one[:N], torch.full((N,), up, device="cuda"), act, out)
+    v = g.double().numpy()
+    z = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    a = v * np.exp(z) / (1 + np.exp(z))
+    tol = np.abs(a) * (2.0 ** -21 + (6 * np.abs(z) * 2.0 ** -24 if act == "gelu_tanh" else 0.0))
+    tol = np.where(np.abs(a) < 2.0 ** -118, np.abs(a), tol)
+    want, tol = a * up, 1.01 * tol * up + U32 * np.abs(a * up) + 2.0 ** -150
+    got = out.cpu().double().numpy()
+    assert (np.abs(got - want) <= tol).all(), np.abs(got - want).max()
+    assert (a < 0).all() and ((got <= 0).all())
