@@ -723,7 +723,8 @@ q8ta_status q8ta_quantize_per_token(const void* x, int64_t x_stride, q8ta_dtype 
  *   y = ((float)acc * x_scales[m]) * weight_scales[n] + bias[n]
  *   out[m, n] = y, or max(y, 0) for "relu", rounded once to out_dtype.
  * x: int8 [M, K], weight: int8 [N, K], x_scales fp32 [M], weight_scales fp32 [N],
- * bias fp32 [N] or NULL; out: dense [M, N].  Requirements: M <= 2^21, N and K <=
+ * bias fp32 [N] or NULL; out: dense [M, N].  Requirements: M, N and K >= 1 (an empty
+ * step leaves the call out, as with every linear here), M <= 2^21, N and K <=
  * 2^30, the elements of each tensor <= 2^40.  Any K and alignment: where K is no
  * multiple of 16 or x or a weight is not 16-byte aligned, for more than some rows, or K
  * below 16, they are first copied into rows that are (workspace: (M + N) * K bytes, K
