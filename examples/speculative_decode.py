@@ -186,12 +186,12 @@ def main():
     known = model.prompt(rows, torch.randint(0, model.vocab, (2, 21), generator=g, device="cuda"))
     # two samples of each prompt
     model.fork(rows.int(), (rows + 2).int())
-    rows = torch.arange(4, device="cuda")
+    rows, known = torch.arange(4, device="cuda"), known.repeat(2)
     for kind, kw in (("drawn chains", dict(drawn=True)), ("trees, greedy", dict(drawn=False, temperature=0.0))):
-        said = generate(model, rows, known.repeat(2), 4, g, **kw)
+        said = generate(model, rows, known, 4, g, **kw)
         for r, text in enumerate(said):
             print(f"{kind}, request {r}: {text}")
-        known = torch.tensor([text[-1] for text in said[:2]], device="cuda")
+        known = torch.tensor([text[-1] for text in said], device="cuda")
     model.free(rows.int())
     print("pages in use:", int((model.refs > 0).sum()))
 
