@@ -802,6 +802,15 @@ q8ta_status q8ta_verify_drafts(const void* logits, int64_t batch_stride, int64_t
  * the order of its rows and below 0 behind them; lens: int32 [requests], its rows; refs:
  * int32 [pages], how many tables hold each page.  A page is free where refs <= 0.
  * One table serves the caches of all layers.
+ * A page that several requests hold is read by all of them, and no call here looks whether
+ * it is: rows may be written only to pages that their request alone holds (refs 1), whether
+ * by q8ta_rope_append or by q8ta_cache_compact.  Requests that grow and fork keep to that, since a
+ * fork's rows go on in a page of its own.  Two things do not.  A request that
+ * q8ta_pages_release cuts back to a row inside a shared page: q8ta_pages_take leaves it
+ * that page's other rows, which the others read.  It goes on as a fork of itself: fork it into
+ * a free request, whose last page is then its own, and release it.  And a compaction of
+ * rows that lie in shared pages (a window from row 0 of a forked request): its pages have to
+ * be its own before, as q8ta_pages_take and q8ta_pages_copy make them.
  *
  * q8ta_pages_take: room for more[b] rows behind lens[b]: the entries from the first
  *   below 0 (at or behind entry lens[b] / page_size) to the last that those rows
@@ -827,7 +836,9 @@ q8ta_status q8ta_verify_drafts(const void* logits, int64_t batch_stride, int64_t
  *   < counts[b]: with q8ta_verify_drafts' path and accepted and base = the context's
  *   length, the kept tokens' rows close up behind the context.  path rises (path[b, i] >=
  *   i), n entries a request; rows with path[b, i] <= i, outside the table or on a page that
- *   is none stay.  Rows behind the kept ones are left as they are.
+ *   is none stay.  Rows behind the kept ones are left as they are.  No page that a row moves
+ *   to stands in another request's table (see above), in one call least of all: the moves
+ *   of its requests run at the same time.
  *
  * The cache's layout and slots as above, any dim, page_size and alignment (multiples of 16
  * bytes move in 16-byte chunks).  lens outside [0, table_pages * page_size] are

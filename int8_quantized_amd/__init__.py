@@ -917,7 +917,8 @@ def q8ta_pages_take(table, lens, page_size, more, refs, granted, stream=None):
     """The lowest free pages for more [R] rows behind each request's lens.
 
     table int32 [R, table_pages], lens, more and granted int32 [R], refs int32 [pages]: how many tables
-    hold each page (0: free).  granted: 1 where a request got what it asked for.  Returns table."""
+    hold each page (0: free).  granted: 1 where a request got what it asked for.  A request cut back to a row
+    inside a page that others hold has to go on as a fork of itself (q8ta_pages_release).  Returns table."""
     tp, R, width, lp, rp, pages, i32 = _table(table, lens, refs)
     _each(R, more=more, granted=granted)
     _check(lib().q8ta_pages_take(tp, R, width, page_size, lp, _ptr(more, i32, "more"), rp, pages,
@@ -944,7 +945,8 @@ def q8ta_pages_fork(table, lens, page_size, src, dst, refs, granted, copy_src, c
 def q8ta_pages_release(table, lens, page_size, rows, keep, refs, stream=None):
     """Requests rows [n] (None: all) give up their pages behind the first keep [n] rows (None: all pages).
 
-    All int32: table [R, table_pages], lens [R], refs [pages].  Returns table."""
+    All int32: table [R, table_pages], lens [R], refs [pages].  A last page in part stays, also where others
+    hold it: rows behind are theirs, and the request goes on as a fork of itself into a free one.  Returns table."""
     tp, R, width, lp, rp, pages, i32 = _table(table, lens, refs)
     n = R if rows is None else (rows.shape[0] if rows.dim() == 1 else -1)
     _each(n, rows=rows, keep=keep)
@@ -979,7 +981,8 @@ def q8ta_cache_compact(cache, cache_scales, table, base, path, counts, stream=No
     """Row base[b] + path[b, i] of request b moves to row base[b] + i, for i < counts[b].
 
     cache and cache_scales as q8ta_rope_append fills them, table int32 [B, table_pages], base and counts
-    int32 [B], path int32 [B, n], rising (q8ta_verify_drafts' path and accepted).  Returns cache."""
+    int32 [B], path int32 [B, n], rising (q8ta_verify_drafts' path and accepted).  Rows may move only to pages
+    that no other request holds.  Returns cache."""
     i32 = _torch().int32
     args = _cache(cache, cache_scales)
     ts, ps = table.shape, path.shape

@@ -5,7 +5,9 @@
 // A page is free where refs[page] <= 0.  There is no list of free pages that could
 // disagree with that: releasing is a subtraction, in any order, and the k-th page
 // that a call asks for is the k-th free one by its number, so that results do not
-// depend on the order in which anything ran.  Three launches for it: free pages are
+// depend on the order in which anything ran.  A shared page in part is given to nobody
+// (a fork's last page is its own); what a caller who cuts a request back into one, or compacts one, has
+// to see to stands in the header.  Three launches for it: free pages are
 // counted in chunks of 4096 (and what each entry asks for, beside it), the counts
 // are summed, and each chunk hands out its free pages to whom they belong.  Up to 65536
 // pages and 4096 entries one workgroup does all of it (64 forks 4.6 us, 64 requests
