@@ -19,8 +19,8 @@
 //    bytes of zeros.
 //  * Rows past M or N read the last row; their products are not stored.
 //
-// Measured: 2048 x 4096 x 11008 94 to 103 us by the card's clock (1.8 to 1.96 Pop/s), gated 180 to 187
-// (2.0), 8192^3 570 (1.93; a library's product 517): the matrix instructions, with the fragment reads and
+// Measured: 2048 x 4096 x 11008 97 to 103 us by the card's clock (1.8 to 1.9 Pop/s), gated 186 to 194
+// (1.9 to 2.0), 8192^3 506 to 570 (1.9 to 2.2; a library's product 517): the matrix instructions, with the fragment reads and
 // the loads between them, bound it.  Fewer rows: scaled.hip says which tile and why; a quarter
 // to a half of the card's rate is left where one round of workgroups has to fetch all of
 // its bytes from the L2s.  K split over workgroups, their sums joined by another launch, gained

@@ -17,11 +17,12 @@
 // once, and the two or three sums over the row meet in LDS.  Rows too long for
 // that are read again for each sum (k_norm_long).
 //
-// Measured: 8191 x 5120 bf16 with both norms, residual and gate 81 us, 294 MB at
-// 3.6 TB/s (a copy of the same bytes 57); 4096 x 6144 36 us, 4.9; 4096 x 4096 28 us, 4.1;
-// without the norm of x 4.6, 5.9 and 5.3.  The vector instructions, 47 for an element, are
+// Measured: 8191 x 5120 bf16 with both norms, residual and gate 75 to 88 us from card to card, 294 MB at
+// 3.3 to 3.9 TB/s (a copy of the same bytes 52); 4096 x 6144 40 us, 4.4; 4096 x 4096 30 us, 3.9;
+// without the norm of x 65 (4.5), 34 (5.2) and 25 (4.7).  The vector instructions, 47 for an element, are
 // busy over half of the time and the rows' barriers keep them and the loads from
-// overlapping whole.  One row of 4096: 2.8 us, a chain of latencies.  Workgroups that
+// overlapping whole.  One row of 4096: 2.8 us, a chain of latencies.  The codes alone of bf16 rows: 1, 64 and
+// 2048 of 11008 4.4, 5.7 and 26 us, of 16384 5.0, 6.6 and 36.  Workgroups that
 // take row after row and load the next one early (their registers spill, 188 us), and
 // 32-bit estimates of the codes, were no faster.
 #include "decode.h"
@@ -312,6 +313,9 @@ __global__ __launch_bounds__(C > 2 ? 256 : kMaxThreads, C == 1 ? 8 : (C == 4 ? 3
 
 // Rows of any length: the row is read again for each sum.  Every thread writes
 // only what it alone has read, last (the sum may stand in x's or the residual's place).
+// One element a lane and load, a workgroup a row whatever their number: the codes of 1, 64 and 2048
+// bf16 rows of 28672 take 21, 22 and 157 us (1.1 TB/s), of 53248 36, 38 and 284; with both norms and a
+// residual 20480 36, 38 and 328.  What bounds it: the loads' latency, a row's after the other's.
 template <class T>
 __global__ __launch_bounds__(kMaxThreads) void k_norm_long(NormArgs a, double inv_n) {
   __shared__ double sh[3][kMaxThreads / 64];

@@ -12,13 +12,16 @@
 // are summed, and each chunk hands out its free pages to whom they belong.  Up to 65536
 // pages and 4096 entries one workgroup does all of it (64 forks 4.6 us, 64 requests
 // that take pages 8.5; the three launches 12.5): latencies of a few dependent
-// loads and scans.
+// loads and scans.  Of the three, the second is one workgroup, 1.6 us for each 1024 entries (65536
+// requests that take pages 105 us, 2^20 1.6 ms; the other two 9 and 15).
 //
 // Rows move in 16-byte chunks where the cache allows it, a workgroup a stretch of
 // rows of one head, all of its loads before its stores; memory bounds it.  Measured (8
 // heads of 128): 8 windows of 6001 rows moved up, 203 MB read and written
-// in 48 us, 4.2 TB/s (a large copy reaches 5.2); 64 trees' rows 5.3 us, 64 pages'
-// parts copied 3.6, both the latency of table, path and row one after the other.
+// in 42 to 48 us, 4.2 to 4.8 TB/s (a copy of as much reaches 5.6); 64 trees' rows 5.4 us, 64 pages'
+// parts copied 3.6, both the latency of table, path and row one after the other.  Where rows move among
+// places that others leave, one workgroup takes a (head, request)'s stretches in turn: 16384 rows that lose
+// 64 behind the first four, 218 us for one request and 1.13 ms for eight (0.3 and 0.5 TB/s).
 #include "decode.h"
 
 namespace q8ta {

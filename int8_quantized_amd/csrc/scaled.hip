@@ -12,8 +12,8 @@
 // has a channel's gate and up rows in one workgroup, so that the block is one
 // launch and the two products never reach memory.
 //
-// Measured (weights that the caches of the card hold): 1 x 4096 x 4096 4.5 us, 1 x 4096 x
-// 11008 9.4, gated 1 x 4096 x 11008 15.5: the weights at 3.7, 4.8 and 5.8 TB/s; a kernel that
+// Measured (weights that the caches of the card hold): 1 x 4096 x 4096 4.8 us (the best of 200 calls 4.5), 1 x
+// 4096 x 11008 9.9 (8.6), gated 1 x 4096 x 11008 16.0 (15.3): the weights at 3.5, 4.6 and 5.6 TB/s; a kernel that
 // but reads as many bytes takes 3.6, 7.5 and 13.9.  What is left is the join of the waves'
 // sums and, with many rows, x, which every workgroup reads whole.
 #include <cmath>

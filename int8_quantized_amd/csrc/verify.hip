@@ -30,8 +30,8 @@
 // All is added in one fixed order, so that a result does not depend on what else is
 // in the batch.
 //
-// Measured: 16 trees of 24 nodes over 131072 bf16 logits, 30 + 9.6 + 7 us.  The first
-// launch reads 101 MB at 3.3 TB/s; the vector instructions bound it (18 for a logit, busy
+// Measured: 16 trees of 24 nodes over 131072 bf16 logits, 28 + 9.5 + 7 us.  The first
+// launch reads 101 MB at 3.6 TB/s; the vector instructions bound it (18 for a logit, busy
 // nine tenths of the time; all weights in 64 bits took 41 us, a loop without the
 // question for large weights, taken by waves that have none, 30 in place of 32).  A chain
 // of 5 over 32000 fp32 logits with its drafter's, 4 + 10 + 6.7 us: latencies, of which the
